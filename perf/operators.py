@@ -98,9 +98,8 @@ def draw(rng):
         return _combine(None, T, H + 8 * (H == 3072), E, k, max(1, int(T * k / E * rng.uniform(0.7, 2.0))))
     x = rng.choice(["bf16", "bf16", "fp8"])
     group = rng.choice([32, 64, 128])
-    unit = 128 if x == "fp8" else group
-    n_in = unit * max(1, round(_log(rng, 256, 7168) / unit))
-    n_in += unit * (n_in == 3072)
+    n_in = 128 * round(_log(rng, 256, 7168) / 128)
+    n_in += 128 * (n_in == 3072)
     n_out = 8 * _log(rng, 32, 512)
     n_out += 8 * (n_out == 3072)
     E = rng.choice([1, 8, 20, 64, 128])
@@ -135,14 +134,6 @@ def _random_routing(T, E, k, C, g):
     top, idx = l.topk(k, dim=1)
     slot, counts = _slots(idx, E, C)
     return idx.to(torch.int32), torch.softmax(top, 1), slot, counts
-
-
-def _pack(codes):
-    """4-bit codes [..., K] as bytes [..., K/2]: in each little-endian 32-bit word of 8 inputs, the even inputs'
-    codes take the low 16 bits and the odd inputs' the high 16."""
-    c = codes.unflatten(-1, (-1, 8))
-    return torch.stack([c[..., 0] | c[..., 2] << 4, c[..., 4] | c[..., 6] << 4, c[..., 1] | c[..., 3] << 4,
-                        c[..., 5] | c[..., 7] << 4], -1).flatten(-2)
 
 
 def _inputs(case, seed):
@@ -295,11 +286,14 @@ def _plain_combine_backward(st):
 
 
 def _unpack(q):
-    """Codes 0..15 of packed bytes, in the inputs' order."""
-    b = q.unflatten(-1, (-1, 4))
+    """Codes 0..15 of packed rows [..., K/2], in the inputs' order. A row holds blocks of 128 inputs, 64 bytes each;
+    the little-endian 32-bit word 4 t + j of a block (t, j < 4) holds its inputs 32 j + 8 t .. 32 j + 8 t + 7, the
+    even ones' codes in the low 16 bits and the odd ones' in the high 16."""
+    b = q.unflatten(-1, (-1, 4, 4, 4))                       # block, t, j, byte
     lo, hi = b & 15, b >> 4
-    return torch.stack([lo[..., 0], lo[..., 2], hi[..., 0], hi[..., 2], lo[..., 1], lo[..., 3], hi[..., 1],
-                        hi[..., 3]], -1).flatten(-2)
+    word = torch.stack([lo[..., 0], lo[..., 2], hi[..., 0], hi[..., 2], lo[..., 1], lo[..., 3], hi[..., 1],
+                        hi[..., 3]], -1)                     # block, t, j, input of the word
+    return word.transpose(-2, -3).flatten(-4)
 
 
 def _plain_expert_w4(st):
@@ -417,9 +411,9 @@ def exact(case, seed):
     for e, n in enumerate(st["counts"].clamp(max=C).tolist()):
         if n == 0:
             continue
-        words = st["w_q"][e].view(torch.int32)[..., None]                   # 8 codes each, input i at bit 2i or 2i + 14
-        at = torch.tensor([0, 16, 4, 20, 8, 24, 12, 28], dtype=torch.int32, device=DEV)
-        q = ((words >> at) & 15).flatten(-2).double() - 8
+        i = torch.arange(case["n_in"], device=DEV)                          # where input i's code stands
+        word = i // 128 * 16 + i % 32 // 8 * 4 + i % 128 // 32
+        q = (st["w_q"][e].view(torch.int32)[:, word] >> (i % 8 // 2 * 4 + i % 2 * 16).int() & 15).double() - 8
         w = q * st["w_scale"][e].double().repeat_interleave(case["group"], 1)
         x = st["x"][e, :n]
         x = x.double() if case["x"] == "bf16" else \
