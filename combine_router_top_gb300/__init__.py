@@ -25,10 +25,28 @@ MOE_ERR_TIMEOUT = -5
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_FP8_E4M3_B128 = 1
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
+MOE_LOGITS_F32 = 0
+MOE_LOGITS_BF16 = 1
+MOE_ACT_NONE = 0
+MOE_ACT_SILU_GATE = 1
+
 
 class moe_problem(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("num_tokens", "hidden", "num_experts", "top_k", "num_ranks",
                                          "capacity", "dispatch_dtype", "max_blocks", "tokens_per_src_rank")]
+
+
+class moe_gate(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("score", "num_groups", "top_groups", "group_rule", "renormalise",
+                                         "logits_type")] + [("scale", C.c_float)]
+
+
+class moe_w4(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_in", "n_out", "group", "act")]
 
 
 class moe_ubatch_bufs(C.Structure):
@@ -69,6 +87,7 @@ def lib() -> C.CDLL:
         L = C.CDLL(LIB_PATH)
         P, i = C.c_void_p, C.c_int
         pp = C.POINTER(moe_problem)
+        gp, wp = C.POINTER(moe_gate), C.POINTER(moe_w4)
         sig = {
             "moe_status_string": ([i], C.c_char_p),
             "moe_validate": ([pp], i),
@@ -87,6 +106,11 @@ def lib() -> C.CDLL:
             "moe_path_host": ([pp, P, P, P, P, P, C.POINTER(moe_ubatch_bufs), P, P, P], i),
             "moe_expert_combine": ([pp, P, P, P, P, P, P, P, P, P, P, C.c_size_t, C.c_uint32, P], i),
             "moe_combine": ([pp, P, P, P, P, P, P], i),
+            "moe_route_gated": ([pp, gp, P, P, P, P, P, P, P, P, P, P, C.c_size_t, P], i),
+            "moe_route_gated_backward": ([pp, gp, P, P, P, P, P, P], i),
+            "moe_combine_backward": ([pp, P, P, P, P, P, P, P, P], i),
+            "moe_expert_w4_workspace_bytes": ([pp, wp], C.c_size_t),
+            "moe_expert_w4": ([pp, wp, P, P, P, P, P, P, P, C.c_size_t, P], i),
             "dbo_create": ([C.POINTER(P)], i),
             "dbo_destroy": ([P], None),
             "dbo_step": ([P, pp, P, P, P, C.POINTER(moe_ubatch_bufs), P, P, P, i], i),
@@ -106,6 +130,8 @@ def lib() -> C.CDLL:
 EXPORTS = ("moe_status_string", "moe_validate", "moe_device_status", "moe_route_workspace_bytes", "moe_route", "moe_route_noalloc",
            "moe_dispatch", "moe_src_offsets", "moe_route_dispatch_workspace_bytes", "moe_route_dispatch",
            "moe_expert_synthetic", "moe_expert_gemm_fp8", "moe_expert_gemm_bf16", "moe_ready_flags_bytes", "moe_expert_combine", "moe_path_host",
+           "moe_route_gated", "moe_route_gated_backward", "moe_combine_backward", "moe_expert_w4_workspace_bytes",
+           "moe_expert_w4",
            "moe_combine", "dbo_create", "dbo_destroy", "dbo_step", "dbo_read_timing",
            "moe_layer_stand_in", "dbo_layers", "dbo_layers_capture", "dbo_graph_launch")
 
@@ -238,6 +264,74 @@ def moe_combine(p, y, topk_idx, topk_w, slot, out, stream=None):
     rc = lib().moe_combine(C.byref(p), _ptr(y), _ptr(topk_idx), _ptr(topk_w), _ptr(slot), _ptr(out),
                            _stream(stream))
     _check("moe_combine", rc)
+
+
+def gate(score=MOE_SCORE_SOFTMAX, groups=1, top_groups=None, group_rule=MOE_GROUP_MAX, renormalise=True, scale=1.0,
+         logits_type=MOE_LOGITS_F32) -> moe_gate:
+    """How moe_route_gated chooses and weights; top_groups None: every group may be chosen from."""
+    return moe_gate(score, groups, groups if top_groups is None else top_groups, group_rule, int(bool(renormalise)),
+                    logits_type, scale)
+
+
+def moe_route_gated(p, gate, logits, bias, topk_idx, topk_w, counts, offsets, slot, rank_counts, dropped, workspace,
+                    stream=None):
+    """moe_route with softmax or sigmoid scores, a balance bias (or None), groups and a scale on the weights."""
+    rc = lib().moe_route_gated(C.byref(p), C.byref(gate), _ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(topk_w),
+                               _ptr(counts), _ptr(offsets), _ptr(slot), _ptr(rank_counts), _ptr(dropped),
+                               _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("moe_route_gated", rc)
+
+
+def moe_route_gated_backward(p, gate, logits, topk_idx, topk_w, d_topk_w, d_logits, stream=None):
+    """d_logits [T][E], every element written: the gradient of topk_w with the choice held fixed. logits may be
+    None for a renormalised softmax."""
+    rc = lib().moe_route_gated_backward(C.byref(p), C.byref(gate), _ptr(logits), _ptr(topk_idx), _ptr(topk_w),
+                                        _ptr(d_topk_w), _ptr(d_logits), _stream(stream))
+    _check("moe_route_gated_backward", rc)
+
+
+def moe_combine_backward(p, y, d_out, topk_idx, topk_w, slot, d_y, d_topk_w, stream=None):
+    """Gradient of moe_combine: d_y's rows of kept pairs (others are not written) and d_topk_w."""
+    rc = lib().moe_combine_backward(C.byref(p), _ptr(y), _ptr(d_out), _ptr(topk_idx), _ptr(topk_w), _ptr(slot),
+                                    _ptr(d_y), _ptr(d_topk_w), _stream(stream))
+    _check("moe_combine_backward", rc)
+
+
+def w4(n_in, n_out, group=128, act=MOE_ACT_NONE) -> moe_w4:
+    """Shape of one 4-bit matrix per expert: n_out rows, or 2 n_out (gate, then up) for MOE_ACT_SILU_GATE."""
+    return moe_w4(n_in, n_out, group, act)
+
+
+def w4_pack(codes):
+    """4-bit codes uint8 [..., K] (0..15, K a multiple of 128) in the inputs' order -> uint8 [..., K/2] as
+    moe_expert_w4 reads them. Done once, when weights are loaded; any device."""
+    import torch
+    if codes.dtype != torch.uint8 or codes.shape[-1] % 128 != 0:
+        raise ValueError("w4_pack takes uint8 codes, a multiple of 128 of them in the last dimension")
+    c = codes.unflatten(-1, (-1, 4, 4, 4, 2))               # block, j, t, pair i, even or odd input
+    c = c.transpose(-4, -3)                                  # block, t, j, i, even or odd
+    halves = c.transpose(-2, -1)                             # ... even or odd, i: 4 codes to 16 bits
+    return (halves[..., 0::2] | halves[..., 1::2] << 4).flatten(-5)
+
+
+def w4_unpack(w_q):
+    """The codes uint8 [..., K], in the inputs' order, of packed rows uint8 [..., K/2]."""
+    import torch
+    b = w_q.unflatten(-1, (-1, 4, 4, 2, 2))                  # block, t, j, even or odd, pair of codes
+    halves = torch.stack([b & 15, b >> 4], -1).flatten(-2)   # ... even or odd, i
+    return halves.transpose(-2, -1).transpose(-4, -3).flatten(-5)
+
+
+def moe_expert_w4_workspace_bytes(p: moe_problem, w: moe_w4) -> int:
+    return lib().moe_expert_w4_workspace_bytes(C.byref(p), C.byref(w))
+
+
+def moe_expert_w4(p, w, x, x_scale, counts, w_q, w_scale, y, workspace, stream=None):
+    """y[e][c] = x[e][c] . W_e^T (or its gated SiLU) on kept rows, W_e of 4-bit codes with group scales. x bf16 with
+    x_scale None, or e4m3 codes with their scales, as p's dispatch type says."""
+    rc = lib().moe_expert_w4(C.byref(p), C.byref(w), _ptr(x), _ptr(x_scale), _ptr(counts), _ptr(w_q), _ptr(w_scale),
+                             _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("moe_expert_w4", rc)
 
 
 class DboContext:

@@ -134,6 +134,14 @@ bool set_smem_once(PerContext<int> &done, Kernel kernel, int bytes) {
 // tile of 8 tokens, and the byte counts cnt8[E][route_small_stride(T)].
 int launch_route_topk_small(const Dims &d, cudaStream_t st, const float *logits, int32_t *topk_idx, float *topk_w,
                             int32_t *rank, uint8_t *cnt8);
+// The route's kernels after its top-k (moe_route.cu): every pair's slot from its
+// rank within its tile and the per-tile counts, and the totals. Small batches
+// take byte counts of tiles of 8 tokens, larger ones 32-bit counts of tiles of
+// 32, with room for the two-level scan behind them.
+int launch_route_slots_small(const Dims &d, cudaStream_t st, const uint8_t *cnt8, const int32_t *topk_idx,
+                             int32_t *slot, int32_t *counts, int32_t *offsets, int32_t *rank_counts, int32_t *dropped);
+int launch_route_slots_large(const Dims &d, cudaStream_t st, int32_t *tile_counts, const int32_t *topk_idx,
+                             int32_t *slot, int32_t *counts, int32_t *offsets, int32_t *rank_counts, int32_t *dropped);
 // moe_layer_stand_in with a cap on its grid (moe_layers.cu).
 int layer_stand_in(const void *in, void *out, int64_t n_elements, float a, int32_t busy_fmas, int max_blocks,
                    cudaStream_t st);
@@ -457,46 +465,14 @@ __device__ __forceinline__ int warp_row_prefix(const uint8_t *__restrict__ row, 
     return (int)warp_sum(acc);
 }
 
-// One block (any multiple of 32 threads, at most 1024) turns the byte counts
-// cnt8[E][stride] of n_tiles tiles into the totals: counts[e], offsets[0..E]
-// (exclusive scan), rank_counts[r] (kept rows of the experts of rank r) and
-// dropped. tot: E ints, wsum: 32 ints, both shared. Each thread issues up to
-// BATCH loads before it uses any.
-template <int BATCH>
-__device__ inline void small_route_totals(const uint8_t *__restrict__ cnt8, size_t stride, int n_tiles, int E, int R,
-                                          int C, int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
-                                          int32_t *__restrict__ rank_counts, int32_t *__restrict__ dropped, int *tot,
-                                          int *wsum) {
+// The totals of a route from tot[e], the pairs that chose expert e (shared, not
+// written here): counts[e], offsets[0..E] (exclusive scan), rank_counts[r] (kept
+// rows of the experts of rank r) and dropped. One block, any multiple of 32
+// threads; wsum: 32 ints, shared.
+__device__ inline void route_totals(const int *tot, int E, int R, int C, int32_t *__restrict__ counts,
+                                    int32_t *__restrict__ offsets, int32_t *__restrict__ rank_counts,
+                                    int32_t *__restrict__ dropped, int *wsum) {
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // every (expert, 16-byte piece) pair is one load, spread over all threads
-    // (so that a few experts with long rows still use the whole block); the
-    // pieces of a row meet in an integer sum, whose order does not matter
-    const int pieces = (n_tiles + 15) / 16;
-    for (int e = tid; e < E; e += nt) tot[e] = 0;
-    __syncthreads();
-    const int pairs = E * pieces;
-    for (int base = 0; base < pairs; base += BATCH * nt) {  // one pass while pairs <= BATCH * threads
-        uint4 v[BATCH];
-        int ex[BATCH];
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {                  // all loads issued before any is used
-            const int i = base + j * nt + tid;
-            ex[j] = -1;
-            if (i < pairs) {
-                ex[j] = i / pieces;
-                v[j] = __ldcg(reinterpret_cast<const uint4 *>(cnt8 + (size_t)ex[j] * stride +
-                                                              (size_t)(i - ex[j] * pieces) * 16));
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            if (ex[j] < 0) continue;
-            const int c = (base + j * nt + tid - ex[j] * pieces) * 16;
-            const unsigned sum = add_bytes_below(v[j], c, n_tiles, 0u);
-            if (sum != 0) atomicAdd(&tot[ex[j]], (int)sum);
-        }
-    }
-    __syncthreads();
     for (int e = tid; e < E; e += nt) counts[e] = tot[e];
     // exclusive scan of tot over e: each thread a run of consecutive experts
     const int per = (E + nt - 1) / nt;
@@ -545,6 +521,49 @@ __device__ inline void small_route_totals(const uint8_t *__restrict__ cnt8, size
         for (int w = 0; w < (nt >> 5); ++w) d += wsum[w];
         *dropped = d;
     }
+}
+
+// One block (any multiple of 32 threads, at most 1024) turns the byte counts
+// cnt8[E][stride] of n_tiles tiles into the totals: counts[e], offsets[0..E]
+// (exclusive scan), rank_counts[r] (kept rows of the experts of rank r) and
+// dropped. tot: E ints, wsum: 32 ints, both shared. Each thread issues up to
+// BATCH loads before it uses any.
+template <int BATCH>
+__device__ inline void small_route_totals(const uint8_t *__restrict__ cnt8, size_t stride, int n_tiles, int E, int R,
+                                          int C, int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
+                                          int32_t *__restrict__ rank_counts, int32_t *__restrict__ dropped, int *tot,
+                                          int *wsum) {
+    const int nt = blockDim.x, tid = threadIdx.x;
+    // every (expert, 16-byte piece) pair is one load, spread over all threads
+    // (so that a few experts with long rows still use the whole block); the
+    // pieces of a row meet in an integer sum, whose order does not matter
+    const int pieces = (n_tiles + 15) / 16;
+    for (int e = tid; e < E; e += nt) tot[e] = 0;
+    __syncthreads();
+    const int pairs = E * pieces;
+    for (int base = 0; base < pairs; base += BATCH * nt) {  // one pass while pairs <= BATCH * threads
+        uint4 v[BATCH];
+        int ex[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {                  // all loads issued before any is used
+            const int i = base + j * nt + tid;
+            ex[j] = -1;
+            if (i < pairs) {
+                ex[j] = i / pieces;
+                v[j] = __ldcg(reinterpret_cast<const uint4 *>(cnt8 + (size_t)ex[j] * stride +
+                                                              (size_t)(i - ex[j] * pieces) * 16));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            if (ex[j] < 0) continue;
+            const int c = (base + j * nt + tid - ex[j] * pieces) * 16;
+            const unsigned sum = add_bytes_below(v[j], c, n_tiles, 0u);
+            if (sum != 0) atomicAdd(&tot[ex[j]], (int)sum);
+        }
+    }
+    __syncthreads();
+    route_totals(tot, E, R, C, counts, offsets, rank_counts, dropped, wsum);
 }
 
 __device__ __forceinline__ uint32_t logit_key(float f) {

@@ -366,6 +366,45 @@ int launch_route_topk_small(const Dims &d, cudaStream_t st, const float *logits,
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Small batches, K2. An empty batch still runs the totals block: it writes the
+// zero counts.
+int launch_route_slots_small(const Dims &d, cudaStream_t st, const uint8_t *cnt8, const int32_t *topk_idx,
+                             int32_t *slot, int32_t *counts, int32_t *offsets, int32_t *rank_counts,
+                             int32_t *dropped) {
+    const int n_tiles = (d.T + kSmallTileTokens - 1) / kSmallTileTokens;
+    const cudaError_t e = launch_pdl(route_slots_small_kernel, n_tiles + 1, kSmallTileTokens * 32, st, d.T, n_tiles,
+                                     d.E, d.k, d.R, d.C, cnt8, (int)route_small_stride(d.T), topk_idx, slot, counts,
+                                     offsets, rank_counts, dropped);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Large batches: many tiles take the two-level scan of the tile counts (chunk
+// sums, then their exclusive bases) before the finaliser, each kernel a
+// programmatic dependent of the last, so that its launch latency overlaps the
+// run of the kernel before it.
+int launch_route_slots_large(const Dims &d, cudaStream_t st, int32_t *wc, const int32_t *topk_idx, int32_t *slot,
+                             int32_t *counts, int32_t *offsets, int32_t *rank_counts, int32_t *dropped) {
+    const int n_tiles = (d.T + kTileTokens - 1) / kTileTokens;
+    const int32_t *chunk_base = nullptr;
+    if (route_two_level((size_t)n_tiles, d.E)) {
+        const int n_chunks = (n_tiles + kChunkTiles - 1) / kChunkTiles;
+        int32_t *sums = wc + (size_t)n_tiles * d.E;
+        int32_t *bases = sums + (size_t)n_chunks * d.E;
+        const int threads = d.E < 1024 ? (d.E + 31) / 32 * 32 : 1024;
+        if (launch_pdl(route_chunk_sums_kernel, n_chunks, threads, st, n_tiles, d.E,
+                       static_cast<const int32_t *>(wc), sums) != cudaSuccess ||
+            launch_pdl(route_chunk_scan_kernel, 1, 1024, st, n_chunks, d.E, static_cast<const int32_t *>(sums),
+                       bases) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        chunk_base = bases;
+    }
+    if (launch_pdl(route_finalize_kernel, n_tiles, 1024, st, d.T, n_tiles, d.E, d.k, d.R, d.C,
+                   static_cast<const int32_t *>(wc), chunk_base, topk_idx, slot, counts, offsets, rank_counts,
+                   dropped) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+}
+
 }  // namespace moe
 
 extern "C" int moe_route(const moe_problem *p, const float *logits, int32_t *topk_idx, float *topk_w,
@@ -397,13 +436,7 @@ extern "C" int moe_route(const moe_problem *p, const float *logits, int32_t *top
             rc = launch_route_topk_small(d, st, logits, topk_idx, topk_w, slot, cnt8);
             if (rc != MOE_OK) return rc;
         }
-        // an empty batch still runs the totals block: it writes the zero counts
-        if (launch_pdl(route_slots_small_kernel, n_tiles + 1, kSmallTileTokens * 32, st, d.T, n_tiles, d.E, d.k, d.R,
-                       d.C, static_cast<const uint8_t *>(cnt8), (int)route_small_stride(d.T),
-                       static_cast<const int32_t *>(topk_idx), slot, counts, offsets, rank_counts,
-                       dropped) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        return MOE_OK;
+        return launch_route_slots_small(d, st, cnt8, topk_idx, slot, counts, offsets, rank_counts, dropped);
     }
     int32_t *wc = static_cast<int32_t *>(workspace);
     const int n_tiles = (d.T + kTileTokens - 1) / kTileTokens;
@@ -418,28 +451,7 @@ extern "C" int moe_route(const moe_problem *p, const float *logits, int32_t *top
         else e = launch_topk<32>(n_tiles, st, logits, d, topk_idx, topk_w, slot, wc);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
-    // many tiles: the two-level scan of the tile counts (chunk sums, then
-    // their exclusive bases), each kernel a programmatic dependent of the last
-    const int32_t *chunk_base = nullptr;
-    if (route_two_level((size_t)n_tiles, d.E)) {
-        const int n_chunks = (n_tiles + kChunkTiles - 1) / kChunkTiles;
-        int32_t *sums = wc + (size_t)n_tiles * d.E;
-        int32_t *bases = sums + (size_t)n_chunks * d.E;
-        const int threads = d.E < 1024 ? (d.E + 31) / 32 * 32 : 1024;
-        if (launch_pdl(route_chunk_sums_kernel, n_chunks, threads, st, n_tiles, d.E,
-                       static_cast<const int32_t *>(wc), sums) != cudaSuccess ||
-            launch_pdl(route_chunk_scan_kernel, 1, 1024, st, n_chunks, d.E, static_cast<const int32_t *>(sums),
-                       bases) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        chunk_base = bases;
-    }
-    // launched as a programmatic dependent of the kernel before it: its launch
-    // latency overlaps that kernel's run
-    if (launch_pdl(route_finalize_kernel, n_tiles, 1024, st, d.T, n_tiles, d.E, d.k, d.R, d.C,
-                   static_cast<const int32_t *>(wc), chunk_base, static_cast<const int32_t *>(topk_idx), slot,
-                   counts, offsets, rank_counts, dropped) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    return MOE_OK;
+    return launch_route_slots_large(d, st, wc, topk_idx, slot, counts, offsets, rank_counts, dropped);
 }
 
 // ---- allocation-free variant ---------------------------------------------

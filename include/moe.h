@@ -308,6 +308,143 @@ int moe_combine(const moe_problem *p, const void *y,
                 const int32_t *topk_idx, const float *topk_w, const int32_t *slot,
                 void *out, void *stream);
 
+/* ---- Gated routing, its gradient and the combine's gradient --------------- */
+
+typedef enum moe_score {
+    MOE_SCORE_SOFTMAX = 0,      /* s = softmax(logits) over the E experts          */
+    MOE_SCORE_SIGMOID = 1       /* s = 1 / (1 + exp(-logit)), each expert by itself  */
+} moe_score;
+
+typedef enum moe_group_rule {
+    MOE_GROUP_MAX = 0,          /* a group counts as its best expert               */
+    MOE_GROUP_TOP2 = 1          /* ... as the sum of its two best experts' scores   */
+} moe_group_rule;
+
+typedef enum moe_logits_type {
+    MOE_LOGITS_F32 = 0,
+    MOE_LOGITS_BF16 = 1
+} moe_logits_type;
+
+/* How moe_route_gated chooses and weights. */
+typedef struct moe_gate {
+    int32_t score;           /* moe_score */
+    int32_t num_groups;      /* G: E % G == 0, 1 <= G <= 32; group g holds experts
+                                [g*E/G, (g+1)*E/G). 1: no groups                    */
+    int32_t top_groups;      /* groups a token may choose from, 1 <= top_groups <= G,
+                                top_groups * E/G >= k                               */
+    int32_t group_rule;      /* moe_group_rule; MOE_GROUP_TOP2 with G > 1 needs E/G >= 2 */
+    int32_t renormalise;     /* nonzero: the k weights are divided by their sum     */
+    int32_t logits_type;     /* moe_logits_type of logits and d_logits              */
+    float scale;             /* factor on the weights: finite, not 0                */
+} moe_gate;
+
+/* moe_route with a gate: per token t, with l = logits[t] (fp32 or bf16) in fp32,
+ *   s_e   = sigmoid(l_e) or softmax(l)_e;
+ *   key_e = s_e + bias[e], or l_e itself where bias is NULL (it orders as s_e);
+ *   the top_groups groups of the largest group scores may be chosen from: a
+ *     group's score is its largest key, or (MOE_GROUP_TOP2) the sum of its two
+ *     largest s_e + bias[e] (s_e where bias is NULL); equal groups go to the
+ *     lower index;
+ *   topk_idx[t][0..k-1]: the k largest keys of those groups, largest first,
+ *     equal keys to the lower expert index;
+ *   topk_w[t][j] = scale * s_{e_j}, divided by sum_i s_{e_i} if renormalise is
+ *     set (no underflow: rows of very low logits have their quotients too).
+ * The bias steers the choice only (balance between the experts); the weights
+ * come from the scores without it. bias: device f32[E] or NULL.
+ * Masked experts. An expert whose logit is -inf, NaN or at most the lowest
+ * finite bf16 value (-3.3895e38, which a mask of the type's lowest value puts
+ * there), or whose bias is -inf or NaN, is never chosen. Where fewer than k
+ * experts are left, the remaining choices are no pairs: topk_w 0, slot -1, an
+ * index that is in range and no other choice's, and counted in neither counts
+ * nor dropped; so offsets[E] = sum of counts can be below T*k. A group's
+ * MOE_GROUP_TOP2 score with fewer than two unmasked experts is -inf; such
+ * groups come last, and may still be chosen. A logit of +inf has sigmoid 1,
+ * and shares a softmax of 1 equally with the row's other +inf logits.
+ * Counts, offsets, slots, rank_counts, dropped, the workspace
+ * (moe_route_workspace_bytes) and determinism are those of moe_route; the hidden
+ * size of p is not used. Alignment: logits rows 16 bytes when E * element size
+ * is a multiple of 16, else the element's. One launch up to 32 tokens, else
+ * moe_route's two (four for large batches). MOE_ERR_INVALID_ARG for a gate
+ * outside the bounds above, MOE_ERR_UNSUPPORTED for G > 32. */
+int moe_route_gated(const moe_problem *p, const moe_gate *gate, const void *logits, const float *bias,
+                    int32_t *topk_idx, float *topk_w,
+                    int32_t *counts, int32_t *offsets, int32_t *slot,
+                    int32_t *rank_counts, int32_t *dropped,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of topk_w with respect to the logits, the choice held fixed (its
+ * bias and groups get none). With w = topk_w, a = scale, g = d_topk_w[t],
+ * dot = sum_i g_i w_i / a:
+ *   sigmoid, renormalised: d_logits[e_j] = w_j (1 - s_{e_j}) (g_j - dot)
+ *   sigmoid:               d_logits[e_j] = w_j (1 - s_{e_j}) g_j
+ *   softmax, renormalised: d_logits[e_j] = w_j (g_j - dot)
+ *   softmax:               d_logits[e]   = a s_e ((g_j if e = e_j, else 0) - dot), every e
+ * and 0 elsewhere: every element of d_logits[T][E] (logits_type) is written,
+ * rounded once from fp32. topk_idx and topk_w are moe_route_gated's outputs for
+ * the same gate and logits; a choice that is no pair, and a masked expert, has
+ * gradient 0, whatever d_topk_w holds for it. logits may be NULL for
+ * a renormalised softmax, whose weights say all. Indices outside [0, E) are
+ * skipped. The bounds of the gate and the alignment are those of
+ * moe_route_gated, d_logits as logits; the capacity of p is not used. */
+int moe_route_gated_backward(const moe_problem *p, const moe_gate *gate, const void *logits,
+                             const int32_t *topk_idx, const float *topk_w, const float *d_topk_w,
+                             void *d_logits, void *stream);
+
+/* Gradient of moe_combine: for every pair with slot[t][j] >= 0, e = topk_idx[t][j],
+ *   d_y[e][slot]   = bf16( topk_w[t][j] * d_out[t] )         (fp32 product);
+ *   d_topk_w[t][j] = sum_h d_out[t][h] * y[e][slot][h]       (fp32 sums);
+ * d_topk_w of a dropped pair is 0; rows of d_y that belong to no pair are not
+ * written. The sums' order is fixed: results do not depend on the grid. y and
+ * d_y bf16 [E][C][H], d_out bf16 [T][H], 16-byte aligned, d_y not overlapping
+ * the inputs; d_topk_w f32[T][k]. d_y, recv's rows and x follow the same
+ * slots, so the gradient of a bf16 moe_dispatch is moe_combine of the rows'
+ * gradients with weights of 1. */
+int moe_combine_backward(const moe_problem *p, const void *y, const void *d_out,
+                         const int32_t *topk_idx, const float *topk_w, const int32_t *slot,
+                         void *d_y, float *d_topk_w, void *stream);
+
+/* ---- Experts with 4-bit weights -------------------------------------------- */
+
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,           /* y = x W^T                                        */
+    MOE_ACT_SILU_GATE = 1       /* y = silu(x Wg^T) * (x Wu^T)                      */
+} moe_act;
+
+/* The shape of one matrix per expert with 4-bit weights and group scales. */
+typedef struct moe_w4 {
+    int32_t n_in;            /* K, a multiple of 128, 128 <= K <= 65536             */
+    int32_t n_out;           /* N, a multiple of 8, 8 <= N <= 65536                 */
+    int32_t group;           /* inputs per scale: 32, 64 or 128                     */
+    int32_t act;             /* moe_act; the matrix has M = N rows, or 2N (the N rows
+                                of Wg, then the N rows of Wu) for MOE_ACT_SILU_GATE */
+} moe_w4;
+
+/* Bytes of device workspace moe_expert_w4 needs (host-only); 0 if p or w is
+ * invalid. Contents need no initialisation. */
+size_t moe_expert_w4_workspace_bytes(const moe_problem *p, const moe_w4 *w);
+
+/* Rows of each expert times that expert's 4-bit matrix:
+ *   r[m] = sum_g w_scale[e][m][g] * sum_{i in group g} x[e][c][i] * (q[e][m][i] - 8)
+ *   y[e][c][n] = bf16(r[n]), or bf16(silu(r[n]) * r[N + n]),  silu(v) = v / (1 + exp(-v))
+ * for c < min(counts[e], C); other rows of y are not written and other rows of
+ * x not used. The products are exact, the sums in fp32 (an fp8 row's scale is
+ * applied to each 128-input block's sum), rounded once.
+ * x: the problem's dispatch_dtype says which: bf16 [E][C][K] with x_scale NULL,
+ *   or e4m3 [E][C][K] with x_scale f32 [E][C][K/128] as moe_dispatch writes
+ *   them; the hidden size of p itself is not used. Two calls make an expert's
+ *   MLP: gate and up with MOE_ACT_SILU_GATE, then down (a bf16 problem).
+ * w_q u8 [E][M][K/2]: 4-bit codes q, 0..15, packed in blocks of 128 inputs (64
+ *   bytes): the little-endian 32-bit word 4 t + j of a block (t, j < 4) holds
+ *   inputs 32 j + 8 t + i, i < 8, input i's code at bit 4 (i / 2) + 16 (i % 2).
+ *   w_scale bf16 [E][M][K/group].
+ * One row to many rows for an expert: for few rows the call is bound by
+ * reading the weights of the experts that have any. counts is moe_route's.
+ * x, w_q, y, workspace 16-byte aligned, w_scale 8; max_blocks caps the grid.
+ * Launched as a programmatic dependent of the previous kernel. */
+int moe_expert_w4(const moe_problem *p, const moe_w4 *w, const void *x, const float *x_scale,
+                  const int32_t *counts, const void *w_q, const void *w_scale, void *y,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- Dual batch overlap ------------------------------------------------- */
 
 /* Buffers of one micro-batch, each sized for its token count (see dbo_step). */
