@@ -32,12 +32,9 @@
 // status word and a CTA-wide abort flag; the CTA then drains its copies and
 // MMAs in flight (again bounded), frees its TMEM and returns.
 #include "moe_internal.cuh"
-
-#include <cuda.h>
-#include <cudaTypedefs.h>
+#include "moe_tc.cuh"
 
 #include <algorithm>
-#include <mutex>
 
 namespace moe {
 namespace {
@@ -74,17 +71,6 @@ constexpr size_t kGemmSmemBytes =
          : GemmGeom<true>::kStages * GemmGeom<true>::kStageBytes) +
     1024;                                        // + alignment slack
 constexpr int kWideMinRows = 512;               // mean kept rows per expert from which bf16 takes wide tiles
-constexpr unsigned kGemmPollLimit = 1u << 20;
-
-// Shared-memory matrix descriptor of a K-major tile whose rows are 128 bytes,
-// 128-byte swizzled (as TMA writes it): 8-row swizzle atoms 1024 bytes apart.
-__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t saddr) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);           // start address
-    d |= (uint64_t)(1024u >> 4) << 32;                           // stride byte offset
-    d |= (uint64_t)1 << 46;                                      // descriptor version
-    d |= (uint64_t)2 << 61;                                      // 128-byte swizzle
-    return d;
-}
 
 // Instruction descriptors, both operands K-major, fp32 accumulator, M = 128,
 // N = kBN: kind::f8f6f4 with A and B e4m3 (format 0), kind::f16 with A and B
@@ -94,17 +80,6 @@ constexpr uint32_t kIdescShape = (1u << 4)                          // D format 
                                  | ((uint32_t)(kBM >> 4) << 24);    // M / 16
 constexpr uint32_t kIdescF8 = kIdescShape | (0u << 7) | (0u << 10);
 constexpr uint32_t kIdescBF16 = kIdescShape | (1u << 7) | (1u << 10);
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
 
 // One MMA of 32 bytes of K per row: 32 e4m3 (kind::f8f6f4) or 16 bf16 (kind::f16).
 template <bool FP8>
@@ -121,36 +96,6 @@ __device__ __forceinline__ void mma_k32b(uint32_t tmem_d, uint64_t a, uint64_t b
             "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(tmem_d),
             "l"(a), "l"(b), "r"(kIdescBF16), "r"(accumulate)
             : "memory");
-}
-
-// Arrives once on the mbarrier when every MMA this thread issued so far is complete.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// Bounded wait on phase `parity`; gives up early once another role aborted.
-__device__ __forceinline__ bool gemm_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
-    for (unsigned i = 0; i < kGemmPollLimit; ++i) {
-        uint32_t done;
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                     : "=r"(done)
-                     : "r"(bar), "r"(parity)
-                     : "memory");
-        if (done) return true;
-        if ((i & 1023u) == 1023u && *abort_flag) return false;
-    }
-    *abort_flag = 1;
-    return false;
 }
 
 // The tiles holding kept rows, in the order (expert, output tile, row tile):
@@ -524,20 +469,6 @@ expert_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_const
 }
 
 // ---- host: tensor maps --------------------------------------------------------
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
 
 // A [rows][cols] matrix of 1- or 2-byte elements read in tiles of box_rows x
 // 128 bytes, 128-byte swizzled; rows past the end read as zero.

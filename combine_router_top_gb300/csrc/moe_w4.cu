@@ -16,34 +16,12 @@
 // (g, t) of the fragment holds bytes 16 t .. 16 t + 15 of row g, one 16-byte
 // load: the packing puts there 8 inputs of each 32, which are the lane's
 // share of two MMA steps, so that every step stays within one group of 32.
-#include "moe_internal.cuh"
-
-#include <cuda_fp16.h>
+#include "moe_w4.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kW4Warps = 8;
-
-struct W4Args {
-    int E, C, K, N, M, group;          // M rows of the matrix: N, or 2N with the gate
-    int nkb;                           // blocks of 128 inputs
-    int row_tiles;                     // tiles of 16 matrix rows (8 outputs with the gate)
-};
-
-// Codes 2i and 2i+1 of a packed word as two 16-bit numbers q - 8: the codes
-// become the low mantissa bits of 128 (bf16) or 1024 (fp16), whose offset one
-// exact subtraction takes off.
-template <bool F16>
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
-    const uint32_t c = ((word >> (4 * i)) & 0x000F000Fu) | (F16 ? 0x64006400u : 0x43004300u);
-    uint32_t r;
-    if constexpr (F16)
-        asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(0x64086408u));
-    else
-        asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(0x43084308u));
-    return r;
-}
 
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -57,14 +35,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// Two e4m3 codes -> two fp16 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
-}
-
-__device__ __forceinline__ float silu(float v) { return __fdiv_rn(v, __fadd_rn(1.0f, expf(-v))); }
 
 // Eight inputs of one row as four 16-bit pairs.
 template <bool F8>
@@ -142,10 +112,10 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
     token_tile_offsets(counts, a.E, a.C, kTokens, off, warp_tot);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const unsigned tiles = off[a.E];
+    const unsigned tiles = off[a.E], row_tiles = (a.N + kOut - 1) / kOut;
     const size_t w_row = (size_t)a.K / 2, s_row = (size_t)a.K / GS, x_row = F8 ? (size_t)a.K : 2 * (size_t)a.K;
 
-    for (UnitWalk wk(blockIdx.x, gridDim.x, a.row_tiles); wk.row < tiles; wk.next()) {
+    for (UnitWalk wk(blockIdx.x, gridDim.x, row_tiles); wk.row < tiles; wk.next()) {
         const int e = expert_of_row(off, a.E, (int)wk.row);
         const int kept = min(__ldg(counts + e), a.C);
         const int tok0 = (int)(wk.row - off[e]) * kTokens;
@@ -172,6 +142,11 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
             float fa[kGroups], fb[kGroups];
             load_scales<GS>(sa + kb * kGroups, fa);
             load_scales<GS>(sb + kb * kGroups, fb);
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q) {
+                fa[q] *= kW4Unit<F8>;
+                fb[q] *= kW4Unit<F8>;
+            }
             const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -180,12 +155,12 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (j % (GS / 32) == 0) part[0] = part[1] = part[2] = part[3] = 0.0f;
-                    uint32_t b[4];
+                    uint32_t b[4], pa[4], pb[4];
                     load_x8<F8>(px[n] + (size_t)kb * (F8 ? 128 : 256) + j * (F8 ? 32 : 64), b);
-                    mma16816<F8>(part, w4_pair<F8>(wa[j], 0), w4_pair<F8>(wb[j], 0), w4_pair<F8>(wa[j], 1),
-                                 w4_pair<F8>(wb[j], 1), b[0], b[1]);
-                    mma16816<F8>(part, w4_pair<F8>(wa[j], 2), w4_pair<F8>(wb[j], 2), w4_pair<F8>(wa[j], 3),
-                                 w4_pair<F8>(wb[j], 3), b[2], b[3]);
+                    w4_pairs<F8>(wa[j], pa);
+                    w4_pairs<F8>(wb[j], pb);
+                    mma16816<F8>(part, pa[0], pb[0], pa[1], pb[1], b[0], b[1]);
+                    mma16816<F8>(part, pa[2], pb[2], pa[3], pb[3], b[2], b[3]);
                     if (j % (GS / 32) == GS / 32 - 1) {
                         const int q = j / (GS / 32);
                         float(&to)[4] = F8 ? blk : acc[n];
@@ -222,20 +197,19 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
             }
             const int c = tok0 + 8 * warp + 2 * t;
             uint16_t *o = y + ((size_t)e * a.C + c) * a.N + n0 + g;
-            const auto put = [](uint16_t *p, float v) { *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(v); };
             if constexpr (GATE) {
                 if (n0 + g < a.N) {
-                    if (c < kept) put(o, silu(r.x) * r.z);
-                    if (c + 1 < kept) put(o + a.N, silu(r.y) * r.w);
+                    if (c < kept) put_bf16(o, silu(r.x) * r.z);
+                    if (c + 1 < kept) put_bf16(o + a.N, silu(r.y) * r.w);
                 }
             } else {
                 if (n0 + g < a.N) {
-                    if (c < kept) put(o, r.x);
-                    if (c + 1 < kept) put(o + a.N, r.y);
+                    if (c < kept) put_bf16(o, r.x);
+                    if (c + 1 < kept) put_bf16(o + a.N, r.y);
                 }
                 if (n0 + 8 + g < a.N) {
-                    if (c < kept) put(o + 8, r.z);
-                    if (c + 1 < kept) put(o + 8 + a.N, r.w);
+                    if (c < kept) put_bf16(o + 8, r.z);
+                    if (c + 1 < kept) put_bf16(o + 8 + a.N, r.w);
                 }
             }
         }
@@ -248,7 +222,7 @@ int launch_rows(const Dims &d, const W4Args &a, cudaStream_t st, const void *x, 
     static PerContext<int> resident_cache;
     const int resident = resident_blocks_cached(resident_cache, expert_w4_rows_kernel<F8, GS, GATE, NT>, kW4Warps * 32);
     const long long tiles = (long long)(d.T * (long long)d.k < (long long)d.E * d.C ? d.T * (long long)d.k : (long long)d.E * d.C);
-    const int grid = persistent_grid(tiles * a.row_tiles, resident, d.max_blocks);
+    const int grid = persistent_grid(tiles * ((a.N + (GATE ? 8 : 16) - 1) / (GATE ? 8 : 16)), resident, d.max_blocks);
     if (launch_pdl(expert_w4_rows_kernel<F8, GS, GATE, NT>, grid, kW4Warps * 32, st, a, static_cast<const uint8_t *>(x),
                    x_scale, counts, static_cast<const uint8_t *>(w_q), static_cast<const uint16_t *>(w_scale),
                    static_cast<uint16_t *>(y)) != cudaSuccess)
@@ -281,13 +255,32 @@ int check_w4(const moe_w4 *w) {
     return MOE_OK;
 }
 
+W4Args w4_args(const Dims &d, const moe_w4 *w) {
+    W4Args a;
+    a.E = d.E;
+    a.C = d.C;
+    a.K = w->n_in;
+    a.N = w->n_out;
+    a.M = w->act == MOE_ACT_SILU_GATE ? 2 * w->n_out : w->n_out;
+    a.group = w->group;
+    a.nkb = a.K / 128;
+    return a;
+}
+
+// Many rows per expert take the tiles.
+bool w4_many_rows(const Dims &d) {
+    return (d.T < d.C ? d.T : d.C) > 8 && (long long)d.T * d.k >= 4LL * d.E;
+}
+
 }  // namespace
 }  // namespace moe
 
 extern "C" size_t moe_expert_w4_workspace_bytes(const moe_problem *p, const moe_w4 *w) {
     using namespace moe;
-    if (check_problem(p, nullptr) != MOE_OK || check_w4(w) != MOE_OK) return 0;
-    return 256;
+    Dims d;
+    if (check_problem(p, &d) != MOE_OK || check_w4(w) != MOE_OK) return 0;
+    const size_t n = w4_many_rows(d) ? w4_tiles_workspace_bytes(d, w4_args(d, w)) : 0;
+    return n < 256 ? 256 : n;
 }
 
 extern "C" int moe_expert_w4(const moe_problem *p, const moe_w4 *w, const void *x, const float *x_scale,
@@ -304,19 +297,12 @@ extern "C" int moe_expert_w4(const moe_problem *p, const moe_w4 *w, const void *
     if (f8 != (x_scale != nullptr)) return MOE_ERR_INVALID_ARG;
     if (!x || !counts || !w_q || !w_scale || !y || !workspace) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < moe_expert_w4_workspace_bytes(p, w)) return MOE_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(w_q, 16) || !aligned(y, 16) || !aligned(workspace, 16) || !aligned(w_scale, 8) ||
+    if (!aligned(x, 16) || !aligned(w_q, 16) || !aligned(y, 16) || !aligned(workspace, 16) || !aligned(w_scale, 16) ||
         !aligned(counts, 4) || !aligned(x_scale, 4))
         return MOE_ERR_INVALID_ARG;
-    W4Args a;
-    a.E = d.E;
-    a.C = d.C;
-    a.K = w->n_in;
-    a.N = w->n_out;
-    a.M = w->act == MOE_ACT_SILU_GATE ? 2 * w->n_out : w->n_out;
-    a.group = w->group;
-    a.nkb = a.K / 128;
-    a.row_tiles = w->act == MOE_ACT_SILU_GATE ? a.N / 8 : (a.N + 15) / 16;
+    const W4Args a = w4_args(d, w);
     cudaStream_t st = as_stream(stream);
+    if (w4_many_rows(d)) return launch_w4_tiles(d, a, st, x, x_scale, counts, w_q, w_scale, y, workspace);
     if (f8) return launch_group<true>(d, a, st, x, x_scale, counts, w_q, w_scale, y);
     return launch_group<false>(d, a, st, x, x_scale, counts, w_q, w_scale, y);
 }

@@ -1,0 +1,641 @@
+// moe_w4_tiles.cu -- the experts' products with 4-bit weights for many rows per
+// expert, on the tcgen05 tensor cores.
+//
+//   r[m] = sum_g scale[m][g] * sum_{i in g} x[i] (q[m][i] - 8)
+//
+// The weights are the 128-row operand and the expert's rows of x the columns
+// (16 to 64 of them), so that a TMEM lane is a row of the matrix: the thread that
+// reads a lane's sums has one scale to multiply them by, and the one that writes
+// the lane's weights has one row of codes to turn into bf16. The codes go from
+// shared memory through registers into TMEM, from where tcgen05.mma takes its
+// first operand; the 16-bit weights exist nowhere else. Each group's sum is exact
+// products added in fp32 into a fresh accumulator, then scaled in fp32.
+//
+// A persistent grid, one CTA per SM, walks tiles of (expert, 2 x 128 matrix rows,
+// up to 64 rows of x): rows n .. n+127 of the gate and of the up matrix, or 256
+// rows of a matrix without the gate. In each CTA:
+//   warp 0      one lane issues the TMA loads of each block of 128 inputs: two
+//               weight boxes of 128 rows x 64 bytes, and x in boxes of 16 rows x
+//               64 inputs, into a ring of 5 stages;
+//   warps 1, 3  the MMAs of a tile's even and odd blocks, one elected lane each: per
+//               group, the steps of both halves into fresh accumulators. All 512 TMEM
+//               columns are held: for each half and parity 64 columns of accumulators
+//               (two slots of 32, or one of 64 where the tile has over 32 rows of x)
+//               and 64 of operand (128 inputs);
+//   warp 2      brings the group scales (and fp8 rows' block scales), 8 groups at a
+//               time, from HBM to a ring in shared memory;
+//   warps 4-19  four TMEM quadrants x two halves x even and odd blocks: turn codes into
+//               operands;
+//   warps 20-27 four quadrants x two halves: add up the groups' sums, and write y.
+// Every mbarrier wait is bounded; one that gives up raises the status word and an
+// abort flag, the CTA drains what it has in flight, frees its TMEM and returns.
+#include "moe_tc.cuh"
+#include "moe_w4.cuh"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+constexpr int kTRows = 128;                          // matrix rows of one half (TMEM lanes)
+constexpr int kTTok = 64;                            // rows of x to a tile, at most
+constexpr int kTStages = 5;
+constexpr int kTThreads = 896;                       // 28 warps of 72 registers
+constexpr uint32_t kTWBytes = kTRows * 64;           // codes of one half's block
+constexpr uint32_t kTXBytes = kTTok * 128;           // x of 64 inputs
+constexpr uint32_t kTStageBytes = 2 * kTWBytes + 2 * kTXBytes;
+constexpr int kTChunks = 4, kTChunk = 8;             // scale ring: 4 chunks of 8 groups
+constexpr int kTScalePad = kTRows + 8;               // stride of a group's 128 scales: 8 groups on 8 bank sets
+constexpr size_t kTExBytes = (size_t)kTTok * kTRows * 4;
+constexpr size_t kTScaleBytes = (size_t)kTChunks * 2 * kTChunk * kTScalePad * 2;
+constexpr size_t kTXsBytes = (size_t)kTChunks * kTChunk * kTTok * 4;
+constexpr size_t kTSmemBytes = 1024 + kTStages * (size_t)kTStageBytes + kTExBytes + kTScaleBytes + kTXsBytes;
+
+// D[128 x N] (+)= A (TMEM) B: one step of 16 inputs.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The tiles holding kept rows, in the order (expert, matrix rows, rows of x), so
+// that the tiles that share weights run at about the same time.
+struct W4Tiles {
+    const int *first;                                // first tile of expert e; first[E] = their number
+    int E, n_tiles;
+    __device__ __forceinline__ void decode(int t, int &e, int &nt, int &tt) const {
+        e = expert_of_row(first, E, t);
+        const int per = (first[e + 1] - first[e]) / n_tiles;
+        const int local = t - first[e];
+        nt = local / per;
+        tt = local - nt * per;
+    }
+};
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
+
+// One warp brings the scales of groups c .. c+7 of the two halves' 128 matrix rows
+// (valid0 and valid1 of them in the matrix) to to[half][group][row], W bytes of a
+// row to a load, up to 16 loads in flight: a chunk serves 2, 4 or 8 blocks of 128
+// inputs. room() waits until the ring's slot may be written.
+template <int W, typename Room>
+__device__ __forceinline__ bool scale_chunk(const uint16_t *__restrict__ src0, const uint16_t *__restrict__ src1,
+                                            int groups, int c, int valid0, int valid1, uint16_t *__restrict__ to,
+                                            int lane, Room room) {
+    constexpr int kLanes = 16 / W, kRows = 32 / kLanes, kIter = kTRows / kRows;
+    constexpr int kWords = W < 4 ? 1 : W / 4, kAll = 16 / kWords, kBatch = 2 * kIter < kAll ? 2 * kIter : kAll;
+    const int r0 = lane / kLanes, c0 = (lane % kLanes) * (W / 2);
+    bool ok = true;
+#pragma unroll
+    for (int b = 0; b < 2 * kIter; b += kBatch) {
+        uint32_t v[kBatch][kWords];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int h = (b + i) / kIter, r = (b + i) % kIter * kRows + r0;
+            const uint16_t *p = (h ? src1 : src0) + (size_t)r * groups + c + c0;
+#pragma unroll
+            for (int q = 0; q < kWords; ++q) v[i][q] = 0u;
+            if (r < (h ? valid1 : valid0) && c + c0 < groups) {
+                if constexpr (W == 16) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+                    v[i][0] = u.x;
+                    v[i][1] = u.y;
+                    v[i][2] = u.z;
+                    v[i][3] = u.w;
+                } else if constexpr (W == 8) {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+                    v[i][0] = u.x;
+                    v[i][1] = u.y;
+                } else if constexpr (W == 4) {
+                    v[i][0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+                } else {
+                    v[i][0] = __ldg(p);
+                }
+            }
+        }
+        if (b == 0) ok = room();
+        if (!ok) return false;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int h = (b + i) / kIter, r = (b + i) % kIter * kRows + r0;
+#pragma unroll
+            for (int q = 0; q < W / 2; ++q)
+                to[(h * kTChunk + c0 + q) * kTScalePad + r] = (uint16_t)(v[i][q / 2] >> (16 * (q & 1)));
+        }
+    }
+    return true;
+}
+
+template <bool F8, int GS, bool GATE>
+__global__ void __launch_bounds__(kTThreads, 1)
+expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, W4Args a,
+                       const int32_t *__restrict__ counts, const uint16_t *__restrict__ w_scale,
+                       const float *__restrict__ x_scale, uint16_t *__restrict__ y, unsigned *status) {
+    constexpr int GPB = 128 / GS;                    // groups to a block of 128 inputs
+    constexpr int kOut = GATE ? kTRows : 2 * kTRows; // outputs of a tile
+    extern __shared__ uint8_t w4_smem_raw[];
+    __shared__ __align__(8) uint64_t full[kTStages], empty[kTStages];
+    __shared__ __align__(8) uint64_t a_full[2], a_free[2];                // operands of even and odd blocks
+    __shared__ __align__(8) uint64_t d_full[4], d_free[4];                // accumulators: [2 (odd block) + slot]
+    __shared__ __align__(8) uint64_t sc_full[kTChunks], sc_empty[kTChunks];
+    __shared__ __align__(8) uint64_t ex_full[4], ex_free[4];           // sums traded between the halves
+    __shared__ __align__(8) uint64_t s_drain;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+    __shared__ int s_first[kMaxExperts + 1];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t smem0 = (smem_u32(w4_smem_raw) + 1023u) & ~1023u;
+    uint8_t *const base = w4_smem_raw + (smem0 - smem_u32(w4_smem_raw));
+    float *const ex = reinterpret_cast<float *>(base + kTStages * kTStageBytes);
+    uint16_t *const sc = reinterpret_cast<uint16_t *>(base + kTStages * kTStageBytes + kTExBytes);
+    float *const xs = reinterpret_cast<float *>(base + kTStages * kTStageBytes + kTExBytes + kTScaleBytes);
+    const int nkb = a.nkb, groups = nkb * GPB;
+    const int n_tiles = (a.N + kOut - 1) / kOut;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kTStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&a_full[i], 8);
+            mbar_init(&a_free[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_free[i], 8);
+        }
+        for (int i = 0; i < kTChunks; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_empty[i], 8);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&ex_full[i], 2);
+            mbar_init(&ex_free[i], 2);
+        }
+        mbar_init(&s_drain, 1);
+        s_abort = 0;
+        fence_mbar_init();
+    }
+    pdl_wait();                                      // counts and x are final from here on
+    if (warp == 0) {
+        const int per = (a.E + 31) / 32;
+        int sum = 0;
+        for (int e = lane * per; e < min(a.E, lane * per + per); ++e)
+            sum += (min(__ldg(counts + e), a.C) + kTTok - 1) / kTTok * n_tiles;
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += v;
+        }
+        int run = incl - sum;
+        for (int e = lane * per; e < min(a.E, lane * per + per); ++e) {
+            s_first[e] = run;
+            run += (min(__ldg(counts + e), a.C) + kTTok - 1) / kTTok * n_tiles;
+        }
+        if (lane == 31) s_first[a.E] = incl;
+    }
+    __syncthreads();
+    const int total = s_first[a.E];
+    if ((int)blockIdx.x >= total) {
+        pdl_launch_dependents();
+        return;
+    }
+    const W4Tiles tiles{s_first, a.E, n_tiles};
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;                    // half h, odd block or even p: accumulators at 128 h + 64 p, operand 256 on
+
+    uint32_t issued = 0;                             // stages loaded, for the drain
+    // setmaxnreg is one instruction of a whole warpgroup (warps 0-3, 4-7, ...). 896 threads of 72 registers are
+    // 64512; 20 warps give up 16 of theirs for the 8 that hold 64 sums: 20 x 32 x 56 + 8 x 32 x 112 = 64512
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            const bool elected = elect_one();
+            uint32_t s = 0, phase = 0;               // stage and its use, odd or even
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                int e, nt, tt;
+                tiles.decode(t, e, nt, tt);
+                const int rows = min(min(__ldg(counts + e), a.C) - tt * kTTok, kTTok);
+                const int boxes = __shfl_sync(kFull, (rows + 15) / 16, 0);
+                const int ez = __shfl_sync(kFull, e, 0), row_w = __shfl_sync(kFull, nt * kOut, 0);
+                const int row_x = __shfl_sync(kFull, tt * kTTok, 0);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (issued >= kTStages && !(ok = warp_wait(smem_u32(&empty[0]) + 8 * s, phase ^ 1u, &s_abort)))
+                        break;
+                    if (elected) {
+                        const uint32_t at = smem0 + s * kTStageBytes, bar = smem_u32(&full[s]);
+                        mbar_expect_tx(&full[s], 2 * kTWBytes + boxes * 4096);
+                        tma_load_3d(at, &map_w, bar, kb * 64, row_w, ez);
+                        tma_load_3d(at + kTWBytes, &map_w, bar, kb * 64, row_w + (GATE ? a.N : kTRows), ez);
+#pragma unroll
+                        for (int i = 0; i < kTTok / 16; ++i) {
+                            if (i < boxes) {
+                                tma_load_3d(at + 2 * kTWBytes + i * 2048, &map_x, bar, kb * 128, row_x + i * 16, ez);
+                                tma_load_3d(at + 2 * kTWBytes + kTXBytes + i * 2048, &map_x, bar, kb * 128 + 64,
+                                            row_x + i * 16, ez);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++s == kTStages) s = 0, phase ^= 1u;
+                }
+            }
+        } else if (warp == 1 || warp == 3) {
+            // The whole warp runs the loop and one elected lane issues: the operands of
+            // tcgen05.mma are then warp-uniform values, and a step of 128 x 32 x 16 takes
+            // 17 cycles to issue where a loop of one lane by itself takes 45 (measured).
+            // One warp for the even blocks of a tile and one for the odd ones: between
+            // two blocks a warp spends as long in its waits as in its MMAs.
+            const uint32_t par = __shfl_sync(kFull, (uint32_t)warp >> 1, 0);
+            const uint32_t op = __shfl_sync(kFull, tmem, 0) + 256 + 64 * par;       // + 128 per half
+            const uint32_t d0 = __shfl_sync(kFull, tmem, 0) + 64 * par;             // + 128 per half, 32 per slot
+            const bool elected = elect_one();
+            const uint32_t b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[par]);
+            const uint32_t b_dfull = smem_u32(&d_full[2 * par]), b_dfree = smem_u32(&d_free[2 * par]);
+            uint32_t s0 = 0;                         // the tile's first stage
+            uint32_t a_phase = 0, d_phase = 0;       // odd or even use of the operand, of the slots (bits)
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                int e, nt, tt;
+                tiles.decode(t, e, nt, tt);
+                const int rows = min(min(__ldg(counts + e), a.C) - tt * kTTok, kTTok);
+                const uint32_t n16 = (uint32_t)__shfl_sync(kFull, (rows + 15) / 16 * 16, 0);
+                const uint32_t slots = n16 <= 32 ? 1u : 0u;          // xor mask: two slots of 32 columns, or one of 64
+                // fp32 sums; both operands fp16 (0) or bf16 (1); 128 x n16
+                const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | ((n16 >> 3) << 17) |
+                                       ((uint32_t)(kTRows >> 4) << 24);
+                // a slot of 64 columns takes the place of both slots of 32
+                if (!slots) ok = warp_wait(b_dfree + 8, (d_phase >> 1 & 1u) ^ 1u, &s_abort);
+                uint32_t slot = 0;
+                uint32_t s = s0 + par >= kTStages ? s0 + par - kTStages : s0 + par;
+                for (int kb = (int)par; kb < nkb && ok; kb += 2) {
+                    const uint64_t bx = umma_desc_sw128(smem0 + s * kTStageBytes + 2 * kTWBytes);
+                    // the warps that made the operand have seen the stage's loads complete
+                    ok = warp_wait(b_afull, a_phase, &s_abort);
+                    a_phase ^= 1u;
+#pragma unroll
+                    for (int q = 0; q < GPB; ++q) {
+                        if (ok) ok = warp_wait(b_dfree + 8 * slot, (d_phase >> slot & 1u) ^ 1u, &s_abort);
+                        if (!ok) break;
+                        d_phase ^= 1u << slot;
+                        tc_fence_after();
+                        if (elected) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                                for (int k = 0; k < GS / 16; ++k) {
+                                    const int k16 = q * (GS / 16) + k;
+                                    mma_ts(d0 + 128 * h + 32 * slot, op + 128 * h + 8 * k16,
+                                           bx + ((k16 >> 2) * kTXBytes + 32 * (k16 & 3)) / 16, idesc, k > 0 ? 1u : 0u);
+                                }
+                            }
+                            mma_commit(b_dfull + 8 * slot);
+                            if (q == GPB - 1) {      // the operand and the stage have been read
+                                mma_commit(b_afree);
+                                mma_commit(smem_u32(&empty[0]) + 8 * s);
+                            }
+                        }
+                        __syncwarp();
+                        slot ^= slots;
+                    }
+                    s += 2;
+                    if (s >= kTStages) s -= kTStages;
+                }
+                s0 = (s0 + nkb) % kTStages;
+            }
+        } else {
+            constexpr int KPC = kTChunk / GPB;       // blocks of 128 inputs to a chunk
+            const int chunks = (groups + kTChunk - 1) / kTChunk;
+            uint32_t cg = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < total && !s_abort; t += gridDim.x) {
+                int e, nt, tt;
+                tiles.decode(t, e, nt, tt);
+                // first outputs and matrix rows of the two halves, and how many of their 128 rows there are
+                const int n0 = nt * kOut, n1 = GATE ? n0 : n0 + kTRows;
+                const int valid0 = min(a.N - n0, kTRows), valid1 = min(a.N - n1, kTRows);
+                const uint16_t *src0 = w_scale + ((size_t)e * a.M + n0) * groups;
+                const uint16_t *src1 = w_scale + ((size_t)e * a.M + (GATE ? a.N + n0 : n1)) * groups;
+                const int kept = min(__ldg(counts + e), a.C) - tt * kTTok;
+                const float *xsrc = F8 ? x_scale + ((size_t)e * a.C + tt * kTTok) * nkb : nullptr;
+                for (int c = 0; c < chunks; ++c, ++cg) {
+                    const int buf = cg % kTChunks;
+                    const auto room = [&] {          // the ring's slot has been read
+                        return cg < kTChunks ||
+                               warp_wait(smem_u32(&sc_empty[buf]), ((cg / kTChunks) + 1) & 1, &s_abort);
+                    };
+                    uint16_t *to = sc + (size_t)buf * 2 * kTChunk * kTScalePad;
+                    const auto both = [&](auto w) {
+                        constexpr int W = decltype(w)::value;
+                        return scale_chunk<W>(src0, src1, groups, c * kTChunk, valid0, valid1, to, lane, room);
+                    };
+                    // rows of a multiple of 8 scales are loaded 16 bytes at a time, others as their alignment lets
+                    if (groups % 8 == 0) ok = both(Int<16>());
+                    else if (GPB == 4 || groups % 4 == 0) ok = both(Int<8>());
+                    else if (GPB == 2 || groups % 2 == 0) ok = both(Int<4>());
+                    else ok = both(Int<2>());
+                    if (!ok) break;
+                    if constexpr (F8) {
+#pragma unroll
+                        for (int r = lane; r < kTTok; r += 32) {
+#pragma unroll
+                            for (int i = 0; i < KPC; ++i)
+                                xs[((size_t)buf * kTChunk + i) * kTTok + r] =
+                                    r < kept && c * KPC + i < nkb ? __ldg(xsrc + (size_t)r * nkb + c * KPC + i) : 0.0f;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_full[buf]);
+                }
+            }
+        }
+    } else if (warp < 20) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int quad = warp & 3, h = ((warp - 4) >> 2) & 1, par = (warp - 4) >> 3;
+        const int row = quad * 32 + lane;            // TMEM lane: row of this half
+        const uint32_t op0 = tmem + ((uint32_t)(quad * 32) << 16) + 256 + 128 * h + 64 * par;
+        // 64 bytes of this row, 64-byte swizzled: chunk t of row r stands at t ^ (r / 2 % 4)
+        const uint8_t *const src0 = base + h * kTWBytes + row * 64;
+        const int swz = ((row >> 1) & 3) << 4;
+        const uint32_t b_full = smem_u32(&full[0]), b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[par]);
+        const int mine = (total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;       // tiles of this CTA
+        // stage and its use, odd or even, of this warp's next block; every other block of a tile
+        uint32_t s = par, phase = 0, a_phase = 0;
+        int kb = par;
+        for (int left = kb < nkb ? mine : 0; left > 0;) {
+            if (!warp_wait(b_full + 8 * s, phase, &s_abort)) break;
+            uint4 q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                q[i] = *reinterpret_cast<const uint4 *>(src0 + s * kTStageBytes + ((i << 4) ^ swz));
+            if (!warp_wait(b_afree, a_phase ^ 1u, &s_abort)) break;
+            a_phase ^= 1u;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t r[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w4_pairs<F8>(j == 0 ? q[i].x : j == 1 ? q[i].y : j == 2 ? q[i].z : q[i].w, r[i]);
+                tmem_st16(op0 + 16 * j, reinterpret_cast<const uint32_t(&)[16]>(r));
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(b_afull);
+            // two blocks on; over the end of a tile, to its next one's first of this parity
+            uint32_t step = 2;
+            if ((kb += 2) >= nkb) {
+                step = (uint32_t)(nkb - (kb - 2) + par);
+                kb = par;
+                --left;
+            }
+            s += step;
+            if (s >= kTStages) s -= kTStages, phase ^= 1u;
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+        const int quad = warp & 3, h = (warp - 20) >> 2;
+        const int row = quad * 32 + lane;            // TMEM lane: row of this half
+        const uint32_t d0 = tmem + ((uint32_t)(quad * 32) << 16) + 128 * h;
+        const uint32_t b_dfull = smem_u32(&d_full[0]), b_dfree = smem_u32(&d_free[0]);
+        uint32_t cg = 0, n_ex = 0;                   // chunks and tiles so far
+        uint32_t d_phase = 0;                        // odd or even use of the accumulators (bits)
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+            int e, nt, tt;
+            tiles.decode(t, e, nt, tt);
+            const int rows = min(min(__ldg(counts + e), a.C) - tt * kTTok, kTTok);
+            float acc[kTTok];
+#pragma unroll
+            for (int i = 0; i < kTTok; ++i) acc[i] = 0.0f;
+            const uint32_t slots = rows <= 32 ? 1u : 0u;
+            uint32_t slot = 0;                       // bit 2 p of it: even (p = 0) or odd block's next slot
+            for (int c = 0; c < groups && ok; c += kTChunk, ++cg) {
+                const uint32_t buf = cg % kTChunks;
+                ok = warp_wait(smem_u32(&sc_full[buf]), (cg / kTChunks) & 1, &s_abort);
+                const uint16_t *scr = sc + ((buf * 2 + h) * kTChunk) * kTScalePad + row;
+                const float *xr = xs + buf * kTChunk * kTTok;
+                const int n = min(kTChunk, groups - c);
+                // the groups of two blocks in turn, as their MMAs run side by side
+                for (int i = 0; i < kTChunk && ok; ++i) {
+                    const int p = i & 1, group = GPB == 1 ? i : GPB == 2 ? (i & 4) | p << 1 | (i >> 1 & 1) : p << 2 | i >> 1;
+                    if (group >= n) continue;
+                    const uint32_t sl = slot >> p & 1u, which = 2 * p + sl;
+                    ok = warp_wait(b_dfull + 8 * which, d_phase >> which & 1u, &s_abort);
+                    if (!ok) break;
+                    d_phase ^= 1u << which;
+                    slot ^= slots << p;
+                    tc_fence_after();
+                    const float ws = __uint_as_float((uint32_t)scr[group * kTScalePad] << 16) * kW4Unit<F8>;
+                    const float4 *xi = reinterpret_cast<const float4 *>(xr + group / GPB * kTTok);
+                    const uint32_t d = d0 + 64 * p + 32 * sl;
+#pragma unroll
+                    for (int b = 0; b < kTTok; b += 32) {              // up to 32 columns at a time: registers
+                        if (b < rows) {
+                            uint32_t v[32];
+                            tmem_ld16(d + b, v);
+                            if (b + 16 < rows) tmem_ld16(d + b + 16, v + 16);
+                            tmem_ld_wait();
+                            if (b + 32 >= rows) {    // the last of them is read
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive_at(b_dfree + 8 * which);
+                            }
+#pragma unroll
+                            for (int u = 0; u < 32; u += 4) {
+                                if (u < 16 || b + 16 < rows) {
+                                    float4 f = make_float4(ws, ws, ws, ws);
+                                    if constexpr (F8) {
+                                        f = xi[(b + u) / 4];
+                                        f = make_float4(f.x * ws, f.y * ws, f.z * ws, f.w * ws);
+                                    }
+                                    acc[b + u] = fmaf(__uint_as_float(v[u]), f.x, acc[b + u]);
+                                    acc[b + u + 1] = fmaf(__uint_as_float(v[u + 1]), f.y, acc[b + u + 1]);
+                                    acc[b + u + 2] = fmaf(__uint_as_float(v[u + 2]), f.z, acc[b + u + 2]);
+                                    acc[b + u + 3] = fmaf(__uint_as_float(v[u + 3]), f.w, acc[b + u + 3]);
+                                }
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_empty[buf]);
+            }
+            if (!ok) break;
+            uint16_t *out = y + ((size_t)e * a.C + tt * kTTok) * a.N;
+            if constexpr (GATE) {
+                // the halves' warps of the same rows trade: each gets the other's sums of half of the columns,
+                // 8 x 4 of the 64, and finishes those
+                const int n = nt * kOut + row;
+                if (n_ex > 0 && !(ok = warp_wait(smem_u32(&ex_free[quad]), (n_ex + 1) & 1, &s_abort))) break;
+#pragma unroll
+                for (int i = 0; i < kTTok; ++i)
+                    if (((i >> 3) & 1) != h && i < rows) ex[i * kTRows + row] = acc[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ex_full[quad]);
+                if (!(ok = warp_wait(smem_u32(&ex_full[quad]), n_ex & 1, &s_abort))) break;
+#pragma unroll
+                for (int b = 0; b < kTTok; b += 16) {
+                    if (b + 8 * h < rows) {
+                        float o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float other = ex[(b + 8 * h + i) * kTRows + row];
+                            const float mine = h == 0 ? acc[b + i] : acc[b + 8 + i];
+                            o[i] = h == 0 ? silu(mine) * other : silu(other) * mine;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (b + 8 * h + i < rows && n < a.N) put_bf16(out + (size_t)(b + 8 * h + i) * a.N + n, o[i]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ex_free[quad]);
+                ++n_ex;
+            } else {
+                const int n = nt * kOut + h * kTRows + row;
+#pragma unroll
+                for (int i = 0; i < kTTok; ++i)
+                    if (i < rows && n < a.N) put_bf16(out + (size_t)i * a.N + n, acc[i]);
+            }
+        }
+    }
+    pdl_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    if (s_abort) {
+        // drain: the loads and MMAs this CTA started must land before its
+        // shared memory and TMEM are released
+        volatile int no_abort = 0;
+        if (warp == 0 && lane == 0) {
+            atomicOr(status, kStatusWaitGaveUp);
+            for (uint32_t g = (issued > kTStages ? issued - kTStages : 0); g < issued; ++g)
+                gemm_wait(smem_u32(&full[g % kTStages]), (g / kTStages) & 1, &no_abort);
+        }
+        if (warp == 1 && elect_one()) {              // the lane that issued the MMAs
+            mma_commit(smem_u32(&s_drain));
+            gemm_wait(smem_u32(&s_drain), 0, &no_abort);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+// fp8 rows as fp16 (exact): the operand of the tiles' MMAs. Kept rows only.
+__global__ void __launch_bounds__(256)
+w4_rows_to_f16_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ counts, uint4 *__restrict__ out, int E,
+                      int C, int K) {
+    __shared__ int32_t off[kMaxExperts + 1];
+    __shared__ int32_t warp_tot[32];
+    pdl_enter();
+    kept_row_offsets(counts, E, C, off, warp_tot);
+    const unsigned rows = off[E], tasks = K / 16;    // a task is 16 codes
+    for (UnitWalk wk(blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8, (tasks + 31) / 32); wk.row < rows; wk.next()) {
+        const int e = expert_of_row(off, E, (int)wk.row);
+        const size_t row = (size_t)e * C + (wk.row - off[e]);
+        const unsigned c = wk.seg * 32 + (threadIdx.x & 31);
+        if (c >= tasks) continue;
+        const uint4 q = ld_stream_v4(x + row * tasks + c);
+        uint4 *o = out + (row * tasks + c) * 2;
+        o[0] = make_uint4(e4m3x2_to_f16x2(q.x), e4m3x2_to_f16x2(q.x >> 16), e4m3x2_to_f16x2(q.y),
+                          e4m3x2_to_f16x2(q.y >> 16));
+        o[1] = make_uint4(e4m3x2_to_f16x2(q.z), e4m3x2_to_f16x2(q.z >> 16), e4m3x2_to_f16x2(q.w),
+                          e4m3x2_to_f16x2(q.w >> 16));
+    }
+}
+
+bool encode_3d(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t inner, uint64_t rows, uint64_t e,
+               int elem_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {inner, rows, e};
+    const cuuint64_t strides[2] = {inner * elem_bytes, inner * rows * elem_bytes};
+    const cuuint32_t box[3] = {box_inner, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, type, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+long long kept_at_most(const Dims &d) {
+    return std::min<long long>((long long)d.T * d.k, (long long)d.E * d.C);
+}
+
+template <bool F8, int GS, bool GATE>
+int launch_one(const Dims &d, const W4Args &a, cudaStream_t st, const void *x, const float *x_scale,
+               const int32_t *counts, const void *w_q, const void *w_scale, void *y, void *workspace) {
+    const int n_tiles = (a.N + (GATE ? kTRows : 2 * kTRows) - 1) / (GATE ? kTRows : 2 * kTRows);
+    const long long tiles = (kept_at_most(d) / kTTok + d.E) * n_tiles;
+    if (tiles * a.nkb >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;    // blocks are counted in 32 bits
+    CUtensorMap map_w, map_x;
+    if (!encode_3d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_q, a.K / 2, a.M, a.E, 1, 64, kTRows,
+                   CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_3d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, F8 ? workspace : x, a.K, a.C, a.E, 2, 64, 16,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+        return MOE_ERR_CUDA;
+    unsigned *status = device_status_word();
+    if (status == nullptr) return MOE_ERR_CUDA;
+    static PerContext<int> smem_done;
+    if (!set_smem_once(smem_done, expert_w4_tiles_kernel<F8, GS, GATE>, (int)kTSmemBytes)) return MOE_ERR_CUDA;
+    if constexpr (F8) {
+        static PerContext<int> resident_cache;
+        const int resident = resident_blocks_cached(resident_cache, w4_rows_to_f16_kernel, 256);
+        const int grid = persistent_grid((kept_at_most(d) * ((a.K / 16 + 31) / 32) + 7) / 8, resident, d.max_blocks);
+        if (launch_pdl(w4_rows_to_f16_kernel, grid, 256, st, static_cast<const uint4 *>(x), counts,
+                       static_cast<uint4 *>(workspace), a.E, a.C, a.K) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    const int grid = persistent_grid(tiles, sm_count(), d.max_blocks);
+    if (launch_pdl_smem(expert_w4_tiles_kernel<F8, GS, GATE>, grid, kTThreads, kTSmemBytes, st, map_w, map_x, a, counts,
+                        static_cast<const uint16_t *>(w_scale), x_scale, static_cast<uint16_t *>(y), status) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+}
+
+template <bool F8, int GS, typename... A>
+int launch_act(const Dims &d, const W4Args &a, A... args) {
+    return a.M == 2 * a.N ? launch_one<F8, GS, true>(d, a, args...) : launch_one<F8, GS, false>(d, a, args...);
+}
+template <bool F8, typename... A>
+int launch_group(const Dims &d, const W4Args &a, A... args) {
+    if (a.group == 32) return launch_act<F8, 32>(d, a, args...);
+    if (a.group == 64) return launch_act<F8, 64>(d, a, args...);
+    return launch_act<F8, 128>(d, a, args...);
+}
+
+}  // namespace
+
+size_t w4_tiles_workspace_bytes(const Dims &d, const W4Args &a) {
+    return d.dtype == MOE_DTYPE_FP8_E4M3_B128 ? (size_t)a.E * a.C * a.K * 2 : 0;
+}
+
+int launch_w4_tiles(const Dims &d, const W4Args &a, cudaStream_t st, const void *x, const float *x_scale,
+                    const int32_t *counts, const void *w_q, const void *w_scale, void *y, void *workspace) {
+    if (d.dtype == MOE_DTYPE_FP8_E4M3_B128)
+        return launch_group<true>(d, a, st, x, x_scale, counts, w_q, w_scale, y, workspace);
+    return launch_group<false>(d, a, st, x, x_scale, counts, w_q, w_scale, y, workspace);
+}
+
+}  // namespace moe

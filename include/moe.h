@@ -439,7 +439,7 @@ size_t moe_expert_w4_workspace_bytes(const moe_problem *p, const moe_w4 *w);
  *   w_scale bf16 [E][M][K/group].
  * One row to many rows for an expert: for few rows the call is bound by
  * reading the weights of the experts that have any. counts is moe_route's.
- * x, w_q, y, workspace 16-byte aligned, w_scale 8; max_blocks caps the grid.
+ * x, w_q, w_scale, y and workspace 16-byte aligned; max_blocks caps the grid.
  * Launched as a programmatic dependent of the previous kernel. */
 int moe_expert_w4(const moe_problem *p, const moe_w4 *w, const void *x, const float *x_scale,
                   const int32_t *counts, const void *w_q, const void *w_scale, void *y,
