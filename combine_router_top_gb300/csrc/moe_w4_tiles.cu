@@ -14,9 +14,8 @@
 // A persistent grid, one CTA per SM, walks tiles of (expert, 2 x 128 matrix rows,
 // up to 64 rows of x): rows n .. n+127 of the gate and of the up matrix, or 256
 // rows of a matrix without the gate. In each CTA:
-//   warp 0      one lane issues the TMA loads of each block of 128 inputs: two
-//               weight boxes of 128 rows x 64 bytes, and x in boxes of 16 rows x
-//               64 inputs, into a ring of 5 stages;
+//   warp 0      one lane issues the TMA loads of x, 128 inputs of the tile's rows in
+//               two boxes, into a ring of 4;
 //   warps 1, 3  the MMAs of a tile's even and odd blocks, one elected lane each: per
 //               group, the steps of both halves into fresh accumulators. All 512 TMEM
 //               columns are held: for each half and parity 64 columns of accumulators
@@ -24,8 +23,8 @@
 //               and 64 of operand (128 inputs);
 //   warp 2      brings the group scales (and fp8 rows' block scales), 8 groups at a
 //               time, from HBM to a ring in shared memory;
-//   warps 4-19  four TMEM quadrants x two halves x even and odd blocks: turn codes into
-//               operands;
+//   warps 4-19  four TMEM quadrants x two halves x even and odd blocks: copy the codes
+//               of their 32 rows to rings of their own and turn them into operands;
 //   warps 20-27 four quadrants x two halves: add up the groups' sums, and write y.
 // Every mbarrier wait is bounded; one that gives up raises the status word and an
 // abort flag, the CTA drains what it has in flight, frees its TMEM and returns.
@@ -39,17 +38,28 @@ namespace {
 
 constexpr int kTRows = 128;                          // matrix rows of one half (TMEM lanes)
 constexpr int kTTok = 64;                            // rows of x to a tile, at most
-constexpr int kTStages = 5;
+constexpr int kTXStages = 4;                         // ring of x blocks
 constexpr int kTThreads = 896;                       // 28 warps of 72 registers
-constexpr uint32_t kTWBytes = kTRows * 64;           // codes of one half's block
+constexpr int kTWDepth = 4;                          // blocks of codes that a warp has in flight or at hand
+constexpr uint32_t kTWBytes = 32 * 64;               // codes of a warp's 32 rows of a block
 constexpr uint32_t kTXBytes = kTTok * 128;           // x of 64 inputs
-constexpr uint32_t kTStageBytes = 2 * kTWBytes + 2 * kTXBytes;
-constexpr int kTChunks = 4, kTChunk = 8;             // scale ring: 4 chunks of 8 groups
+constexpr int kTChunks = 3, kTChunk = 8;             // scale ring: 3 chunks of 8 groups
 constexpr int kTScalePad = kTRows + 8;               // stride of a group's 128 scales: 8 groups on 8 bank sets
-constexpr size_t kTExBytes = (size_t)kTTok * kTRows * 4;
+constexpr size_t kTExBytes = (size_t)16 * kTRows * 4;
 constexpr size_t kTScaleBytes = (size_t)kTChunks * 2 * kTChunk * kTScalePad * 2;
 constexpr size_t kTXsBytes = (size_t)kTChunks * kTChunk * kTTok * 4;
-constexpr size_t kTSmemBytes = 1024 + kTStages * (size_t)kTStageBytes + kTExBytes + kTScaleBytes + kTXsBytes;
+constexpr size_t kTSmemBytes = 1024 + kTXStages * 2 * (size_t)kTXBytes + 16 * kTWDepth * (size_t)kTWBytes + kTExBytes +
+                               kTScaleBytes + kTXsBytes;
+
+// 16 bytes of global memory to shared memory, tracked by this thread's groups.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // D[128 x N] (+)= A (TMEM) B: one step of 16 inputs.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -74,10 +84,32 @@ struct W4Tiles {
     }
 };
 
+// x of [E][C][K] in boxes of 16, 32, 48 and 64 rows x 64 inputs.
+struct W4Maps {
+    CUtensorMap x[4];
+};
+
 template <int N>
 struct Int {
     static constexpr int value = N;
 };
+
+// acc[i] += v[i] * scale (times the fp8 row's own scale), 16 columns.
+template <bool F8>
+__device__ __forceinline__ void add16(float *acc, const uint32_t *v, float ws, const float *xs) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        float4 f = make_float4(ws, ws, ws, ws);
+        if constexpr (F8) {
+            f = *reinterpret_cast<const float4 *>(xs + i);
+            f = make_float4(f.x * ws, f.y * ws, f.z * ws, f.w * ws);
+        }
+        acc[i] = fmaf(__uint_as_float(v[i]), f.x, acc[i]);
+        acc[i + 1] = fmaf(__uint_as_float(v[i + 1]), f.y, acc[i + 1]);
+        acc[i + 2] = fmaf(__uint_as_float(v[i + 2]), f.z, acc[i + 2]);
+        acc[i + 3] = fmaf(__uint_as_float(v[i + 3]), f.w, acc[i + 3]);
+    }
+}
 
 // One warp brings the scales of groups c .. c+7 of the two halves' 128 matrix rows
 // (valid0 and valid1 of them in the matrix) to to[half][group][row], W bytes of a
@@ -133,18 +165,19 @@ __device__ __forceinline__ bool scale_chunk(const uint16_t *__restrict__ src0, c
 
 template <bool F8, int GS, bool GATE>
 __global__ void __launch_bounds__(kTThreads, 1)
-expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, W4Args a,
+expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint8_t *__restrict__ w_q,
                        const int32_t *__restrict__ counts, const uint16_t *__restrict__ w_scale,
                        const float *__restrict__ x_scale, uint16_t *__restrict__ y, unsigned *status) {
     constexpr int GPB = 128 / GS;                    // groups to a block of 128 inputs
     constexpr int kOut = GATE ? kTRows : 2 * kTRows; // outputs of a tile
     extern __shared__ uint8_t w4_smem_raw[];
-    __shared__ __align__(8) uint64_t full[kTStages], empty[kTStages];
+    constexpr int SX = kTXStages;
+    __shared__ __align__(8) uint64_t x_full[SX], x_empty[SX];
     __shared__ __align__(8) uint64_t a_full[2], a_free[2];                // operands of even and odd blocks
     __shared__ __align__(8) uint64_t d_full[4], d_free[4];                // accumulators: [2 (odd block) + slot]
     __shared__ __align__(8) uint64_t sc_full[kTChunks], sc_empty[kTChunks];
     __shared__ __align__(8) uint64_t ex_full[4], ex_free[4];           // sums traded between the halves
-    __shared__ __align__(8) uint64_t s_drain;
+    __shared__ __align__(8) uint64_t s_drain[2];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     __shared__ int s_first[kMaxExperts + 1];
@@ -152,16 +185,17 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t smem0 = (smem_u32(w4_smem_raw) + 1023u) & ~1023u;
     uint8_t *const base = w4_smem_raw + (smem0 - smem_u32(w4_smem_raw));
-    float *const ex = reinterpret_cast<float *>(base + kTStages * kTStageBytes);
-    uint16_t *const sc = reinterpret_cast<uint16_t *>(base + kTStages * kTStageBytes + kTExBytes);
-    float *const xs = reinterpret_cast<float *>(base + kTStages * kTStageBytes + kTExBytes + kTScaleBytes);
+    uint8_t *const codes = base + SX * 2 * kTXBytes;
+    float *const ex = reinterpret_cast<float *>(codes + 16 * kTWDepth * kTWBytes);
+    uint16_t *const sc = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(ex) + kTExBytes);
+    float *const xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(sc) + kTScaleBytes);   // fp8 rows only
     const int nkb = a.nkb, groups = nkb * GPB;
     const int n_tiles = (a.N + kOut - 1) / kOut;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kTStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+        for (int i = 0; i < SX; ++i) {
+            mbar_init(&x_full[i], 1);
+            mbar_init(&x_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&a_full[i], 8);
@@ -179,7 +213,8 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             mbar_init(&ex_full[i], 2);
             mbar_init(&ex_free[i], 2);
         }
-        mbar_init(&s_drain, 1);
+        mbar_init(&s_drain[0], 1);
+        mbar_init(&s_drain[1], 1);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -220,42 +255,33 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     tc_fence_after();
     const uint32_t tmem = s_tmem;                    // half h, odd block or even p: accumulators at 128 h + 64 p, operand 256 on
 
-    uint32_t issued = 0;                             // stages loaded, for the drain
+    uint32_t x_issued = 0;                           // blocks of x loaded, for the drain
     // setmaxnreg is one instruction of a whole warpgroup (warps 0-3, 4-7, ...). 896 threads of 72 registers are
     // 64512; 20 warps give up 16 of theirs for the 8 that hold 64 sums: 20 x 32 x 56 + 8 x 32 x 112 = 64512
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             const bool elected = elect_one();
-            uint32_t s = 0, phase = 0;               // stage and its use, odd or even
+            uint32_t s = 0, phase = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 int e, nt, tt;
                 tiles.decode(t, e, nt, tt);
                 const int rows = min(min(__ldg(counts + e), a.C) - tt * kTTok, kTTok);
-                const int boxes = __shfl_sync(kFull, (rows + 15) / 16, 0);
-                const int ez = __shfl_sync(kFull, e, 0), row_w = __shfl_sync(kFull, nt * kOut, 0);
-                const int row_x = __shfl_sync(kFull, tt * kTTok, 0);
+                const int n16 = __shfl_sync(kFull, (rows + 15) / 16, 0);
+                const int ez = __shfl_sync(kFull, e, 0), row_x = __shfl_sync(kFull, tt * kTTok, 0);
+                const CUtensorMap *map = &maps.x[n16 - 1];
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (issued >= kTStages && !(ok = warp_wait(smem_u32(&empty[0]) + 8 * s, phase ^ 1u, &s_abort)))
-                        break;
+                    if (x_issued >= SX && !(ok = warp_wait(smem_u32(&x_empty[0]) + 8 * s, phase ^ 1u, &s_abort))) break;
                     if (elected) {
-                        const uint32_t at = smem0 + s * kTStageBytes, bar = smem_u32(&full[s]);
-                        mbar_expect_tx(&full[s], 2 * kTWBytes + boxes * 4096);
-                        tma_load_3d(at, &map_w, bar, kb * 64, row_w, ez);
-                        tma_load_3d(at + kTWBytes, &map_w, bar, kb * 64, row_w + (GATE ? a.N : kTRows), ez);
-#pragma unroll
-                        for (int i = 0; i < kTTok / 16; ++i) {
-                            if (i < boxes) {
-                                tma_load_3d(at + 2 * kTWBytes + i * 2048, &map_x, bar, kb * 128, row_x + i * 16, ez);
-                                tma_load_3d(at + 2 * kTWBytes + kTXBytes + i * 2048, &map_x, bar, kb * 128 + 64,
-                                            row_x + i * 16, ez);
-                            }
-                        }
+                        const uint32_t at = smem0 + s * 2 * kTXBytes, bar = smem_u32(&x_full[0]) + 8 * s;
+                        mbar_expect_tx(&x_full[s], n16 * 4096);
+                        tma_load_3d(at, map, bar, kb * 128, row_x, ez);
+                        tma_load_3d(at + kTXBytes, map, bar, kb * 128 + 64, row_x, ez);
                     }
                     __syncwarp();
-                    ++issued;
-                    if (++s == kTStages) s = 0, phase ^= 1u;
+                    ++x_issued;
+                    if (++s == SX) s = 0, phase ^= 1u;
                 }
             }
         } else if (warp == 1 || warp == 3) {
@@ -270,7 +296,7 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             const bool elected = elect_one();
             const uint32_t b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[par]);
             const uint32_t b_dfull = smem_u32(&d_full[2 * par]), b_dfree = smem_u32(&d_free[2 * par]);
-            uint32_t s0 = 0;                         // the tile's first stage
+            uint32_t n0 = 0;                         // blocks before the tile: block n has x stage n % SX
             uint32_t a_phase = 0, d_phase = 0;       // odd or even use of the operand, of the slots (bits)
             bool ok = true;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
@@ -285,11 +311,12 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
                 // a slot of 64 columns takes the place of both slots of 32
                 if (!slots) ok = warp_wait(b_dfree + 8, (d_phase >> 1 & 1u) ^ 1u, &s_abort);
                 uint32_t slot = 0;
-                uint32_t s = s0 + par >= kTStages ? s0 + par - kTStages : s0 + par;
+                static_assert(SX == 4, "a block's x stage and its use are bits of its number");
                 for (int kb = (int)par; kb < nkb && ok; kb += 2) {
-                    const uint64_t bx = umma_desc_sw128(smem0 + s * kTStageBytes + 2 * kTWBytes);
-                    // the warps that made the operand have seen the stage's loads complete
-                    ok = warp_wait(b_afull, a_phase, &s_abort);
+                    const uint32_t s = (n0 + kb) & 3u;
+                    const uint64_t bx = umma_desc_sw128(smem0 + s * 2 * kTXBytes);
+                    ok = warp_wait(smem_u32(&x_full[0]) + 8 * s, (n0 + kb) >> 2 & 1u, &s_abort) &&
+                         warp_wait(b_afull, a_phase, &s_abort);
                     a_phase ^= 1u;
 #pragma unroll
                     for (int q = 0; q < GPB; ++q) {
@@ -308,18 +335,16 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
                                 }
                             }
                             mma_commit(b_dfull + 8 * slot);
-                            if (q == GPB - 1) {      // the operand and the stage have been read
+                            if (q == GPB - 1) {      // the operand and x have been read
                                 mma_commit(b_afree);
-                                mma_commit(smem_u32(&empty[0]) + 8 * s);
+                                mma_commit(smem_u32(&x_empty[0]) + 8 * s);
                             }
                         }
                         __syncwarp();
                         slot ^= slots;
                     }
-                    s += 2;
-                    if (s >= kTStages) s -= kTStages;
                 }
-                s0 = (s0 + nkb) % kTStages;
+                n0 += nkb;
             }
         } else {
             constexpr int KPC = kTChunk / GPB;       // blocks of 128 inputs to a chunk
@@ -370,24 +395,50 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     } else if (warp < 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int quad = warp & 3, h = ((warp - 4) >> 2) & 1, par = (warp - 4) >> 3;
-        const int row = quad * 32 + lane;            // TMEM lane: row of this half
         const uint32_t op0 = tmem + ((uint32_t)(quad * 32) << 16) + 256 + 128 * h + 64 * par;
-        // 64 bytes of this row, 64-byte swizzled: chunk t of row r stands at t ^ (r / 2 % 4)
-        const uint8_t *const src0 = base + h * kTWBytes + row * 64;
-        const int swz = ((row >> 1) & 3) << 4;
-        const uint32_t b_full = smem_u32(&full[0]), b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[par]);
+        const uint32_t b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[par]);
+        // The codes of this warp's 32 rows come to a ring of the warp's own, by its own asynchronous copies: no other
+        // warp waits for them. Lane l copies chunk l % 4 (16 bytes) of rows l / 4 + 8 i; chunk t of row r stands at
+        // t ^ (r / 2 % 4), so that neither the copies nor the reads of a row a lane meet in a bank.
+        uint8_t *const ring = codes + (warp - 4) * kTWDepth * kTWBytes;
+        const uint32_t dst = smem_u32(ring) + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+        const uint8_t *const src = ring + lane * 64;
+        const int swz = ((lane >> 1) & 3) << 4;
         const int mine = (total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1;       // tiles of this CTA
-        // stage and its use, odd or even, of this warp's next block; every other block of a tile
-        uint32_t s = par, phase = 0, a_phase = 0;
-        int kb = par;
-        for (int left = kb < nkb ? mine : 0; left > 0;) {
-            if (!warp_wait(b_full + 8 * s, phase, &s_abort)) break;
+        const uint32_t blocks = (uint32_t)mine * (uint32_t)((nkb - par + 1) / 2);  // every other block of each
+        const uint8_t *from = nullptr;               // the tile's rows, at this lane's first chunk of the next block
+        uint32_t off[4] = {};                        // and the offsets of its four rows
+        int it = (int)blockIdx.x - (int)gridDim.x, ikb = nkb;
+        const auto fetch = [&](uint32_t n) {         // block n of this warp's, in turn
+            if (n < blocks) {
+                if (ikb >= nkb) {
+                    int e, nt, tt;
+                    tiles.decode(it += gridDim.x, e, nt, tt);
+                    const int n0 = GATE ? nt * kOut : nt * kOut + h * kTRows;
+                    from = w_q + ((size_t)e * a.M + (GATE ? h * a.N : 0)) * (a.K / 2) + 16 * (lane & 3) + 64 * par;
+                    const int last = a.N - 1;        // rows past the matrix are read as its last: their scales are 0
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) off[i] = (uint32_t)min(n0 + quad * 32 + (lane >> 2) + 8 * i, last) * (a.K / 2);
+                    ikb = par;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cp_async16(dst + (n % kTWDepth) * kTWBytes + i * 512, from + off[i]);
+                from += 128;
+                ikb += 2;
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int n = 0; n < kTWDepth - 1; ++n) fetch(n);
+        for (uint32_t n = 0; n < blocks; ++n) {
+            cp_async_wait<kTWDepth - 2>();
+            __syncwarp();                            // every lane's copies of block n are there, and block n - 1 is read
+            fetch(n + kTWDepth - 1);
             uint4 q[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                q[i] = *reinterpret_cast<const uint4 *>(src0 + s * kTStageBytes + ((i << 4) ^ swz));
-            if (!warp_wait(b_afree, a_phase ^ 1u, &s_abort)) break;
-            a_phase ^= 1u;
+                q[i] = *reinterpret_cast<const uint4 *>(src + (n % kTWDepth) * kTWBytes + ((i << 4) ^ swz));
+            if (!warp_wait(b_afree, (n & 1u) ^ 1u, &s_abort)) break;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -401,16 +452,8 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_at(b_afull);
-            // two blocks on; over the end of a tile, to its next one's first of this parity
-            uint32_t step = 2;
-            if ((kb += 2) >= nkb) {
-                step = (uint32_t)(nkb - (kb - 2) + par);
-                kb = par;
-                --left;
-            }
-            s += step;
-            if (s >= kTStages) s -= kTStages, phase ^= 1u;
         }
+        cp_async_wait<0>();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         const int quad = warp & 3, h = (warp - 20) >> 2;
@@ -427,90 +470,95 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             float acc[kTTok];
 #pragma unroll
             for (int i = 0; i < kTTok; ++i) acc[i] = 0.0f;
-            const uint32_t slots = rows <= 32 ? 1u : 0u;
-            uint32_t slot = 0;                       // bit 2 p of it: even (p = 0) or odd block's next slot
-            for (int c = 0; c < groups && ok; c += kTChunk, ++cg) {
-                const uint32_t buf = cg % kTChunks;
-                ok = warp_wait(smem_u32(&sc_full[buf]), (cg / kTChunks) & 1, &s_abort);
-                const uint16_t *scr = sc + ((buf * 2 + h) * kTChunk) * kTScalePad + row;
-                const float *xr = xs + buf * kTChunk * kTTok;
-                const int n = min(kTChunk, groups - c);
-                // the groups of two blocks in turn, as their MMAs run side by side
-                for (int i = 0; i < kTChunk && ok; ++i) {
-                    const int p = i & 1, group = GPB == 1 ? i : GPB == 2 ? (i & 4) | p << 1 | (i >> 1 & 1) : p << 2 | i >> 1;
-                    if (group >= n) continue;
-                    const uint32_t sl = slot >> p & 1u, which = 2 * p + sl;
-                    ok = warp_wait(b_dfull + 8 * which, d_phase >> which & 1u, &s_abort);
-                    if (!ok) break;
-                    d_phase ^= 1u << which;
-                    slot ^= slots << p;
-                    tc_fence_after();
-                    const float ws = __uint_as_float((uint32_t)scr[group * kTScalePad] << 16) * kW4Unit<F8>;
-                    const float4 *xi = reinterpret_cast<const float4 *>(xr + group / GPB * kTTok);
-                    const uint32_t d = d0 + 64 * p + 32 * sl;
+            // the tile's groups into acc: wide for over 32 rows of x, whose accumulators have one slot, not two
+            const auto add_up = [&](auto wide) {
+                constexpr bool kWide = decltype(wide)::value != 0;
+                for (int c = 0; c < groups; c += kTChunk, ++cg) {
+                    const uint32_t buf = cg % kTChunks;
+                    if (!warp_wait(smem_u32(&sc_full[buf]), (cg / kTChunks) & 1, &s_abort)) return false;
+                    const uint16_t *scr = sc + ((buf * 2 + h) * kTChunk) * kTScalePad + row;
+                    const float *xr = xs + buf * kTChunk * kTTok;
+                    const int n = min(kTChunk, groups - c);
 #pragma unroll
-                    for (int b = 0; b < kTTok; b += 32) {              // up to 32 columns at a time: registers
-                        if (b < rows) {
-                            uint32_t v[32];
-                            tmem_ld16(d + b, v);
-                            if (b + 16 < rows) tmem_ld16(d + b + 16, v + 16);
-                            tmem_ld_wait();
-                            if (b + 32 >= rows) {    // the last of them is read
+                    for (int i = 0; i < kTChunk; ++i) {
+                        // the groups of an even and an odd block in turn, as their MMAs run side by side; a chunk has
+                        // four of each, so that each chunk begins with slot 0
+                        const int p = i & 1, group = GPB == 1   ? i
+                                                     : GPB == 2 ? (i & 4) | p << 1 | (i >> 1 & 1)
+                                                                : p << 2 | i >> 1;
+                        const int slot = kWide ? 0 : i >> 1 & 1, which = 2 * p + slot;
+                        if (group < n) {
+                            if (!warp_wait(b_dfull + 8 * which, d_phase >> which & 1u, &s_abort)) return false;
+                            d_phase ^= 1u << which;
+                            tc_fence_after();
+                            const float ws = __uint_as_float((uint32_t)scr[group * kTScalePad] << 16);
+                            const float *xg = xr + group / GPB * kTTok;
+                            const uint32_t d = d0 + 64 * p + 32 * slot;
+                            if constexpr (kWide) {   // 16 columns at a time: registers
+#pragma unroll
+                                for (int b = 0; b < kTTok; b += 16) {
+                                    if (b < 48 || rows > 48) {
+                                        uint32_t v[16];
+                                        tmem_ld16(d + b, v);
+                                        tmem_ld_wait();
+                                        add16<F8>(acc + b, v, ws, xg + b);
+                                    }
+                                }
                                 tc_fence_before();
                                 __syncwarp();
                                 if (lane == 0) mbar_arrive_at(b_dfree + 8 * which);
-                            }
-#pragma unroll
-                            for (int u = 0; u < 32; u += 4) {
-                                if (u < 16 || b + 16 < rows) {
-                                    float4 f = make_float4(ws, ws, ws, ws);
-                                    if constexpr (F8) {
-                                        f = xi[(b + u) / 4];
-                                        f = make_float4(f.x * ws, f.y * ws, f.z * ws, f.w * ws);
-                                    }
-                                    acc[b + u] = fmaf(__uint_as_float(v[u]), f.x, acc[b + u]);
-                                    acc[b + u + 1] = fmaf(__uint_as_float(v[u + 1]), f.y, acc[b + u + 1]);
-                                    acc[b + u + 2] = fmaf(__uint_as_float(v[u + 2]), f.z, acc[b + u + 2]);
-                                    acc[b + u + 3] = fmaf(__uint_as_float(v[u + 3]), f.w, acc[b + u + 3]);
-                                }
+                            } else {
+                                uint32_t v[32];
+                                tmem_ld16(d, v);
+                                if (rows > 16) tmem_ld16(d + 16, v + 16);
+                                tmem_ld_wait();
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive_at(b_dfree + 8 * which);
+                                add16<F8>(acc, v, ws, xg);
+                                if (rows > 16) add16<F8>(acc + 16, v + 16, ws, xg + 16);
                             }
                         }
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sc_empty[buf]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sc_empty[buf]);
-            }
+                return true;
+            };
+            ok = rows <= 32 ? add_up(Int<0>()) : add_up(Int<1>());
+#pragma unroll
+            for (int i = 0; i < kTTok; ++i) acc[i] *= kW4Unit<F8>;
             if (!ok) break;
             uint16_t *out = y + ((size_t)e * a.C + tt * kTTok) * a.N;
             if constexpr (GATE) {
-                // the halves' warps of the same rows trade: each gets the other's sums of half of the columns,
-                // 8 x 4 of the 64, and finishes those
+                // the halves' warps of the same rows trade, 16 columns at a time: each gets the other's sums of 8
+                // of them, and finishes those
                 const int n = nt * kOut + row;
-                if (n_ex > 0 && !(ok = warp_wait(smem_u32(&ex_free[quad]), (n_ex + 1) & 1, &s_abort))) break;
-#pragma unroll
-                for (int i = 0; i < kTTok; ++i)
-                    if (((i >> 3) & 1) != h && i < rows) ex[i * kTRows + row] = acc[i];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ex_full[quad]);
-                if (!(ok = warp_wait(smem_u32(&ex_full[quad]), n_ex & 1, &s_abort))) break;
 #pragma unroll
                 for (int b = 0; b < kTTok; b += 16) {
-                    if (b + 8 * h < rows) {
-                        float o[8];
+                    if (b >= rows || !ok) break;
+                    ok = warp_wait(smem_u32(&ex_free[quad]), (n_ex & 1u) ^ 1u, &s_abort);
+                    if (!ok) break;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float other = ex[(b + 8 * h + i) * kTRows + row];
-                            const float mine = h == 0 ? acc[b + i] : acc[b + 8 + i];
-                            o[i] = h == 0 ? silu(mine) * other : silu(other) * mine;
-                        }
+                    for (int i = 0; i < 8; ++i) ex[(8 * (1 - h) + i) * kTRows + row] = h == 0 ? acc[b + 8 + i] : acc[b + i];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ex_full[quad]);
+                    ok = warp_wait(smem_u32(&ex_full[quad]), n_ex & 1u, &s_abort);
+                    if (!ok) break;
+                    float o[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (b + 8 * h + i < rows && n < a.N) put_bf16(out + (size_t)(b + 8 * h + i) * a.N + n, o[i]);
+                    for (int i = 0; i < 8; ++i) {
+                        const float other = ex[(8 * h + i) * kTRows + row];
+                        o[i] = h == 0 ? silu(acc[b + i]) * other : silu(other) * acc[b + 8 + i];
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ex_free[quad]);
+                    ++n_ex;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (b + 8 * h + i < rows && n < a.N) put_bf16(out + (size_t)(b + 8 * h + i) * a.N + n, o[i]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ex_free[quad]);
-                ++n_ex;
+                if (!ok) break;
             } else {
                 const int n = nt * kOut + h * kTRows + row;
 #pragma unroll
@@ -528,12 +576,12 @@ expert_w4_tiles_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         volatile int no_abort = 0;
         if (warp == 0 && lane == 0) {
             atomicOr(status, kStatusWaitGaveUp);
-            for (uint32_t g = (issued > kTStages ? issued - kTStages : 0); g < issued; ++g)
-                gemm_wait(smem_u32(&full[g % kTStages]), (g / kTStages) & 1, &no_abort);
+            for (uint32_t g = (x_issued > SX ? x_issued - SX : 0); g < x_issued; ++g)
+                gemm_wait(smem_u32(&x_full[g % SX]), (g / SX) & 1, &no_abort);
         }
-        if (warp == 1 && elect_one()) {              // the lane that issued the MMAs
-            mma_commit(smem_u32(&s_drain));
-            gemm_wait(smem_u32(&s_drain), 0, &no_abort);
+        if ((warp == 1 || warp == 3) && elect_one()) {   // the lanes that issued the MMAs
+            mma_commit(smem_u32(&s_drain[warp >> 1]));
+            gemm_wait(smem_u32(&s_drain[warp >> 1]), 0, &no_abort);
         }
         __syncthreads();
     }
@@ -566,16 +614,17 @@ w4_rows_to_f16_kernel(const uint4 *__restrict__ x, const int32_t *__restrict__ c
     }
 }
 
-bool encode_3d(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t inner, uint64_t rows, uint64_t e,
-               int elem_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+// x [E][rows][K] of 16-bit numbers in boxes of box_rows x 64, 128-byte swizzled; rows past the end read as zero.
+bool encode_3d(CUtensorMap *map, const void *base, uint64_t K, uint64_t rows, uint64_t E, uint32_t box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (fn == nullptr) return false;
-    const cuuint64_t dims[3] = {inner, rows, e};
-    const cuuint64_t strides[2] = {inner * elem_bytes, inner * rows * elem_bytes};
-    const cuuint32_t box[3] = {box_inner, box_rows, 1};
+    const cuuint64_t dims[3] = {K, rows, E};
+    const cuuint64_t strides[2] = {K * 2, K * rows * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, type, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 long long kept_at_most(const Dims &d) {
@@ -588,12 +637,9 @@ int launch_one(const Dims &d, const W4Args &a, cudaStream_t st, const void *x, c
     const int n_tiles = (a.N + (GATE ? kTRows : 2 * kTRows) - 1) / (GATE ? kTRows : 2 * kTRows);
     const long long tiles = (kept_at_most(d) / kTTok + d.E) * n_tiles;
     if (tiles * a.nkb >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;    // blocks are counted in 32 bits
-    CUtensorMap map_w, map_x;
-    if (!encode_3d(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_q, a.K / 2, a.M, a.E, 1, 64, kTRows,
-                   CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode_3d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT16, F8 ? workspace : x, a.K, a.C, a.E, 2, 64, 16,
-                   CU_TENSOR_MAP_SWIZZLE_128B))
-        return MOE_ERR_CUDA;
+    W4Maps maps;
+    for (int i = 0; i < 4; ++i)
+        if (!encode_3d(&maps.x[i], F8 ? workspace : x, a.K, a.C, a.E, 16 * (i + 1))) return MOE_ERR_CUDA;
     unsigned *status = device_status_word();
     if (status == nullptr) return MOE_ERR_CUDA;
     static PerContext<int> smem_done;
@@ -607,7 +653,8 @@ int launch_one(const Dims &d, const W4Args &a, cudaStream_t st, const void *x, c
             return MOE_ERR_CUDA;
     }
     const int grid = persistent_grid(tiles, sm_count(), d.max_blocks);
-    if (launch_pdl_smem(expert_w4_tiles_kernel<F8, GS, GATE>, grid, kTThreads, kTSmemBytes, st, map_w, map_x, a, counts,
+    if (launch_pdl_smem(expert_w4_tiles_kernel<F8, GS, GATE>, grid, kTThreads, kTSmemBytes, st, maps, a,
+                        static_cast<const uint8_t *>(w_q), counts,
                         static_cast<const uint16_t *>(w_scale), x_scale, static_cast<uint16_t *>(y), status) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
