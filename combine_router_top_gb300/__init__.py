@@ -154,10 +154,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream):
-    import torch
+    global _raw_stream
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        import torch
+        if _raw_stream is None:
+            # the current stream's handle without a Stream object around it: 0.3 instead of 3 us a call
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

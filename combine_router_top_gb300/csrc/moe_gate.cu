@@ -56,18 +56,37 @@ __device__ __forceinline__ void unpack16(uint4 q, float (&f)[8]) {
     }
 }
 
+__device__ __forceinline__ uint4 pack16(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack16(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
 // Not masked: above the mask value and not NaN.
 __device__ __forceinline__ bool open_logit(float l) { return l > kMaskLogit; }
 
-// 1 / (1 + exp(-l)): expf and one IEEE division, 1 at +inf, 0 once exp(-l) overflows.
-__device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l))); }
+// 1 / (1 + exp(-l)): expf and the correctly rounded reciprocal, 1 at +inf, 0 once exp(-l) overflows.
+__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
+// logit_key of a number (no NaN) in three instructions: -0 becomes +0 by adding 0.
+__device__ __forceinline__ uint32_t number_key(float f) {
+    const uint32_t u = __float_as_uint(__fadd_rn(f, 0.0f));
+    return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
+}
 // exp(l - top), 1 where l is the top (also where both are +inf).
 __device__ __forceinline__ float exp_below(float l, float top) { return l == top ? 1.0f : expf(__fsub_rn(l, top)); }
 
-// Sum of x over the warp, fp32, every lane the same value.
-__device__ __forceinline__ float warp_sum_f(float x) {
+// Sum and maximum over LP neighbouring lanes, every lane the same value.
+template <int LP>
+__device__ __forceinline__ float lanes_sum(float x) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, o));
+    for (int o = LP / 2; o > 0; o >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, o));
+    return x;
+}
+template <int LP>
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+    for (int o = LP / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
     return x;
 }
 
@@ -113,7 +132,7 @@ __device__ __forceinline__ void warp_gate(const T *__restrict__ row, const float
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (open_logit(l[i])) m = max(m, logit_key(l[i]));
+            if (open_logit(l[i])) m = max(m, number_key(l[i]));
         m = __reduce_max_sync(kFull, m);
         top = m == 0 ? 0.0f : key_logit(m);
         float hi = 0.0f, lo = 0.0f;
@@ -134,17 +153,31 @@ __device__ __forceinline__ void warp_gate(const T *__restrict__ row, const float
     }
 
     uint32_t key[V];
+    if (bias != nullptr) {
+        float b[V];
+        if (V % 4 == 0 && n == V && e0 % 4 == 0 && (reinterpret_cast<uintptr_t>(bias) & 15) == 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float f = l[i];
-        bool open = open_logit(f);
-        if (bias != nullptr && i < n) {
-            const float b = __ldg(bias + e0 + i);
-            const float s = a.sigmoid ? sigmoid(f) : __fdiv_rn(exp_below(f, top), sum);
-            open = open && b > -INFINITY;
-            f = __fadd_rn(s, b);
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(bias + e0) + i);
+                b[4 * i] = f.x;
+                b[4 * i + 1] = f.y;
+                b[4 * i + 2] = f.z;
+                b[4 * i + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) b[i] = i < n ? __ldg(bias + e0 + i) : 0.0f;
         }
-        key[i] = i >= n ? kTaken : open ? logit_key(f) : kMasked;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float s = a.sigmoid ? sigmoid(l[i]) : __fdiv_rn(exp_below(l[i], top), sum);
+            const bool open = open_logit(l[i]) && b[i] > -INFINITY;
+            key[i] = i >= n ? kTaken : open ? number_key(__fadd_rn(s, b[i])) : kMasked;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            key[i] = i >= n ? kTaken : open_logit(l[i]) ? number_key(l[i]) : kMasked;
     }
 
     if (a.G > 1) {
@@ -184,25 +217,31 @@ __device__ __forceinline__ void warp_gate(const T *__restrict__ row, const float
         }
     }
 
-    uint32_t my_key = 0;
+    // k rounds. A lane's best remaining key changes only when the lane wins, and which of its experts has it is
+    // looked for by the winner alone: the lowest of its tied ones, in the lowest tied lane.
+    uint32_t my_key = 0, best = 0;
     my_e = 0;
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0;
-        int bi = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                bi = i;
-            }
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    for (int j = 0; j < a.k; ++j) {
         const uint32_t m = __reduce_max_sync(kFull, best);             // >= kMasked: k <= E
         const int wl = __ffs(__ballot_sync(kFull, best == m)) - 1;
-        const int e = __shfl_sync(kFull, e0 + bi, wl);
+        int bi = 0;
         if (lane == wl) {
+            best = 0;
+            bool found = false;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i == bi) key[i] = kTaken;
+            for (int i = 0; i < V; ++i) {
+                const bool hit = !found && key[i] == m;
+                if (hit) {
+                    bi = i;
+                    key[i] = kTaken;
+                }
+                found |= hit;
+                best = max(best, key[i]);
+            }
         }
+        const int e = __shfl_sync(kFull, e0 + bi, wl);
         if (lane == j) {
             my_key = m;
             my_e = e;
@@ -217,7 +256,7 @@ __device__ __forceinline__ void warp_gate(const T *__restrict__ row, const float
         const float most = key_logit(m);                               // the largest chosen logit
         // below -30 a sigmoid is exp(l) to the last bit, so the quotients are a softmax's, which cannot underflow
         if (ok) s = a.sigmoid && most > -30.0f ? sigmoid(f) : exp_below(f, most);
-        const float total = warp_sum_f(s);                             // 0 only where nothing was chosen
+        const float total = lanes_sum<32>(s);                             // 0 only where nothing was chosen
         s = ok ? __fdiv_rn(s, total) : 0.0f;
     } else if (ok) {
         s = a.sigmoid ? sigmoid(f) : __fdiv_rn(exp_below(f, top), sum);
@@ -284,20 +323,111 @@ gate_kernel(const T *__restrict__ logits, const float *__restrict__ bias, GateAr
 
 // ---- gradient -----------------------------------------------------------------
 
-// One warp per token. Lanes j < k form the chosen experts' gradients; the row is
-// written whole first (zeros, or -a s_e dot for a softmax over all experts), the
-// chosen places after it by the same warp. Bound by the T*E elements written
-// (and, for a softmax over all experts, read).
-template <typename T, bool DENSE>
+// LP lanes to a token, NV 16-byte words of its row to a lane. The lanes form the
+// chosen experts' gradients between them, then write the row whole (zeros, or
+// -a s_e dot for a softmax over all experts) and the chosen places after it, within
+// the same warp. Bound by the T*E elements written (and, for a softmax over all
+// experts, read, which stay in registers from the sum to the product).
+template <typename T, bool DENSE, int LP, int NV>
 __global__ void __launch_bounds__(256)
 gate_backward_kernel(const T *__restrict__ logits, const int32_t *__restrict__ topk_idx,
                      const float *__restrict__ topk_w, const float *__restrict__ d_topk_w, T *__restrict__ d_logits,
                      int T_, int E, int k, int sigm, int renorm, float scale) {
+    constexpr int kVec = 16 / (int)sizeof(T), kTokens = 256 / LP, kPer = LP < kMaxTopK ? kMaxTopK / LP : 1;
+    pdl_enter();
+    const int sub = threadIdx.x % LP;
+    const float inv = __fdiv_rn(1.0f, scale);
+    const int words = E / kVec;
+    for (int t0 = blockIdx.x * kTokens; t0 < T_; t0 += gridDim.x * kTokens) {
+        const int t = t0 + threadIdx.x / LP;
+        const bool live = t < T_;                                      // lanes past the end go through the motions
+        const T *row = logits + (size_t)t * E;
+        T *out = d_logits + (size_t)t * E;
+        uint4 word[NV];
+        if constexpr (DENSE) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (live && v * LP + sub < words) word[v] = ld_stream_v4(reinterpret_cast<const uint4 *>(row) + v * LP + sub);
+        }
+        int e[kPer];
+        float w[kPer], gw[kPer], f[kPer], part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int j = i * LP + sub;
+            e[i] = -1;
+            w[i] = gw[i] = f[i] = 0.0f;
+            if (live && j < k) {
+                e[i] = __ldg(topk_idx + (size_t)t * k + j);
+                w[i] = __ldg(topk_w + (size_t)t * k + j);
+                gw[i] = __ldg(d_topk_w + (size_t)t * k + j);
+                if ((unsigned)e[i] >= (unsigned)E) e[i] = -1;
+                if (e[i] >= 0 && sigm) f[i] = to_f32(row[e[i]]);
+                if (e[i] < 0 || w[i] == 0.0f) w[i] = gw[i] = 0.0f;     // no pair: whatever d_topk_w holds
+            }
+            part = __fmaf_rn(w[i], gw[i], part);
+        }
+        const float dot = (DENSE || renorm) ? __fmul_rn(lanes_sum<LP>(part), inv) : 0.0f;
+        if constexpr (DENSE) {
+            float top = -INFINITY, total = 0.0f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (live && v * LP + sub < words) {
+                    float x[kVec];
+                    unpack16(word[v], x);
+#pragma unroll
+                    for (int q = 0; q < kVec; ++q) top = fmaxf(top, x[q]);         // NaN stays out
+                }
+            }
+            top = lanes_max<LP>(top);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (live && v * LP + sub < words) {
+                    float x[kVec];
+                    unpack16(word[v], x);
+#pragma unroll
+                    for (int q = 0; q < kVec; ++q)
+                        if (open_logit(x[q])) total = __fadd_rn(total, exp_below(x[q], top));
+                }
+            }
+            total = lanes_sum<LP>(total);
+            const float c = total > 0.0f ? __fdiv_rn(-__fmul_rn(scale, dot), total) : 0.0f;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                if (live && v * LP + sub < words) {
+                    float x[kVec];
+                    unpack16(word[v], x);
+#pragma unroll
+                    for (int q = 0; q < kVec; ++q) x[q] = open_logit(x[q]) ? __fmul_rn(exp_below(x[q], top), c) : 0.0f;
+                    st_v4(reinterpret_cast<uint4 *>(out) + v * LP + sub, pack16(x));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (live && v * LP + sub < words)
+                    st_v4(reinterpret_cast<uint4 *>(out) + v * LP + sub, make_uint4(0u, 0u, 0u, 0u));
+        }
+        __syncwarp();                                                  // the row before the chosen places
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            float d = __fmul_rn(w[i], __fsub_rn(gw[i], dot));
+            // 1 - sigmoid(f) = 1 / (1 + exp(f)); exp(f) = inf gives 0
+            if (sigm) d = __fdiv_rn(d, __fadd_rn(1.0f, expf(f[i])));
+            if (w[i] != 0.0f) from_f32(out + e[i], d);
+        }
+    }
+}
+
+// The same for rows that are no multiple of 16 bytes: a warp to a token, an element
+// at a time.
+template <typename T, bool DENSE>
+__global__ void __launch_bounds__(256)
+gate_backward_odd_kernel(const T *__restrict__ logits, const int32_t *__restrict__ topk_idx,
+                         const float *__restrict__ topk_w, const float *__restrict__ d_topk_w,
+                         T *__restrict__ d_logits, int T_, int E, int k, int sigm, int renorm, float scale) {
     pdl_enter();
     const int lane = threadIdx.x & 31;
     const float inv = __fdiv_rn(1.0f, scale);
-    constexpr int kVec = 16 / (int)sizeof(T);
-    const bool vec = E % kVec == 0;
     for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < T_; t += gridDim.x * (blockDim.x >> 5)) {
         const T *row = logits + (size_t)t * E;
         T *out = d_logits + (size_t)t * E;
@@ -308,40 +438,31 @@ gate_backward_kernel(const T *__restrict__ logits, const int32_t *__restrict__ t
             w = __ldg(topk_w + (size_t)t * k + lane);
             gw = __ldg(d_topk_w + (size_t)t * k + lane);
             if ((unsigned)e >= (unsigned)E) e = -1;
-            if (e >= 0 && (sigm || DENSE)) f = to_f32(row[e]);
-            if (e < 0 || w == 0.0f) w = gw = 0.0f;                     // no pair: whatever d_topk_w holds
+            if (e >= 0 && sigm) f = to_f32(row[e]);
+            if (e < 0 || w == 0.0f) w = gw = 0.0f;
         }
-        const float dot = (DENSE || renorm) ? __fmul_rn(warp_sum_f(__fmul_rn(w, gw)), inv) : 0.0f;
-        float d = __fmul_rn(w, __fsub_rn(gw, dot));
-        // 1 - sigmoid(f) = 1 / (1 + exp(f)); exp(f) = inf gives 0
-        if (sigm) d = __fdiv_rn(d, __fadd_rn(1.0f, expf(f)));
+        const float dot = (DENSE || renorm) ? __fmul_rn(lanes_sum<32>(__fmul_rn(w, gw)), inv) : 0.0f;
         if constexpr (DENSE) {
-            uint32_t m = 0;
+            float top = -INFINITY, total = 0.0f;
+            for (int i = lane; i < E; i += 32) top = fmaxf(top, to_f32(row[i]));
+            top = lanes_max<32>(top);
             for (int i = lane; i < E; i += 32) {
                 const float x = to_f32(row[i]);
-                if (open_logit(x)) m = max(m, logit_key(x));
+                if (open_logit(x)) total = __fadd_rn(total, exp_below(x, top));
             }
-            m = __reduce_max_sync(kFull, m);
-            const float top = m == 0 ? 0.0f : key_logit(m);
-            float part = 0.0f;
-            for (int i = lane; i < E; i += 32) {
-                const float x = to_f32(row[i]);
-                if (open_logit(x)) part += exp_below(x, top);
-            }
-            const float total = warp_sum_f(part);
+            total = lanes_sum<32>(total);
             const float c = total > 0.0f ? __fdiv_rn(-__fmul_rn(scale, dot), total) : 0.0f;
             for (int i = lane; i < E; i += 32) {
                 const float x = to_f32(row[i]);
                 from_f32(out + i, open_logit(x) ? __fmul_rn(exp_below(x, top), c) : 0.0f);
             }
-        } else if (vec) {
-            uint4 *o = reinterpret_cast<uint4 *>(out);
-            for (int i = lane; i < E / kVec; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
         } else {
             for (int i = lane; i < E; i += 32) from_f32(out + i, 0.0f);
         }
-        __syncwarp();                                                  // the row before the chosen places
-        if (e >= 0 && w != 0.0f) from_f32(out + e, d);
+        __syncwarp();
+        float d = __fmul_rn(w, __fsub_rn(gw, dot));
+        if (sigm) d = __fdiv_rn(d, __fadd_rn(1.0f, expf(f)));
+        if (w != 0.0f) from_f32(out + e, d);
     }
 }
 
@@ -412,22 +533,41 @@ int launch_gate_v(const Dims &d, const GateArgs &a, A... args) {
     return launch_gate<T, 64>(d, a, args...);                          // v <= 61: E <= 1024, G <= 32
 }
 
+template <typename T, bool DENSE, int LP, int NV, typename... A>
+int launch_backward_one(const Dims &d, cudaStream_t st, A... args) {
+    static PerContext<int> resident_cache;
+    const int resident = resident_blocks_cached(resident_cache, gate_backward_kernel<T, DENSE, LP, NV>, 256);
+    const int grid = persistent_grid(((long long)d.T + 256 / LP - 1) / (256 / LP), resident, d.max_blocks);
+    return launch_pdl(gate_backward_kernel<T, DENSE, LP, NV>, grid, 256, st, args...) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <typename T, bool DENSE, typename... A>
+int launch_backward_rows(const Dims &d, cudaStream_t st, A... args) {
+    constexpr int kVec = 16 / (int)sizeof(T);
+    const int words = d.E / kVec;
+    if (d.E % kVec != 0) {
+        static PerContext<int> resident_cache;
+        const int resident = resident_blocks_cached(resident_cache, gate_backward_odd_kernel<T, DENSE>, 256);
+        const int grid = persistent_grid(((long long)d.T + 7) / 8, resident, d.max_blocks);
+        return launch_pdl(gate_backward_odd_kernel<T, DENSE>, grid, 256, st, args...) == cudaSuccess ? MOE_OK
+                                                                                                     : MOE_ERR_CUDA;
+    }
+    if (words <= 8) return launch_backward_one<T, DENSE, 8, 1>(d, st, args...);
+    if (words <= 16) return launch_backward_one<T, DENSE, 16, 1>(d, st, args...);
+    if (words <= 32) return launch_backward_one<T, DENSE, 16, 2>(d, st, args...);
+    if (words <= 64) return launch_backward_one<T, DENSE, 16, 4>(d, st, args...);
+    if (words <= 128) return launch_backward_one<T, DENSE, 32, 4>(d, st, args...);
+    return launch_backward_one<T, DENSE, 32, 8>(d, st, args...);        // 1024 fp32 logits are 256 words
+}
+
 template <typename T>
 int launch_backward(const Dims &d, const GateArgs &a, cudaStream_t st, const void *logits, const int32_t *idx,
                     const float *w, const float *dw, void *out) {
-    const bool dense = !a.sigmoid && !a.renorm;
-    static PerContext<int> resident_dense, resident_sparse;
-    const int resident = dense ? resident_blocks_cached(resident_dense, gate_backward_kernel<T, true>, 256)
-                               : resident_blocks_cached(resident_sparse, gate_backward_kernel<T, false>, 256);
-    const int grid = persistent_grid(((long long)d.T + 7) / 8, resident, d.max_blocks);
     const T *l = static_cast<const T *>(logits);
     T *o = static_cast<T *>(out);
-    const cudaError_t e =
-        dense ? launch_pdl(gate_backward_kernel<T, true>, grid, 256, st, l, idx, w, dw, o, d.T, d.E, d.k, a.sigmoid,
-                           a.renorm, a.scale)
-              : launch_pdl(gate_backward_kernel<T, false>, grid, 256, st, l, idx, w, dw, o, d.T, d.E, d.k, a.sigmoid,
-                           a.renorm, a.scale);
-    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    if (!a.sigmoid && !a.renorm)
+        return launch_backward_rows<T, true>(d, st, l, idx, w, dw, o, d.T, d.E, d.k, a.sigmoid, a.renorm, a.scale);
+    return launch_backward_rows<T, false>(d, st, l, idx, w, dw, o, d.T, d.E, d.k, a.sigmoid, a.renorm, a.scale);
 }
 
 }  // namespace

@@ -18,10 +18,15 @@
 // share of two MMA steps, so that every step stays within one group of 32.
 #include "moe_w4.cuh"
 
+#include <algorithm>
+
 namespace moe {
 namespace {
 
 constexpr int kW4Warps = 8;
+constexpr int kW4Depth = 4;            // blocks of codes that a warp has in flight or at hand
+constexpr int kW4Stage = 1024 + 128;   // a block of 16 rows: 64 bytes of codes and up to 8 of scales each
+constexpr int kW4TileMap = 1024;       // token tiles whose expert is looked up instead of searched
 
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -54,17 +59,19 @@ __device__ __forceinline__ void load_x8(const uint8_t *p, uint32_t (&b)[4]) {
     }
 }
 
-// The scales of one row's 128 inputs: group 128: one bf16; 64: two; 32: four.
+// The scales of one row's 128 inputs from shared memory: group 128: one bf16, the
+// upper one of its word if odd; 64: two; 32: four.
 template <int GS>
-__device__ __forceinline__ void load_scales(const uint16_t *p, float (&s)[128 / GS]) {
+__device__ __forceinline__ void read_scales(const uint8_t *p, unsigned odd, float (&s)[128 / GS]) {
     if constexpr (GS == 128) {
-        s[0] = __uint_as_float((uint32_t)__ldg(p) << 16);
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
+        s[0] = odd ? bf16_hi(v) : bf16_lo(v);
     } else if constexpr (GS == 64) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(p));
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
         s[0] = bf16_lo(v);
         s[1] = bf16_hi(v);
     } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
         s[0] = bf16_lo(v.x);
         s[1] = bf16_hi(v.x);
         s[2] = bf16_lo(v.y);
@@ -72,15 +79,19 @@ __device__ __forceinline__ void load_scales(const uint16_t *p, float (&s)[128 / 
     }
 }
 
-// Exclusive scan over e of the token tiles (of `tile` rows) of min(counts[e], C)
-// rows into off[0..E]; one block of kW4Warps * 32 threads.
-__device__ __forceinline__ void token_tile_offsets(const int32_t *__restrict__ counts, int E, int C, int tile, int *off,
-                                                   int *warp_tot) {
+// kept[e] = min(counts[e], C); the exclusive scan over e of their token tiles (of
+// `tile` rows) into off[0..E]; and the expert of each of the first kW4TileMap tiles
+// into tile_e. One block of kW4Warps * 32 threads.
+__device__ __forceinline__ void token_tile_offsets(const int32_t *__restrict__ counts, int E, int C, int tile, int *kept,
+                                                   int *off, uint16_t *tile_e, int *warp_tot) {
     const int nt = kW4Warps * 32, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (E + nt - 1) / nt;
     const int e0 = min(E, tid * per), e1 = min(E, e0 + per);
     int local = 0;
-    for (int e = e0; e < e1; ++e) local += (min(__ldg(counts + e), C) + tile - 1) / tile;
+    for (int e = e0; e < e1; ++e) {
+        kept[e] = min(__ldg(counts + e), C);
+        local += (kept[e] + tile - 1) / tile;
+    }
     int incl = local;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -93,147 +104,273 @@ __device__ __forceinline__ void token_tile_offsets(const int32_t *__restrict__ c
     for (int i = 0; i < warp; ++i) run += warp_tot[i];
     for (int e = e0; e < e1; ++e) {
         off[e] = run;
-        run += (min(__ldg(counts + e), C) + tile - 1) / tile;
+        const int n = (kept[e] + tile - 1) / tile;
+        for (int i = run; i < min(run + n, kW4TileMap); ++i) tile_e[i] = (uint16_t)e;
+        run += n;
     }
     if (tid == nt - 1) off[E] = run;
     __syncthreads();
 }
 
-template <bool F8, int GS, bool GATE, int NT>
-__global__ void __launch_bounds__(kW4Warps * 32)
+// BYTES (4, 8 or 16) of global memory to shared memory, tracked by this thread's groups.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+
+// What a block needs to know of a unit of its work.
+struct W4Unit {
+    int e, n0, tok0, kept;             // expert, first output, first row of x, rows of the expert
+};
+
+// A block takes 16 MT rows of one expert's matrix (with the gate 8 MT outputs) and
+// up to 8 NT of the expert's rows of x; its 8 warps split the inputs in blocks of
+// 128, warp w the blocks w, w + 8, ... Each warp keeps kW4Depth blocks of codes and
+// scales coming to a ring of its own by asynchronous copies, over the end of one
+// unit of work into the next, so that the joining of the sums at the unit's end does
+// not empty it. A lane reads the codes that it copied itself.
+template <bool F8, int GS, bool GATE, int NT, int MT>
+__global__ void __launch_bounds__(kW4Warps * 32, NT * MT == 1 ? 3 : 2)
 expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__restrict__ x_scale,
                       const int32_t *__restrict__ counts, const uint8_t *__restrict__ w_q,
                       const uint16_t *__restrict__ w_scale, uint16_t *__restrict__ y) {
-    constexpr int kTokens = 8 * NT, kOut = GATE ? 8 : 16, kGroups = 128 / GS;
-    __shared__ int off[kMaxExperts + 1];
+    constexpr int kTokens = 8 * NT, kOut = (GATE ? 8 : 16) * MT, kGroups = 128 / GS;
+    constexpr int kScaleBytes = GS == 32 ? 8 : 4;    // copied for a row's block: its scales, or the word they are in
+    constexpr int kStage = MT * kW4Stage;
+    __shared__ __align__(16) uint8_t ring[kW4Warps][kW4Depth][kStage];
+    __shared__ int rows_of[kMaxExperts], off[kMaxExperts + 1];
+    __shared__ uint16_t tile_e[kW4TileMap];
     __shared__ int warp_tot[kW4Warps];
-    __shared__ float4 red[kW4Warps][NT][32];
+    __shared__ float4 red[2][kW4Warps][NT * MT][32];
     pdl_enter();
-    token_tile_offsets(counts, a.E, a.C, kTokens, off, warp_tot);
+    token_tile_offsets(counts, a.E, a.C, kTokens, rows_of, off, tile_e, warp_tot);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const unsigned tiles = off[a.E], row_tiles = (a.N + kOut - 1) / kOut;
     const size_t w_row = (size_t)a.K / 2, s_row = (size_t)a.K / GS, x_row = F8 ? (size_t)a.K : 2 * (size_t)a.K;
+    const auto expert_of = [&](unsigned p) { return p < kW4TileMap ? (int)tile_e[p] : expert_of_row(off, a.E, (int)p); };
 
-    for (UnitWalk wk(blockIdx.x, gridDim.x, row_tiles); wk.row < tiles; wk.next()) {
-        const int e = expert_of_row(off, a.E, (int)wk.row);
-        const int kept = min(__ldg(counts + e), a.C);
-        const int tok0 = (int)(wk.row - off[e]) * kTokens;
-        const int n0 = (int)wk.seg * kOut;
-        // rows past the matrix read its last row, and their sums are not stored
-        const int ra = min(n0 + g, a.N - 1);
-        const int rb = GATE ? a.N + ra : min(n0 + 8 + g, a.N - 1);
-        const uint8_t *qa = w_q + ((size_t)e * a.M + ra) * w_row + 16 * t;
-        const uint8_t *qb = w_q + ((size_t)e * a.M + rb) * w_row + 16 * t;
-        const uint16_t *sa = w_scale + ((size_t)e * a.M + ra) * s_row;
-        const uint16_t *sb = w_scale + ((size_t)e * a.M + rb) * s_row;
+    // matrix rows g and g + 8 of a fragment; rows past the matrix read its last, and their sums are not stored
+    const auto row_a = [&](int n0, int m) { return min(n0 + (GATE ? 8 : 16) * m + g, a.N - 1); };
+    const auto row_b = [&](int n0, int m) { return GATE ? a.N + row_a(n0, m) : min(n0 + 16 * m + 8 + g, a.N - 1); };
+    // the blocks to fetch, in the order that they are used
+    UnitWalk fw(blockIdx.x, gridDim.x, row_tiles);
+    int fkb = a.nkb;                                 // past the end: unit fw is the next
+    const uint8_t *fa[MT], *fb[MT], *fs[MT];
+    const uint32_t dst = smem_u32(&ring[warp][0][0]) + 16 * lane;
+    const uint32_t sdst = smem_u32(&ring[warp][0][1024 * MT]) + 64 * t + 8 * g;  // lanes t = 0, 1: rows g and g + 8
+    const auto fetch = [&](unsigned slot) {
+        if (fkb >= a.nkb && warp < a.nkb) {
+            if (fw.row < tiles) {
+                const size_t m0 = (size_t)expert_of(fw.row) * a.M;
+                const int n0 = (int)fw.seg * kOut;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int ra = row_a(n0, m), rb = row_b(n0, m);
+                    fa[m] = w_q + (m0 + ra) * w_row + 64 * warp + 16 * t;
+                    fb[m] = w_q + (m0 + rb) * w_row + 64 * warp + 16 * t;
+                    fs[m] = reinterpret_cast<const uint8_t *>(w_scale + (m0 + (t == 0 ? ra : rb)) * s_row + warp * kGroups);
+                    fs[m] -= reinterpret_cast<uintptr_t>(fs[m]) & (kScaleBytes - 1);
+                }
+                fkb = warp;
+                fw.next();
+            }
+        }
+        if (fkb < a.nkb) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                cp_async<16>(dst + slot * kStage + 1024 * m, fa[m]);
+                cp_async<16>(dst + slot * kStage + 1024 * m + 512, fb[m]);
+                if (t < 2) cp_async<kScaleBytes>(sdst + slot * kStage + 128 * m, fs[m]);
+                fa[m] += 64 * kW4Warps;
+                fb[m] += 64 * kW4Warps;
+                fs[m] += 2 * kGroups * kW4Warps;
+            }
+            fkb += kW4Warps;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (unsigned i = 0; i < kW4Depth - 1; ++i) fetch(i);
+
+    unsigned step = 0;
+    unsigned n_unit = 0;
+    for (UnitWalk wk(blockIdx.x, gridDim.x, row_tiles); wk.row < tiles; wk.next(), ++n_unit) {
+        W4Unit u;
+        u.e = expert_of(wk.row);
+        u.n0 = (int)wk.seg * kOut;
+        u.tok0 = (int)(wk.row - off[u.e]) * kTokens;
+        u.kept = rows_of[u.e];
         const uint8_t *px[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n)           // columns past the rows read the last row, not stored either
-            px[n] = x + ((size_t)e * a.C + min(tok0 + 8 * n + g, kept - 1)) * x_row + (F8 ? 8 : 16) * t;
-        float acc[NT][4];
+            px[n] = x + ((size_t)u.e * a.C + min(u.tok0 + 8 * n + g, u.kept - 1)) * x_row + (F8 ? 8 : 16) * t +
+                    (size_t)warp * (F8 ? 128 : 256);
+        // which half of its word holds the scale of a group of 128: the same for all of a warp's blocks of a row
+        unsigned odd = 0;
+        if constexpr (GS == 128) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < MT; ++m)
+                odd |= (((unsigned)row_a(u.n0, m) * a.nkb + warp) & 1u) << (2 * m) |
+                       (((unsigned)row_b(u.n0, m) * a.nkb + warp) & 1u) << (2 * m + 1);
+        }
+        float acc[MT][NT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
 
-        for (int kb = warp; kb < a.nkb; kb += kW4Warps) {
-            const uint4 va = ld_stream_v4(qa + (size_t)kb * 64), vb = ld_stream_v4(qb + (size_t)kb * 64);
-            float fa[kGroups], fb[kGroups];
-            load_scales<GS>(sa + kb * kGroups, fa);
-            load_scales<GS>(sb + kb * kGroups, fb);
+        for (int kb = warp; kb < a.nkb; kb += kW4Warps, ++step) {
+            uint32_t b[NT == 1 ? 4 : 1][4];
+            if constexpr (NT == 1) {                 // the block's x, before the wait for its codes
 #pragma unroll
-            for (int q = 0; q < kGroups; ++q) {
-                fa[q] *= kW4Unit<F8>;
-                fb[q] *= kW4Unit<F8>;
+                for (int j = 0; j < 4; ++j) load_x8<F8>(px[0] + j * (F8 ? 32 : 64), b[j]);
             }
-            const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+            asm volatile("cp.async.wait_group %0;" ::"n"(kW4Depth - 2) : "memory");
+            __syncwarp();                            // this block is there, and the last one's slot has been read
+            fetch((step + kW4Depth - 1) % kW4Depth);
+            const uint8_t *at = &ring[warp][step % kW4Depth][0];
+            uint4 va[MT], vb[MT];
+            float sa[MT][kGroups], sb[MT][kGroups];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float blk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                float part[4];
+            for (int m = 0; m < MT; ++m) {
+                va[m] = *reinterpret_cast<const uint4 *>(at + 1024 * m + 16 * lane);
+                vb[m] = *reinterpret_cast<const uint4 *>(at + 1024 * m + 512 + 16 * lane);
+                read_scales<GS>(at + 1024 * MT + 128 * m + 8 * g, odd >> (2 * m) & 1u, sa[m]);
+                read_scales<GS>(at + 1024 * MT + 128 * m + 64 + 8 * g, odd >> (2 * m + 1) & 1u, sb[m]);
+            }
+            float part[MT][NT][4], blk[F8 ? MT : 1][NT][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j % (GS / 32) == 0) part[0] = part[1] = part[2] = part[3] = 0.0f;
-                    uint32_t b[4], pa[4], pb[4];
-                    load_x8<F8>(px[n] + (size_t)kb * (F8 ? 128 : 256) + j * (F8 ? 32 : 64), b);
-                    w4_pairs<F8>(wa[j], pa);
-                    w4_pairs<F8>(wb[j], pb);
-                    mma16816<F8>(part, pa[0], pb[0], pa[1], pb[1], b[0], b[1]);
-                    mma16816<F8>(part, pa[2], pb[2], pa[3], pb[3], b[2], b[3]);
-                    if (j % (GS / 32) == GS / 32 - 1) {
-                        const int q = j / (GS / 32);
-                        float(&to)[4] = F8 ? blk : acc[n];
-                        to[0] = fmaf(part[0], fa[q], to[0]);
-                        to[1] = fmaf(part[1], fa[q], to[1]);
-                        to[2] = fmaf(part[2], fb[q], to[2]);
-                        to[3] = fmaf(part[3], fb[q], to[3]);
+            for (int j = 0; j < 4; ++j) {
+                uint32_t pa[MT][4], pb[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    w4_pairs<F8>(j == 0 ? va[m].x : j == 1 ? va[m].y : j == 2 ? va[m].z : va[m].w, pa[m]);
+                    w4_pairs<F8>(j == 0 ? vb[m].x : j == 1 ? vb[m].y : j == 2 ? vb[m].z : vb[m].w, pb[m]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint32_t l[4];
+                    if constexpr (NT == 1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) l[i] = b[j][i];
+                    } else {
+                        load_x8<F8>(px[n] + j * (F8 ? 32 : 64), l);
+                    }
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        float(&p)[4] = part[m][n];
+                        if (j % (GS / 32) == 0) p[0] = p[1] = p[2] = p[3] = 0.0f;
+                        mma16816<F8>(p, pa[m][0], pb[m][0], pa[m][1], pb[m][1], l[0], l[1]);
+                        mma16816<F8>(p, pa[m][2], pb[m][2], pa[m][3], pb[m][3], l[2], l[3]);
+                        if (j % (GS / 32) == GS / 32 - 1) {
+                            const int q = j / (GS / 32);
+                            float(&to)[4] = F8 ? blk[m][n] : acc[m][n];
+                            if (F8 && q == 0) to[0] = to[1] = to[2] = to[3] = 0.0f;
+                            to[0] = fmaf(p[0], sa[m][q], to[0]);
+                            to[1] = fmaf(p[1], sa[m][q], to[1]);
+                            to[2] = fmaf(p[2], sb[m][q], to[2]);
+                            to[3] = fmaf(p[3], sb[m][q], to[3]);
+                        }
                     }
                 }
-                if constexpr (F8) {
-                    const int c0 = min(tok0 + 8 * n + 2 * t, kept - 1), c1 = min(tok0 + 8 * n + 2 * t + 1, kept - 1);
-                    const float s0 = __ldg(x_scale + ((size_t)e * a.C + c0) * a.nkb + kb);
-                    const float s1 = __ldg(x_scale + ((size_t)e * a.C + c1) * a.nkb + kb);
-                    acc[n][0] = fmaf(blk[0], s0, acc[n][0]);
-                    acc[n][1] = fmaf(blk[1], s1, acc[n][1]);
-                    acc[n][2] = fmaf(blk[2], s0, acc[n][2]);
-                    acc[n][3] = fmaf(blk[3], s1, acc[n][3]);
+            }
+            if constexpr (F8) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int c0 = min(u.tok0 + 8 * n + 2 * t, u.kept - 1);
+                    const int c1 = min(u.tok0 + 8 * n + 2 * t + 1, u.kept - 1);
+                    const float s0 = __ldg(x_scale + ((size_t)u.e * a.C + c0) * a.nkb + kb);
+                    const float s1 = __ldg(x_scale + ((size_t)u.e * a.C + c1) * a.nkb + kb);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        acc[m][n][0] = fmaf(blk[m][n][0], s0, acc[m][n][0]);
+                        acc[m][n][1] = fmaf(blk[m][n][1], s1, acc[m][n][1]);
+                        acc[m][n][2] = fmaf(blk[m][n][2], s0, acc[m][n][2]);
+                        acc[m][n][3] = fmaf(blk[m][n][3], s1, acc[m][n][3]);
+                    }
                 }
             }
-        }
-        __syncthreads();                       // the previous unit's sums have been read
 #pragma unroll
-        for (int n = 0; n < NT; ++n) red[warp][n][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            for (int n = 0; n < NT; ++n) px[n] += kW4Warps * (F8 ? 128 : 256);
+        }
+        // two buffers of sums: a warp that writes unit u + 2's has passed the barrier of unit u + 1, which the
+        // readers of unit u's pass after reading
+        float4(&sums)[kW4Warps][NT * MT][32] = red[n_unit & 1];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                sums[warp][m * NT + n][lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
         __syncthreads();
-        if (warp < NT) {                       // warp n joins the sums of columns 8n .. 8n+7
-            float4 r = red[0][warp][lane];
+        if (warp < NT * MT) {                  // one warp for each fragment of 16 matrix rows x 8 rows of x
+            const int m = warp / NT, n = warp % NT;
+            float4 r = sums[0][warp][lane];
 #pragma unroll
             for (int i = 1; i < kW4Warps; ++i) {
-                const float4 v = red[i][warp][lane];
+                const float4 v = sums[i][warp][lane];
                 r.x += v.x;
                 r.y += v.y;
                 r.z += v.z;
                 r.w += v.w;
             }
-            const int c = tok0 + 8 * warp + 2 * t;
-            uint16_t *o = y + ((size_t)e * a.C + c) * a.N + n0 + g;
+            r.x *= kW4Unit<F8>;
+            r.y *= kW4Unit<F8>;
+            r.z *= kW4Unit<F8>;
+            r.w *= kW4Unit<F8>;
+            const int c = u.tok0 + 8 * n + 2 * t, out = u.n0 + (GATE ? 8 : 16) * m + g;
+            uint16_t *o = y + ((size_t)u.e * a.C + c) * a.N + out;
             if constexpr (GATE) {
-                if (n0 + g < a.N) {
-                    if (c < kept) put_bf16(o, silu(r.x) * r.z);
-                    if (c + 1 < kept) put_bf16(o + a.N, silu(r.y) * r.w);
+                if (out < a.N) {
+                    if (c < u.kept) put_bf16(o, silu(r.x) * r.z);
+                    if (c + 1 < u.kept) put_bf16(o + a.N, silu(r.y) * r.w);
                 }
             } else {
-                if (n0 + g < a.N) {
-                    if (c < kept) put_bf16(o, r.x);
-                    if (c + 1 < kept) put_bf16(o + a.N, r.y);
+                if (out < a.N) {
+                    if (c < u.kept) put_bf16(o, r.x);
+                    if (c + 1 < u.kept) put_bf16(o + a.N, r.y);
                 }
-                if (n0 + 8 + g < a.N) {
-                    if (c < kept) put_bf16(o + 8, r.z);
-                    if (c + 1 < kept) put_bf16(o + 8 + a.N, r.w);
+                if (out + 8 < a.N) {
+                    if (c < u.kept) put_bf16(o + 8, r.z);
+                    if (c + 1 < u.kept) put_bf16(o + 8 + a.N, r.w);
                 }
             }
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <bool F8, int GS, bool GATE, int NT>
+template <bool F8, int GS, bool GATE, int NT, int MT>
 int launch_rows(const Dims &d, const W4Args &a, cudaStream_t st, const void *x, const float *x_scale,
                 const int32_t *counts, const void *w_q, const void *w_scale, void *y) {
     static PerContext<int> resident_cache;
-    const int resident = resident_blocks_cached(resident_cache, expert_w4_rows_kernel<F8, GS, GATE, NT>, kW4Warps * 32);
-    const long long tiles = (long long)(d.T * (long long)d.k < (long long)d.E * d.C ? d.T * (long long)d.k : (long long)d.E * d.C);
-    const int grid = persistent_grid(tiles * ((a.N + (GATE ? 8 : 16) - 1) / (GATE ? 8 : 16)), resident, d.max_blocks);
-    if (launch_pdl(expert_w4_rows_kernel<F8, GS, GATE, NT>, grid, kW4Warps * 32, st, a, static_cast<const uint8_t *>(x),
-                   x_scale, counts, static_cast<const uint8_t *>(w_q), static_cast<const uint16_t *>(w_scale),
+    const auto kernel = expert_w4_rows_kernel<F8, GS, GATE, NT, MT>;
+    const int resident = resident_blocks_cached(resident_cache, kernel, kW4Warps * 32);
+    constexpr int kOut = (GATE ? 8 : 16) * MT;
+    const long long tiles = std::min<long long>((long long)d.T * d.k, (long long)d.E * d.C);
+    const int grid = persistent_grid(tiles * ((a.N + kOut - 1) / kOut), resident, d.max_blocks);
+    if (launch_pdl(kernel, grid, kW4Warps * 32, st, a, static_cast<const uint8_t *>(x), x_scale, counts,
+                   static_cast<const uint8_t *>(w_q), static_cast<const uint16_t *>(w_scale),
                    static_cast<uint16_t *>(y)) != cudaSuccess)
         return MOE_ERR_CUDA;
     return MOE_OK;
 }
 
 template <bool F8, int GS, bool GATE, typename... A>
-int launch_nt(const Dims &d, A... args) {
-    if ((d.T < d.C ? d.T : d.C) <= 8) return launch_rows<F8, GS, GATE, 1>(d, args...);
-    return launch_rows<F8, GS, GATE, 2>(d, args...);
+int launch_nt(const Dims &d, const W4Args &a, A... args) {
+    // two fragments of matrix rows to a warp halve what it spends beside the products, where the experts that can
+    // have rows give every resident block a few units all the same
+    const long long live = std::min<long long>((long long)d.T * d.k, d.E);
+    const bool two = live * a.N / (GATE ? 16 : 32) >= 3LL * sm_count();
+    // one fragment of 8 rows of x where the experts average 4 or fewer: the few with more than 8 are read twice
+    if (std::min(d.T, d.C) <= 8 || (long long)d.T * d.k <= 4LL * d.E)
+        return two ? launch_rows<F8, GS, GATE, 1, 2>(d, a, args...) : launch_rows<F8, GS, GATE, 1, 1>(d, a, args...);
+    return two ? launch_rows<F8, GS, GATE, 2, 2>(d, a, args...) : launch_rows<F8, GS, GATE, 2, 1>(d, a, args...);
 }
 template <bool F8, int GS, typename... A>
 int launch_gate_act(const Dims &d, const W4Args &a, A... args) {
