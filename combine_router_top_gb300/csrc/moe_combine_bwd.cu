@@ -13,9 +13,12 @@
 namespace moe {
 namespace {
 
-// A token's row is walked by WPT warps in segments of WPT*32*U chunks of 16
-// bytes (8 elements); block = WPT warps, one token at a time.
-template <int WPT, int U, int KMAX>
+// A block of WPT warps takes a token at a time and walks its row in segments of
+// WPT*32 chunks of 16 bytes (8 elements), one chunk to a lane. Many small blocks
+// with one load in flight a lane keep HBM busier than few with several: 4096 x 7168
+// top-8, 4 warps with 7 chunks a lane 189 us, 7 warps with 4, 2 and 1 174, 164 and
+// 161 (0.92 of the copy bandwidth), 14 and 28 warps with 1 163 and 233.
+template <int WPT, int KMAX>
 __global__ void __launch_bounds__(WPT * 32)
 combine_backward_kernel(const uint4 *__restrict__ y, const uint4 *__restrict__ d_out,
                         const int32_t *__restrict__ topk_idx, const float *__restrict__ topk_w,
@@ -39,12 +42,10 @@ combine_backward_kernel(const uint4 *__restrict__ y, const uint4 *__restrict__ d
         float dot[KMAX];
 #pragma unroll
         for (int j = 0; j < KMAX; ++j) dot[j] = 0.0f;
-        for (int c0 = threadIdx.x; c0 - (int)threadIdx.x < H8; c0 += WPT * 32 * U) {
-            uint4 g[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-                g[i] = c0 + i * WPT * 32 < H8 ? ld_stream_v4(d_out + (size_t)t * H8 + c0 + i * WPT * 32)
-                                              : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = threadIdx.x; c - (int)threadIdx.x < H8; c += WPT * 32) {
+            uint4 g = make_uint4(0u, 0u, 0u, 0u);
+            if (c < H8) g = ld_stream_v4(d_out + (size_t)t * H8 + c);
+            const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
             unsigned rem = kept;
 #pragma unroll
             for (int j = 0; j < KMAX; ++j) {
@@ -53,25 +54,17 @@ combine_backward_kernel(const uint4 *__restrict__ y, const uint4 *__restrict__ d
                     rem &= rem - 1;
                     const size_t at = (size_t)__shfl_sync(kFull, row, src) * H8;
                     const float wj = __shfl_sync(kFull, w, src);
-                    uint4 v[U];
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (c < H8) v = ld_stream_v4(y + at + c);
+                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < U; ++i)
-                        v[i] = c0 + i * WPT * 32 < H8 ? ld_stream_v4(y + at + c0 + i * WPT * 32)
-                                                      : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
-                        const uint32_t vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            dot[j] = __fmaf_rn(bf16_lo(gw[q]), bf16_lo(vw[q]), dot[j]);
-                            dot[j] = __fmaf_rn(bf16_hi(gw[q]), bf16_hi(vw[q]), dot[j]);
-                            o[q] = pack_bf16x2(__fmul_rn(wj, bf16_lo(gw[q])), __fmul_rn(wj, bf16_hi(gw[q])));
-                        }
-                        if (c0 + i * WPT * 32 < H8)
-                            st_v4(d_y + at + c0 + i * WPT * 32, make_uint4(o[0], o[1], o[2], o[3]));
+                    for (int q = 0; q < 4; ++q) {
+                        dot[j] = __fmaf_rn(bf16_lo(gw[q]), bf16_lo(vw[q]), dot[j]);
+                        dot[j] = __fmaf_rn(bf16_hi(gw[q]), bf16_hi(vw[q]), dot[j]);
+                        o[q] = pack_bf16x2(__fmul_rn(wj, bf16_lo(gw[q])), __fmul_rn(wj, bf16_hi(gw[q])));
                     }
+                    if (c < H8) st_v4(d_y + at + c, make_uint4(o[0], o[1], o[2], o[3]));
                 }
             }
         }
@@ -99,13 +92,13 @@ combine_backward_kernel(const uint4 *__restrict__ y, const uint4 *__restrict__ d
     }
 }
 
-template <int WPT, int U, int KMAX>
+template <int WPT, int KMAX>
 int launch_one(const Dims &d, cudaStream_t st, const void *y, const void *d_out, const int32_t *idx, const float *w,
                const int32_t *slot, void *d_y, float *d_w) {
     static PerContext<int> resident_cache;
-    const int resident = resident_blocks_cached(resident_cache, combine_backward_kernel<WPT, U, KMAX>, WPT * 32);
+    const int resident = resident_blocks_cached(resident_cache, combine_backward_kernel<WPT, KMAX>, WPT * 32);
     const int grid = persistent_grid(d.T, resident, d.max_blocks);
-    if (launch_pdl(combine_backward_kernel<WPT, U, KMAX>, grid, WPT * 32, st, static_cast<const uint4 *>(y),
+    if (launch_pdl(combine_backward_kernel<WPT, KMAX>, grid, WPT * 32, st, static_cast<const uint4 *>(y),
                    static_cast<const uint4 *>(d_out), idx, w, slot, static_cast<uint4 *>(d_y), d_w, d.T, d.H / 8, d.k,
                    d.C) != cudaSuccess)
         return MOE_ERR_CUDA;
@@ -115,11 +108,14 @@ int launch_one(const Dims &d, cudaStream_t st, const void *y, const void *d_out,
 template <int KMAX, typename... A>
 int launch_k(const Dims &d, A... args) {
     const int H8 = d.H / 8;
-    if (H8 <= 64) return launch_one<1, 2, KMAX>(d, args...);
-    if (H8 <= 128) return launch_one<1, 4, KMAX>(d, args...);
-    if (H8 % (128 * 7) == 0) return launch_one<4, 7, KMAX>(d, args...);
-    if (H8 > 256) return launch_one<4, 4, KMAX>(d, args...);
-    return launch_one<4, 2, KMAX>(d, args...);
+    if (H8 <= 32) return launch_one<1, KMAX>(d, args...);
+    if (H8 <= 64) return launch_one<2, KMAX>(d, args...);
+    if (H8 <= 128) return launch_one<4, KMAX>(d, args...);
+    // few tokens: the time is a block's own, which more warps to a row shorten (237 x 2056 top-6: 5.3 us with 16
+    // warps, 6.9 with 7); many: the width that wastes fewer lanes at the row's end
+    if (d.T <= 2 * sm_count()) return launch_one<16, KMAX>(d, args...);
+    if ((H8 + 223) / 224 * 224 < (H8 + 255) / 256 * 256) return launch_one<7, KMAX>(d, args...);
+    return launch_one<8, KMAX>(d, args...);
 }
 
 }  // namespace

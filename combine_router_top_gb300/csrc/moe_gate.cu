@@ -180,13 +180,59 @@ __device__ __forceinline__ void warp_gate(const T *__restrict__ row, const float
             key[i] = i >= n ? kTaken : open_logit(l[i]) ? number_key(l[i]) : kMasked;
     }
 
+    // Lanes of up to 8 experts sort theirs once, largest first, ties by index: a round of the choice then looks at
+    // the first key alone. `order` holds the sorted experts' places within the lane, 4 bits each.
+    uint32_t order = 0;
+    if constexpr (V <= 8) {
+        uint32_t id[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) id[i] = i;
+        const auto swap = [&](int x, int y) {                          // x < y: the larger to x
+            const bool s = key[y] > key[x] || (key[y] == key[x] && id[y] < id[x]);
+            const uint32_t kx = key[x], ix = id[x];
+            key[x] = s ? key[y] : kx;
+            key[y] = s ? kx : key[y];
+            id[x] = s ? id[y] : ix;
+            id[y] = s ? ix : id[y];
+        };
+        if constexpr (V == 2) swap(0, 1);
+        if constexpr (V >= 4) {                                        // Batcher's odd-even merge
+#pragma unroll
+            for (int h = 0; h < V; h += 4) {
+                swap(h, h + 1);
+                swap(h + 2, h + 3);
+                swap(h, h + 2);
+                swap(h + 1, h + 3);
+                swap(h + 1, h + 2);
+            }
+        }
+        if constexpr (V == 8) {
+            swap(0, 4);
+            swap(1, 5);
+            swap(2, 6);
+            swap(3, 7);
+            swap(2, 4);
+            swap(3, 5);
+            swap(1, 2);
+            swap(3, 4);
+            swap(5, 6);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) order |= id[i] << (4 * i);
+    }
+
     if (a.G > 1) {
         // this lane's two best keys, then its group's by a turn around the group's lanes
         uint32_t k1 = 0, k2 = 0;
+        if constexpr (V <= 8) {
+            k1 = key[0];
+            k2 = key[1];
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            k2 = max(k2, min(k1, key[i]));
-            k1 = max(k1, key[i]);
+            for (int i = 0; i < V; ++i) {
+                k2 = max(k2, min(k1, key[i]));
+                k1 = max(k1, key[i]);
+            }
         }
         const uint32_t own1 = k1, own2 = k2;
         const int base = lane - r;
@@ -207,6 +253,7 @@ __device__ __forceinline__ void warp_gate(const T *__restrict__ row, const float
             gk = k2 >= kFirstNumber ? logit_key(__fadd_rn(s1, s2)) : kFirstNumber;
         }
         int better = 0;
+#pragma unroll 4
         for (int o = 0; o < a.G; ++o) {
             const uint32_t ok_ = __shfl_sync(kFull, gk, o * a.L);
             better += ok_ > gk || (ok_ == gk && o < g);
@@ -217,34 +264,53 @@ __device__ __forceinline__ void warp_gate(const T *__restrict__ row, const float
         }
     }
 
-    // k rounds. A lane's best remaining key changes only when the lane wins, and which of its experts has it is
-    // looked for by the winner alone: the lowest of its tied ones, in the lowest tied lane.
-    uint32_t my_key = 0, best = 0;
+    uint32_t my_key = 0;
     my_e = 0;
+    if constexpr (V <= 8) {
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t m = __reduce_max_sync(kFull, key[0]);       // >= kMasked: k <= E
+            const int wl = __ffs(__ballot_sync(kFull, key[0] == m)) - 1;
+            const int e = __shfl_sync(kFull, e0 + (int)(order & 15u), wl);
+            if (lane == wl) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) best = max(best, key[i]);
-    for (int j = 0; j < a.k; ++j) {
-        const uint32_t m = __reduce_max_sync(kFull, best);             // >= kMasked: k <= E
-        const int wl = __ffs(__ballot_sync(kFull, best == m)) - 1;
-        int bi = 0;
-        if (lane == wl) {
-            best = 0;
-            bool found = false;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool hit = !found && key[i] == m;
-                if (hit) {
-                    bi = i;
-                    key[i] = kTaken;
-                }
-                found |= hit;
-                best = max(best, key[i]);
+                for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+                key[V - 1] = kTaken;
+                order >>= 4;
+            }
+            if (lane == j) {
+                my_key = m;
+                my_e = e;
             }
         }
-        const int e = __shfl_sync(kFull, e0 + bi, wl);
-        if (lane == j) {
-            my_key = m;
-            my_e = e;
+    } else {
+        // A lane's best remaining key changes only when the lane wins, and which of its experts has it is looked
+        // for by the winner alone: the lowest of its tied ones, in the lowest tied lane.
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) best = max(best, key[i]);
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t m = __reduce_max_sync(kFull, best);
+            const int wl = __ffs(__ballot_sync(kFull, best == m)) - 1;
+            int bi = 0;
+            if (lane == wl) {
+                best = 0;
+                bool found = false;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const bool hit = !found && key[i] == m;
+                    if (hit) {
+                        bi = i;
+                        key[i] = kTaken;
+                    }
+                    found |= hit;
+                    best = max(best, key[i]);
+                }
+            }
+            const int e = __shfl_sync(kFull, e0 + bi, wl);
+            if (lane == j) {
+                my_key = m;
+                my_e = e;
+            }
         }
     }
 

@@ -256,7 +256,7 @@ route_chunk_scan_kernel(int n_chunks, int E, const int32_t *__restrict__ chunk_s
 // chunk; slot = base + rank in tile (or -1 at or past C). The last CTA also
 // adds its own tile to get the totals and writes counts, offsets,
 // rank_counts and dropped.
-__global__ void __launch_bounds__(1024, 1)
+__global__ void __launch_bounds__(1024, 2)          // 32 registers: two blocks to an SM
 route_finalize_kernel(int T, int n_tiles, int E, int k, int R, int C, const int32_t *__restrict__ tile_counts,
                       const int32_t *__restrict__ chunk_base,
                       const int32_t *__restrict__ topk_idx, int32_t *__restrict__ slot,
