@@ -92,16 +92,6 @@ __device__ __forceinline__ uint32_t mbar_try_wait(uint32_t bar, uint32_t parity)
                  : "memory");
     return done;
 }
-// The same without waiting.
-__device__ __forceinline__ uint32_t mbar_test_wait(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(done)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return done;
-}
-
 // gemm_wait by a whole warp; every lane returns the same. The first try is the
 // common case and costs a few instructions: a wait stands in the loops whose
 // latency the tensor cores wait for.

@@ -19,8 +19,8 @@
 //   warps 1, 3  the MMAs of a tile's even and odd blocks, one elected lane each: per
 //               group, the steps of both halves into fresh accumulators. All 512 TMEM
 //               columns are held: for each half and parity 64 columns of accumulators
-//               (two slots of 32, or one of 64 where the tile has over 32 rows of x)
-//               and 64 of operand (128 inputs);
+//               (one group of up to 64 rows of x, two of 32 or four of 16) and 64 of
+//               operand (128 inputs);
 //   warp 2      brings the group scales (and fp8 rows' block scales), 8 groups at a
 //               time, from HBM to a ring in shared memory;
 //   warps 4-19  four TMEM quadrants x two halves x even and odd blocks: copy the codes
@@ -38,24 +38,47 @@ namespace {
 
 constexpr int kTRows = 128;                          // matrix rows of one half (TMEM lanes)
 constexpr int kTTok = 64;                            // rows of x to a tile, at most
-constexpr int kTXStages = 4;                         // ring of x blocks
+constexpr int kTXStages = 4;                         // rings of x blocks: two of even and two of odd blocks
 constexpr int kTThreads = 896;                       // 28 warps of 72 registers
 constexpr int kTWDepth = 4;                          // blocks of codes that a warp has in flight or at hand
 constexpr uint32_t kTWBytes = 32 * 64;               // codes of a warp's 32 rows of a block
 constexpr uint32_t kTXBytes = kTTok * 128;           // x of 64 inputs
 constexpr int kTChunks = 3, kTChunk = 8;             // scale ring: 3 chunks of 8 groups
-constexpr int kTScalePad = kTRows + 8;               // stride of a group's 128 scales: 8 groups on 8 bank sets
 constexpr size_t kTExBytes = (size_t)16 * kTRows * 4;
-constexpr size_t kTScaleBytes = (size_t)kTChunks * 2 * kTChunk * kTScalePad * 2;
+constexpr size_t kTScaleBytes = (size_t)kTChunks * 2 * kTRows * kTChunk * 2;
 constexpr size_t kTXsBytes = (size_t)kTChunks * kTChunk * kTTok * 4;
 constexpr size_t kTSmemBytes = 1024 + kTXStages * 2 * (size_t)kTXBytes + 16 * kTWDepth * (size_t)kTWBytes + kTExBytes +
                                kTScaleBytes + kTXsBytes;
 
-// 16 bytes of global memory to shared memory, tracked by this thread's groups.
+// How a tile of up to CAP rows of x uses a parity's 64 columns of accumulators: the
+// sums of kBatch groups of CAP columns go to one slot and are waited for together,
+// kSlots slots.
+template <int GPB, int CAP>
+struct W4Acc {
+    static constexpr int kRoom = kTTok / CAP;                          // 4, 2, 1
+    static constexpr int kBatch = GPB < kRoom ? GPB : kRoom;
+    static constexpr int kSlots = kRoom / kBatch;
+};
+
+// 16 bytes of global memory to shared memory, asynchronously.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// The same for BYTES (4, 8 or 16), or as many zeros where there is nothing to copy.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void *src, bool some) {
+    const int n = some ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+}
+// Arrives on the mbarrier once all of this thread's copies so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -111,56 +134,26 @@ __device__ __forceinline__ void add16(float *acc, const uint32_t *v, float ws, c
     }
 }
 
-// One warp brings the scales of groups c .. c+7 of the two halves' 128 matrix rows
-// (valid0 and valid1 of them in the matrix) to to[half][group][row], W bytes of a
-// row to a load, up to 16 loads in flight: a chunk serves 2, 4 or 8 blocks of 128
-// inputs. room() waits until the ring's slot may be written.
-template <int W, typename Room>
-__device__ __forceinline__ bool scale_chunk(const uint16_t *__restrict__ src0, const uint16_t *__restrict__ src1,
-                                            int groups, int c, int valid0, int valid1, uint16_t *__restrict__ to,
-                                            int lane, Room room) {
-    constexpr int kLanes = 16 / W, kRows = 32 / kLanes, kIter = kTRows / kRows;
-    constexpr int kWords = W < 4 ? 1 : W / 4, kAll = 16 / kWords, kBatch = 2 * kIter < kAll ? 2 * kIter : kAll;
-    const int r0 = lane / kLanes, c0 = (lane % kLanes) * (W / 2);
-    bool ok = true;
+// One warp brings the scales of groups c .. c+7 of 128 matrix rows, `valid` of them
+// in the matrix, to `to` (16 bytes a row), W bytes of a row to a copy; zeros for rows
+// and groups past the end. Rows of an odd number of scales, which 4-byte copies
+// cannot reach, go through registers.
+template <int W>
+__device__ __forceinline__ void scale_chunk(const uint16_t *__restrict__ src, int groups, int c, int valid,
+                                            uint16_t *to, int lane) {
 #pragma unroll
-    for (int b = 0; b < 2 * kIter; b += kBatch) {
-        uint32_t v[kBatch][kWords];
+    for (int i = 0; i < kTRows / 32; ++i) {
+        const int r = 32 * i + lane;
+        const uint16_t *from = src + (size_t)min(r, max(valid - 1, 0)) * groups + c;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int h = (b + i) / kIter, r = (b + i) % kIter * kRows + r0;
-            const uint16_t *p = (h ? src1 : src0) + (size_t)r * groups + c + c0;
-#pragma unroll
-            for (int q = 0; q < kWords; ++q) v[i][q] = 0u;
-            if (r < (h ? valid1 : valid0) && c + c0 < groups) {
-                if constexpr (W == 16) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-                    v[i][0] = u.x;
-                    v[i][1] = u.y;
-                    v[i][2] = u.z;
-                    v[i][3] = u.w;
-                } else if constexpr (W == 8) {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-                    v[i][0] = u.x;
-                    v[i][1] = u.y;
-                } else if constexpr (W == 4) {
-                    v[i][0] = __ldg(reinterpret_cast<const uint32_t *>(p));
-                } else {
-                    v[i][0] = __ldg(p);
-                }
-            }
-        }
-        if (b == 0) ok = room();
-        if (!ok) return false;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int h = (b + i) / kIter, r = (b + i) % kIter * kRows + r0;
-#pragma unroll
-            for (int q = 0; q < W / 2; ++q)
-                to[(h * kTChunk + c0 + q) * kTScalePad + r] = (uint16_t)(v[i][q / 2] >> (16 * (q & 1)));
+        for (int q = 0; q < kTChunk; q += W / 2) {
+            const bool some = r < valid && c + q < groups;
+            if constexpr (W >= 4)
+                cp_async_or_zero<W>(smem_u32(to + r * kTChunk + q), some ? from + q : src, some);
+            else
+                to[r * kTChunk + q] = some ? __ldg(from + q) : (uint16_t)0;
         }
     }
-    return true;
 }
 
 template <bool F8, int GS, bool GATE>
@@ -172,9 +165,9 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
     constexpr int kOut = GATE ? kTRows : 2 * kTRows; // outputs of a tile
     extern __shared__ uint8_t w4_smem_raw[];
     constexpr int SX = kTXStages;
-    __shared__ __align__(8) uint64_t x_full[SX], x_empty[SX];
-    __shared__ __align__(8) uint64_t a_full[2], a_free[2];                // operands of even and odd blocks
-    __shared__ __align__(8) uint64_t d_full[4], d_free[4];                // accumulators: [2 (odd block) + slot]
+    __shared__ __align__(8) uint64_t x_full[SX];
+    __shared__ __align__(8) uint64_t a_full[2], a_free[4];                // operands of even and odd blocks; [2 (odd block) + odd use]
+    __shared__ __align__(8) uint64_t d_full[8], d_free[8];                // accumulators: [4 (odd block) + slot]
     __shared__ __align__(8) uint64_t sc_full[kTChunks], sc_empty[kTChunks];
     __shared__ __align__(8) uint64_t ex_full[4], ex_free[4];           // sums traded between the halves
     __shared__ __align__(8) uint64_t s_drain[2];
@@ -195,18 +188,17 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
     if (threadIdx.x == 0) {
         for (int i = 0; i < SX; ++i) {
             mbar_init(&x_full[i], 1);
-            mbar_init(&x_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&a_full[i], 8);
-            mbar_init(&a_free[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i) mbar_init(&a_free[i], 1);
+        for (int i = 0; i < 8; ++i) {
             mbar_init(&d_full[i], 1);
             mbar_init(&d_free[i], 8);
         }
         for (int i = 0; i < kTChunks; ++i) {
-            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_full[i], 32);
             mbar_init(&sc_empty[i], 8);
         }
         for (int i = 0; i < 4; ++i) {
@@ -255,14 +247,13 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
     tc_fence_after();
     const uint32_t tmem = s_tmem;                    // half h, odd block or even p: accumulators at 128 h + 64 p, operand 256 on
 
-    uint32_t x_issued = 0;                           // blocks of x loaded, for the drain
+    uint32_t x_even = 0, x_odd = 0;                  // blocks of x loaded, also for the drain
     // setmaxnreg is one instruction of a whole warpgroup (warps 0-3, 4-7, ...). 896 threads of 72 registers are
     // 64512; 20 warps give up 16 of theirs for the 8 that hold 64 sums: 20 x 32 x 56 + 8 x 32 x 112 = 64512
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             const bool elected = elect_one();
-            uint32_t s = 0, phase = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 int e, nt, tt;
@@ -272,7 +263,10 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                 const int ez = __shfl_sync(kFull, e, 0), row_x = __shfl_sync(kFull, tt * kTTok, 0);
                 const CUtensorMap *map = &maps.x[n16 - 1];
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (x_issued >= SX && !(ok = warp_wait(smem_u32(&x_empty[0]) + 8 * s, phase ^ 1u, &s_abort))) break;
+                    uint32_t &use = kb & 1 ? x_odd : x_even;
+                    const uint32_t s = 2 * (kb & 1) + (use & 1);
+                    // the block two uses ago has been multiplied: its x stage is its operand use's
+                    if (use >= 2 && !(ok = warp_wait(smem_u32(&a_free[0]) + 8 * s, ((use >> 1) + 1) & 1, &s_abort))) break;
                     if (elected) {
                         const uint32_t at = smem0 + s * 2 * kTXBytes, bar = smem_u32(&x_full[0]) + 8 * s;
                         mbar_expect_tx(&x_full[s], n16 * 4096);
@@ -280,8 +274,7 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                         tma_load_3d(at + kTXBytes, map, bar, kb * 128 + 64, row_x, ez);
                     }
                     __syncwarp();
-                    ++x_issued;
-                    if (++s == SX) s = 0, phase ^= 1u;
+                    ++use;
                 }
             }
         } else if (warp == 1 || warp == 3) {
@@ -294,57 +287,61 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
             const uint32_t op = __shfl_sync(kFull, tmem, 0) + 256 + 64 * par;       // + 128 per half
             const uint32_t d0 = __shfl_sync(kFull, tmem, 0) + 64 * par;             // + 128 per half, 32 per slot
             const bool elected = elect_one();
-            const uint32_t b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[par]);
-            const uint32_t b_dfull = smem_u32(&d_full[2 * par]), b_dfree = smem_u32(&d_free[2 * par]);
-            uint32_t n0 = 0;                         // blocks before the tile: block n has x stage n % SX
-            uint32_t a_phase = 0, d_phase = 0;       // odd or even use of the operand, of the slots (bits)
+            const uint32_t b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[2 * par]);
+            const uint32_t b_dfull = smem_u32(&d_full[4 * par]), b_dfree = smem_u32(&d_free[4 * par]);
+            uint32_t use = 0;                        // blocks so far: of the operand, and of the parity's two x stages
+            uint32_t d_phase = 0;                    // odd or even use of the slots (bits)
+            int last_cap = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                int e, nt, tt;
-                tiles.decode(t, e, nt, tt);
-                const int rows = min(min(__ldg(counts + e), a.C) - tt * kTTok, kTTok);
-                const uint32_t n16 = (uint32_t)__shfl_sync(kFull, (rows + 15) / 16 * 16, 0);
-                const uint32_t slots = n16 <= 32 ? 1u : 0u;          // xor mask: two slots of 32 columns, or one of 64
+            const auto tile = [&](auto cap_, uint32_t n16) {
+                constexpr int CAP = decltype(cap_)::value;
+                using Acc = W4Acc<GPB, CAP>;
                 // fp32 sums; both operands fp16 (0) or bf16 (1); 128 x n16
                 const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | ((n16 >> 3) << 17) |
                                        ((uint32_t)(kTRows >> 4) << 24);
-                // a slot of 64 columns takes the place of both slots of 32
-                if (!slots) ok = warp_wait(b_dfree + 8, (d_phase >> 1 & 1u) ^ 1u, &s_abort);
+                if (last_cap != CAP) {               // slots of other widths: every one of the last tile's has been read
+                    for (int i = 0; i < 4; ++i)
+                        if (!warp_wait(b_dfree + 8 * i, (d_phase >> i & 1u) ^ 1u, &s_abort)) return false;
+                    last_cap = CAP;
+                }
                 uint32_t slot = 0;
-                static_assert(SX == 4, "a block's x stage and its use are bits of its number");
-                for (int kb = (int)par; kb < nkb && ok; kb += 2) {
-                    const uint32_t s = (n0 + kb) & 3u;
+                for (int kb = (int)par; kb < nkb; kb += 2, ++use) {
+                    const uint32_t s = 2 * par + (use & 1);
                     const uint64_t bx = umma_desc_sw128(smem0 + s * 2 * kTXBytes);
-                    ok = warp_wait(smem_u32(&x_full[0]) + 8 * s, (n0 + kb) >> 2 & 1u, &s_abort) &&
-                         warp_wait(b_afull, a_phase, &s_abort);
-                    a_phase ^= 1u;
+                    if (!warp_wait(smem_u32(&x_full[0]) + 8 * s, use >> 1 & 1u, &s_abort)) return false;
+                    if (!warp_wait(b_afull, use & 1u, &s_abort)) return false;
 #pragma unroll
-                    for (int q = 0; q < GPB; ++q) {
-                        if (ok) ok = warp_wait(b_dfree + 8 * slot, (d_phase >> slot & 1u) ^ 1u, &s_abort);
-                        if (!ok) break;
+                    for (int q = 0; q < GPB; q += Acc::kBatch) {
+                        if (!warp_wait(b_dfree + 8 * slot, (d_phase >> slot & 1u) ^ 1u, &s_abort)) return false;
                         d_phase ^= 1u << slot;
                         tc_fence_after();
+                        const uint32_t d = d0 + slot * (Acc::kBatch * CAP);
                         if (elected) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                                for (int k = 0; k < GS / 16; ++k) {
+                                for (int k = 0; k < Acc::kBatch * GS / 16; ++k) {
                                     const int k16 = q * (GS / 16) + k;
-                                    mma_ts(d0 + 128 * h + 32 * slot, op + 128 * h + 8 * k16,
-                                           bx + ((k16 >> 2) * kTXBytes + 32 * (k16 & 3)) / 16, idesc, k > 0 ? 1u : 0u);
+                                    mma_ts(d + 128 * h + k / (GS / 16) * CAP, op + 128 * h + 8 * k16,
+                                           bx + ((k16 >> 2) * kTXBytes + 32 * (k16 & 3)) / 16, idesc,
+                                           k % (GS / 16) > 0 ? 1u : 0u);
                                 }
                             }
                             mma_commit(b_dfull + 8 * slot);
-                            if (q == GPB - 1) {      // the operand and x have been read
-                                mma_commit(b_afree);
-                                mma_commit(smem_u32(&x_empty[0]) + 8 * s);
-                            }
+                            if (q + Acc::kBatch == GPB) mma_commit(b_afree + 8 * (use & 1));   // operand and x are read
                         }
                         __syncwarp();
-                        slot ^= slots;
+                        if (++slot == Acc::kSlots) slot = 0;
                     }
                 }
-                n0 += nkb;
+                return true;
+            };
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                int e, nt, tt;
+                tiles.decode(t, e, nt, tt);
+                const int rows = __shfl_sync(kFull, min(min(__ldg(counts + e), a.C) - tt * kTTok, kTTok), 0);
+                const uint32_t n16 = (uint32_t)(rows + 15) / 16 * 16;
+                ok = rows <= 16 ? tile(Int<16>(), n16) : rows <= 32 ? tile(Int<32>(), n16) : tile(Int<64>(), n16);
             }
         } else {
             constexpr int KPC = kTChunk / GPB;       // blocks of 128 inputs to a chunk
@@ -363,40 +360,41 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                 const float *xsrc = F8 ? x_scale + ((size_t)e * a.C + tt * kTTok) * nkb : nullptr;
                 for (int c = 0; c < chunks; ++c, ++cg) {
                     const int buf = cg % kTChunks;
-                    const auto room = [&] {          // the ring's slot has been read
-                        return cg < kTChunks ||
-                               warp_wait(smem_u32(&sc_empty[buf]), ((cg / kTChunks) + 1) & 1, &s_abort);
-                    };
-                    uint16_t *to = sc + (size_t)buf * 2 * kTChunk * kTScalePad;
+                    if (cg >= kTChunks &&              // the ring's slot has been read
+                        !(ok = warp_wait(smem_u32(&sc_empty[buf]), ((cg / kTChunks) + 1) & 1, &s_abort)))
+                        break;
+                    uint16_t *to = sc + (size_t)buf * 2 * kTRows * kTChunk;
                     const auto both = [&](auto w) {
                         constexpr int W = decltype(w)::value;
-                        return scale_chunk<W>(src0, src1, groups, c * kTChunk, valid0, valid1, to, lane, room);
+                        scale_chunk<W>(src0, groups, c * kTChunk, valid0, to, lane);
+                        scale_chunk<W>(src1, groups, c * kTChunk, valid1, to + kTRows * kTChunk, lane);
                     };
-                    // rows of a multiple of 8 scales are loaded 16 bytes at a time, others as their alignment lets
-                    if (groups % 8 == 0) ok = both(Int<16>());
-                    else if (GPB == 4 || groups % 4 == 0) ok = both(Int<8>());
-                    else if (GPB == 2 || groups % 2 == 0) ok = both(Int<4>());
-                    else ok = both(Int<2>());
-                    if (!ok) break;
+                    // rows of a multiple of 8 scales are copied 16 bytes at a time, others as their alignment lets
+                    if (groups % 8 == 0) both(Int<16>());
+                    else if (GPB == 4 || groups % 4 == 0) both(Int<8>());
+                    else if (GPB == 2 || groups % 2 == 0) both(Int<4>());
+                    else both(Int<2>());
                     if constexpr (F8) {
 #pragma unroll
                         for (int r = lane; r < kTTok; r += 32) {
 #pragma unroll
-                            for (int i = 0; i < KPC; ++i)
-                                xs[((size_t)buf * kTChunk + i) * kTTok + r] =
-                                    r < kept && c * KPC + i < nkb ? __ldg(xsrc + (size_t)r * nkb + c * KPC + i) : 0.0f;
+                            for (int i = 0; i < KPC; ++i) {
+                                const bool some = r < kept && c * KPC + i < nkb;
+                                cp_async_or_zero<4>(smem_u32(xs + ((size_t)buf * kTChunk + i) * kTTok + r),
+                                                    some ? xsrc + (size_t)r * nkb + c * KPC + i : x_scale, some);
+                            }
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sc_full[buf]);
+                    cp_async_arrive(&sc_full[buf]);
                 }
             }
+            cp_async_wait_all();
         }
     } else if (warp < 20) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int quad = warp & 3, h = ((warp - 4) >> 2) & 1, par = (warp - 4) >> 3;
         const uint32_t op0 = tmem + ((uint32_t)(quad * 32) << 16) + 256 + 128 * h + 64 * par;
-        const uint32_t b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[par]);
+        const uint32_t b_afull = smem_u32(&a_full[par]), b_afree = smem_u32(&a_free[2 * par]);
         // The codes of this warp's 32 rows come to a ring of the warp's own, by its own asynchronous copies: no other
         // warp waits for them. Lane l copies chunk l % 4 (16 bytes) of rows l / 4 + 8 i; chunk t of row r stands at
         // t ^ (r / 2 % 4), so that neither the copies nor the reads of a row a lane meet in a bank.
@@ -438,7 +436,7 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 q[i] = *reinterpret_cast<const uint4 *>(src + (n % kTWDepth) * kTWBytes + ((i << 4) ^ swz));
-            if (!warp_wait(b_afree, (n & 1u) ^ 1u, &s_abort)) break;
+            if (n > 0 && !warp_wait(b_afree + 8 * ((n - 1) & 1), (n - 1) >> 1 & 1u, &s_abort)) break;
             tc_fence_after();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -460,7 +458,7 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
         const int row = quad * 32 + lane;            // TMEM lane: row of this half
         const uint32_t d0 = tmem + ((uint32_t)(quad * 32) << 16) + 128 * h;
         const uint32_t b_dfull = smem_u32(&d_full[0]), b_dfree = smem_u32(&d_free[0]);
-        uint32_t cg = 0, n_ex = 0;                   // chunks and tiles so far
+        uint32_t cg = 0, n_ex = 0;                   // chunks and trades so far
         uint32_t d_phase = 0;                        // odd or even use of the accumulators (bits)
         bool ok = true;
         for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
@@ -470,53 +468,50 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
             float acc[kTTok];
 #pragma unroll
             for (int i = 0; i < kTTok; ++i) acc[i] = 0.0f;
-            // the tile's groups into acc: wide for over 32 rows of x, whose accumulators have one slot, not two
-            const auto add_up = [&](auto wide) {
-                constexpr bool kWide = decltype(wide)::value != 0;
+            const auto add_up = [&](auto cap_) {
+                constexpr int CAP = decltype(cap_)::value;
+                using Acc = W4Acc<GPB, CAP>;
                 for (int c = 0; c < groups; c += kTChunk, ++cg) {
                     const uint32_t buf = cg % kTChunks;
                     if (!warp_wait(smem_u32(&sc_full[buf]), (cg / kTChunks) & 1, &s_abort)) return false;
-                    const uint16_t *scr = sc + ((buf * 2 + h) * kTChunk) * kTScalePad + row;
+                    const uint4 s8 = *reinterpret_cast<const uint4 *>(sc + ((buf * 2 + h) * kTRows + row) * kTChunk);
+                    const uint32_t s2[4] = {s8.x, s8.y, s8.z, s8.w};   // this row's 8 scales
                     const float *xr = xs + buf * kTChunk * kTTok;
                     const int n = min(kTChunk, groups - c);
+                    // a chunk's batches: of an even and an odd block in turn, as their MMAs run side by side. A parity's
+                    // batches in a chunk are a multiple of its slots, so that each chunk begins with slot 0.
+                    constexpr int kSteps = kTChunk / 2 / Acc::kBatch, kPerBlock = GPB / Acc::kBatch;
+                    static_assert(kSteps % Acc::kSlots == 0, "slots");
 #pragma unroll
-                    for (int i = 0; i < kTChunk; ++i) {
-                        // the groups of an even and an odd block in turn, as their MMAs run side by side; a chunk has
-                        // four of each, so that each chunk begins with slot 0
-                        const int p = i & 1, group = GPB == 1   ? i
-                                                     : GPB == 2 ? (i & 4) | p << 1 | (i >> 1 & 1)
-                                                                : p << 2 | i >> 1;
-                        const int slot = kWide ? 0 : i >> 1 & 1, which = 2 * p + slot;
+                    for (int i = 0; i < 2 * kSteps; ++i) {
+                        const int p = i & 1, step = i >> 1;
+                        // the batch's first group: block 2 (step / kPerBlock) + p of the chunk
+                        const int group = (2 * (step / kPerBlock) + p) * GPB + step % kPerBlock * Acc::kBatch;
                         if (group < n) {
+                            const int which = 4 * p + step % Acc::kSlots;
                             if (!warp_wait(b_dfull + 8 * which, d_phase >> which & 1u, &s_abort)) return false;
                             d_phase ^= 1u << which;
                             tc_fence_after();
-                            const float ws = __uint_as_float((uint32_t)scr[group * kTScalePad] << 16);
+                            const uint32_t d = d0 + 64 * p + step % Acc::kSlots * (Acc::kBatch * CAP);
                             const float *xg = xr + group / GPB * kTTok;
-                            const uint32_t d = d0 + 64 * p + 32 * slot;
-                            if constexpr (kWide) {   // 16 columns at a time: registers
+                            constexpr int kCols = Acc::kBatch * CAP, kNow = CAP == 64 || kCols < 32 ? 16 : 32;
 #pragma unroll
-                                for (int b = 0; b < kTTok; b += 16) {
-                                    if (b < 48 || rows > 48) {
-                                        uint32_t v[16];
-                                        tmem_ld16(d + b, v);
-                                        tmem_ld_wait();
-                                        add16<F8>(acc + b, v, ws, xg + b);
-                                    }
-                                }
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive_at(b_dfree + 8 * which);
-                            } else {
-                                uint32_t v[32];
-                                tmem_ld16(d, v);
-                                if (rows > 16) tmem_ld16(d + 16, v + 16);
+                            for (int b = 0; b < kCols; b += kNow) {    // some columns at a time: registers
+                                uint32_t v[kNow];
+                                tmem_ld16(d + b, v);
+                                if constexpr (kNow > 16) tmem_ld16(d + b + 16, v + 16);
                                 tmem_ld_wait();
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive_at(b_dfree + 8 * which);
-                                add16<F8>(acc, v, ws, xg);
-                                if (rows > 16) add16<F8>(acc + 16, v + 16, ws, xg + 16);
+                                if (b + kNow >= kCols) {               // the last of them is read
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) mbar_arrive_at(b_dfree + 8 * which);
+                                }
+#pragma unroll
+                                for (int u = 0; u < kNow; u += 16) {
+                                    const int gi = group + (b + u) / CAP;
+                                    const float ws = gi & 1 ? bf16_hi(s2[gi >> 1]) : bf16_lo(s2[gi >> 1]);
+                                    add16<F8>(acc + (b + u) % CAP, v + u, ws, xg + (b + u) % CAP);
+                                }
                             }
                         }
                     }
@@ -525,10 +520,10 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                 }
                 return true;
             };
-            ok = rows <= 32 ? add_up(Int<0>()) : add_up(Int<1>());
+            ok = rows <= 16 ? add_up(Int<16>()) : rows <= 32 ? add_up(Int<32>()) : add_up(Int<64>());
+            if (!ok) break;
 #pragma unroll
             for (int i = 0; i < kTTok; ++i) acc[i] *= kW4Unit<F8>;
-            if (!ok) break;
             uint16_t *out = y + ((size_t)e * a.C + tt * kTTok) * a.N;
             if constexpr (GATE) {
                 // the halves' warps of the same rows trade, 16 columns at a time: each gets the other's sums of 8
@@ -576,8 +571,11 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
         volatile int no_abort = 0;
         if (warp == 0 && lane == 0) {
             atomicOr(status, kStatusWaitGaveUp);
-            for (uint32_t g = (x_issued > SX ? x_issued - SX : 0); g < x_issued; ++g)
-                gemm_wait(smem_u32(&x_full[g % SX]), (g / SX) & 1, &no_abort);
+            for (uint32_t p = 0; p < 2; ++p) {
+                const uint32_t n = p ? x_odd : x_even;
+                for (uint32_t u = n > 2 ? n - 2 : 0; u < n; ++u)
+                    gemm_wait(smem_u32(&x_full[2 * p + (u & 1)]), u >> 1 & 1, &no_abort);
+            }
         }
         if ((warp == 1 || warp == 3) && elect_one()) {   // the lanes that issued the MMAs
             mma_commit(smem_u32(&s_drain[warp >> 1]));
