@@ -465,6 +465,33 @@ def run_path(p: moe_problem, x, logits, s, bufs: dict, out, stream=None, fused=F
     moe_combine(p, bufs["y"], bufs["topk_idx"], bufs["topk_w"], bufs["slot"], out, stream)
 
 
+def run_w4_path(p: moe_problem, gate: moe_gate, x, logits, bias, gate_up, down, bufs: dict, h, out, stream=None):
+    """moe_route_gated -> moe_dispatch -> experts with 4-bit weights (gate and up through SiLU, then down) ->
+    moe_combine for one batch, on one stream. gate_up and down: (w4 shape, w_q, w_scale) of H -> I with
+    MOE_ACT_SILU_GATE and of I -> H; bufs as alloc_buffers(p) makes them; h bf16 [E][C][I], the MLP's inner rows."""
+    import torch
+    b, T, H, E = bufs, p.num_tokens, p.hidden, p.num_experts
+    pd = problem(T, H, E, p.top_k, p.num_ranks, p.capacity, MOE_DTYPE_BF16, p.max_blocks)     # h is bf16
+    if "w4_workspace" not in b:                              # made once for the problem, kept with its buffers
+        n = max(moe_expert_w4_workspace_bytes(p, gate_up[0]), moe_expert_w4_workspace_bytes(pd, down[0]))
+        b["w4_workspace"] = torch.empty(n, dtype=torch.uint8, device=h.device)
+    moe_route_gated(p, gate, logits, bias, b["topk_idx"], b["topk_w"], b["counts"], b["offsets"], b["slot"],
+                    b["rank_counts"], b["dropped"], b["workspace"], stream)
+    moe_dispatch(p, x, b["topk_idx"], b["slot"], b["recv"], b.get("recv_scale"), b["recv_src"], stream)
+    moe_expert_w4(p, gate_up[0], b["recv"], b.get("recv_scale"), b["counts"], gate_up[1], gate_up[2], h,
+                  b["w4_workspace"], stream)
+    moe_expert_w4(pd, down[0], h, None, b["counts"], down[1], down[2], b["y"], b["w4_workspace"], stream)
+    moe_combine(p, b["y"], b["topk_idx"], b["topk_w"], b["slot"], out, stream)
+
+
+def run_gate_backward(p: moe_problem, gate: moe_gate, logits, d_out, bufs: dict, d_y, d_topk_w, d_logits, stream=None):
+    """The way back from moe_combine to the router: moe_combine_backward, then moe_route_gated_backward, on the
+    buffers that a forward pass left. d_y [E][C][H] bf16 is the gradient of the experts' rows."""
+    b = bufs
+    moe_combine_backward(p, b["y"], d_out, b["topk_idx"], b["topk_w"], b["slot"], d_y, d_topk_w, stream)
+    moe_route_gated_backward(p, gate, logits, b["topk_idx"], b["topk_w"], d_topk_w, d_logits, stream)
+
+
 def moe_layer_stand_in(x, out, a: float, busy_fmas: int = 0, stream=None):
     """out = bf16(x * a) (+ busy work that does not change the output)."""
     _check("moe_layer_stand_in", lib().moe_layer_stand_in(_ptr(x), _ptr(out), x.numel(), float(a), int(busy_fmas),

@@ -8,14 +8,16 @@
 // it is, the scale multiplies the sum in fp32, and the only rounding to 16 bits
 // is the output's.
 //
-// Few rows per expert (this file's first kernel): every weight is read once for
-// few products, so the call is bound by HBM. The weights are the 16-row operand
-// of mma.m16n8k16 and 8 rows of x its 8 columns. A block takes 16 rows of one
-// expert's matrix; its warps split the inputs in blocks of 128 and join their
-// sums through shared memory in the warps' order. Within 128 inputs lane
-// (g, t) of the fragment holds bytes 16 t .. 16 t + 15 of row g, one 16-byte
-// load: the packing puts there 8 inputs of each 32, which are the lane's
-// share of two MMA steps, so that every step stays within one group of 32.
+// Few rows per expert (this file; moe_w4_tiles.cu has the kernel for many): every
+// weight is read once for few products, so the call is bound by HBM. The weights are
+// the 16-row operand of mma.m16n8k16 and up to 8 rows of x its 8 columns: a tcgen05
+// tile of 128 rows would leave most SMs without work for one token's few experts.
+// Within 128 inputs lane (g, t) of the fragment holds bytes 16 t .. 16 t + 15 of row
+// g, one 16-byte copy: the packing puts there 8 inputs of each 32, which are the
+// lane's share of two MMA steps, so that every step stays within one group of 32.
+// One token, 8 experts of 2 x 2048 x 7168 (121 MB): 29 us, 0.61 of the copy
+// bandwidth; of it about 7 us are the launch, the wait for the counts and the
+// unequal last round of units. 64 such experts: 0.76.
 #include "moe_w4.cuh"
 
 #include <algorithm>
@@ -127,24 +129,24 @@ struct W4Unit {
 };
 
 // A block takes 16 MT rows of one expert's matrix (with the gate 8 MT outputs) and
-// up to 8 NT of the expert's rows of x; its 8 warps split the inputs in blocks of
+// up to 8 of the expert's rows of x; its 8 warps split the inputs in blocks of
 // 128, warp w the blocks w, w + 8, ... Each warp keeps kW4Depth blocks of codes and
 // scales coming to a ring of its own by asynchronous copies, over the end of one
 // unit of work into the next, so that the joining of the sums at the unit's end does
 // not empty it. A lane reads the codes that it copied itself.
-template <bool F8, int GS, bool GATE, int NT, int MT>
-__global__ void __launch_bounds__(kW4Warps * 32, NT * MT == 1 ? 3 : 2)
+template <bool F8, int GS, bool GATE, int MT>
+__global__ void __launch_bounds__(kW4Warps * 32, MT == 1 ? 3 : 2)
 expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__restrict__ x_scale,
                       const int32_t *__restrict__ counts, const uint8_t *__restrict__ w_q,
                       const uint16_t *__restrict__ w_scale, uint16_t *__restrict__ y) {
-    constexpr int kTokens = 8 * NT, kOut = (GATE ? 8 : 16) * MT, kGroups = 128 / GS;
+    constexpr int kTokens = 8, kOut = (GATE ? 8 : 16) * MT, kGroups = 128 / GS;
     constexpr int kScaleBytes = GS == 32 ? 8 : 4;    // copied for a row's block: its scales, or the word they are in
     constexpr int kStage = MT * kW4Stage;
     __shared__ __align__(16) uint8_t ring[kW4Warps][kW4Depth][kStage];
     __shared__ int rows_of[kMaxExperts], off[kMaxExperts + 1];
     __shared__ uint16_t tile_e[kW4TileMap];
     __shared__ int warp_tot[kW4Warps];
-    __shared__ float4 red[2][kW4Warps][NT * MT][32];
+    __shared__ float4 red[2][kW4Warps][MT][32];
     pdl_enter();
     token_tile_offsets(counts, a.E, a.C, kTokens, rows_of, off, tile_e, warp_tot);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -204,11 +206,9 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
         u.n0 = (int)wk.seg * kOut;
         u.tok0 = (int)(wk.row - off[u.e]) * kTokens;
         u.kept = rows_of[u.e];
-        const uint8_t *px[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)           // columns past the rows read the last row, not stored either
-            px[n] = x + ((size_t)u.e * a.C + min(u.tok0 + 8 * n + g, u.kept - 1)) * x_row + (F8 ? 8 : 16) * t +
-                    (size_t)warp * (F8 ? 128 : 256);
+        // columns past the rows read the last row, and are not stored
+        const uint8_t *px = x + ((size_t)u.e * a.C + min(u.tok0 + g, u.kept - 1)) * x_row + (F8 ? 8 : 16) * t +
+                            (size_t)warp * (F8 ? 128 : 256);
         // which half of its word holds the scale of a group of 128: the same for all of a warp's blocks of a row
         unsigned odd = 0;
         if constexpr (GS == 128) {
@@ -217,20 +217,17 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
                 odd |= (((unsigned)row_a(u.n0, m) * a.nkb + warp) & 1u) << (2 * m) |
                        (((unsigned)row_b(u.n0, m) * a.nkb + warp) & 1u) << (2 * m + 1);
         }
-        float acc[MT][NT][4];
+        float acc[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+            for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
 
         for (int kb = warp; kb < a.nkb; kb += kW4Warps, ++step) {
-            uint32_t b[NT == 1 ? 4 : 1][4];
-            if constexpr (NT == 1) {                 // the block's x, before the wait for its codes
+            uint32_t b[4][4];                        // the block's x, before the wait for its codes
 #pragma unroll
-                for (int j = 0; j < 4; ++j) load_x8<F8>(px[0] + j * (F8 ? 32 : 64), b[j]);
-            }
+            for (int j = 0; j < 4; ++j) load_x8<F8>(px + j * (F8 ? 32 : 64), b[j]);
+            px += kW4Warps * (F8 ? 128 : 256);
             asm volatile("cp.async.wait_group %0;" ::"n"(kW4Depth - 2) : "memory");
             __syncwarp();                            // this block is there, and the last one's slot has been read
             fetch((step + kW4Depth - 1) % kW4Depth);
@@ -244,72 +241,49 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
                 read_scales<GS>(at + 1024 * MT + 128 * m + 8 * g, odd >> (2 * m) & 1u, sa[m]);
                 read_scales<GS>(at + 1024 * MT + 128 * m + 64 + 8 * g, odd >> (2 * m + 1) & 1u, sb[m]);
             }
-            float part[MT][NT][4], blk[F8 ? MT : 1][NT][4];
+            float part[MT][4], blk[F8 ? MT : 1][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint32_t pa[MT][4], pb[MT][4];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    w4_pairs<F8>(j == 0 ? va[m].x : j == 1 ? va[m].y : j == 2 ? va[m].z : va[m].w, pa[m]);
-                    w4_pairs<F8>(j == 0 ? vb[m].x : j == 1 ? vb[m].y : j == 2 ? vb[m].z : vb[m].w, pb[m]);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    uint32_t l[4];
-                    if constexpr (NT == 1) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) l[i] = b[j][i];
-                    } else {
-                        load_x8<F8>(px[n] + j * (F8 ? 32 : 64), l);
-                    }
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        float(&p)[4] = part[m][n];
-                        if (j % (GS / 32) == 0) p[0] = p[1] = p[2] = p[3] = 0.0f;
-                        mma16816<F8>(p, pa[m][0], pb[m][0], pa[m][1], pb[m][1], l[0], l[1]);
-                        mma16816<F8>(p, pa[m][2], pb[m][2], pa[m][3], pb[m][3], l[2], l[3]);
-                        if (j % (GS / 32) == GS / 32 - 1) {
-                            const int q = j / (GS / 32);
-                            float(&to)[4] = F8 ? blk[m][n] : acc[m][n];
-                            if (F8 && q == 0) to[0] = to[1] = to[2] = to[3] = 0.0f;
-                            to[0] = fmaf(p[0], sa[m][q], to[0]);
-                            to[1] = fmaf(p[1], sa[m][q], to[1]);
-                            to[2] = fmaf(p[2], sb[m][q], to[2]);
-                            to[3] = fmaf(p[3], sb[m][q], to[3]);
-                        }
+                    uint32_t pa[4], pb[4];
+                    w4_pairs<F8>(j == 0 ? va[m].x : j == 1 ? va[m].y : j == 2 ? va[m].z : va[m].w, pa);
+                    w4_pairs<F8>(j == 0 ? vb[m].x : j == 1 ? vb[m].y : j == 2 ? vb[m].z : vb[m].w, pb);
+                    float(&p)[4] = part[m];
+                    if (j % (GS / 32) == 0) p[0] = p[1] = p[2] = p[3] = 0.0f;
+                    mma16816<F8>(p, pa[0], pb[0], pa[1], pb[1], b[j][0], b[j][1]);
+                    mma16816<F8>(p, pa[2], pb[2], pa[3], pb[3], b[j][2], b[j][3]);
+                    if (j % (GS / 32) == GS / 32 - 1) {
+                        const int q = j / (GS / 32);
+                        float(&to)[4] = F8 ? blk[m] : acc[m];
+                        if (F8 && q == 0) to[0] = to[1] = to[2] = to[3] = 0.0f;
+                        to[0] = fmaf(p[0], sa[m][q], to[0]);
+                        to[1] = fmaf(p[1], sa[m][q], to[1]);
+                        to[2] = fmaf(p[2], sb[m][q], to[2]);
+                        to[3] = fmaf(p[3], sb[m][q], to[3]);
                     }
                 }
             }
             if constexpr (F8) {
+                const int c0 = min(u.tok0 + 2 * t, u.kept - 1), c1 = min(u.tok0 + 2 * t + 1, u.kept - 1);
+                const float s0 = __ldg(x_scale + ((size_t)u.e * a.C + c0) * a.nkb + kb);
+                const float s1 = __ldg(x_scale + ((size_t)u.e * a.C + c1) * a.nkb + kb);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int c0 = min(u.tok0 + 8 * n + 2 * t, u.kept - 1);
-                    const int c1 = min(u.tok0 + 8 * n + 2 * t + 1, u.kept - 1);
-                    const float s0 = __ldg(x_scale + ((size_t)u.e * a.C + c0) * a.nkb + kb);
-                    const float s1 = __ldg(x_scale + ((size_t)u.e * a.C + c1) * a.nkb + kb);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        acc[m][n][0] = fmaf(blk[m][n][0], s0, acc[m][n][0]);
-                        acc[m][n][1] = fmaf(blk[m][n][1], s1, acc[m][n][1]);
-                        acc[m][n][2] = fmaf(blk[m][n][2], s0, acc[m][n][2]);
-                        acc[m][n][3] = fmaf(blk[m][n][3], s1, acc[m][n][3]);
-                    }
+                for (int m = 0; m < MT; ++m) {
+                    acc[m][0] = fmaf(blk[m][0], s0, acc[m][0]);
+                    acc[m][1] = fmaf(blk[m][1], s1, acc[m][1]);
+                    acc[m][2] = fmaf(blk[m][2], s0, acc[m][2]);
+                    acc[m][3] = fmaf(blk[m][3], s1, acc[m][3]);
                 }
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) px[n] += kW4Warps * (F8 ? 128 : 256);
         }
         // two buffers of sums: a warp that writes unit u + 2's has passed the barrier of unit u + 1, which the
         // readers of unit u's pass after reading
-        float4(&sums)[kW4Warps][NT * MT][32] = red[n_unit & 1];
+        float4(&sums)[kW4Warps][MT][32] = red[n_unit & 1];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                sums[warp][m * NT + n][lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+        for (int m = 0; m < MT; ++m) sums[warp][m][lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
         __syncthreads();
-        if (warp < NT * MT) {                  // one warp for each fragment of 16 matrix rows x 8 rows of x
-            const int m = warp / NT, n = warp % NT;
+        if (warp < MT) {                       // one warp for each fragment of 16 matrix rows
             float4 r = sums[0][warp][lane];
 #pragma unroll
             for (int i = 1; i < kW4Warps; ++i) {
@@ -323,7 +297,7 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
             r.y *= kW4Unit<F8>;
             r.z *= kW4Unit<F8>;
             r.w *= kW4Unit<F8>;
-            const int c = u.tok0 + 8 * n + 2 * t, out = u.n0 + (GATE ? 8 : 16) * m + g;
+            const int c = u.tok0 + 2 * t, out = u.n0 + (GATE ? 8 : 16) * warp + g;
             uint16_t *o = y + ((size_t)u.e * a.C + c) * a.N + out;
             if constexpr (GATE) {
                 if (out < a.N) {
@@ -345,11 +319,11 @@ expert_w4_rows_kernel(W4Args a, const uint8_t *__restrict__ x, const float *__re
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <bool F8, int GS, bool GATE, int NT, int MT>
+template <bool F8, int GS, bool GATE, int MT>
 int launch_rows(const Dims &d, const W4Args &a, cudaStream_t st, const void *x, const float *x_scale,
                 const int32_t *counts, const void *w_q, const void *w_scale, void *y) {
     static PerContext<int> resident_cache;
-    const auto kernel = expert_w4_rows_kernel<F8, GS, GATE, NT, MT>;
+    const auto kernel = expert_w4_rows_kernel<F8, GS, GATE, MT>;
     const int resident = resident_blocks_cached(resident_cache, kernel, kW4Warps * 32);
     constexpr int kOut = (GATE ? 8 : 16) * MT;
     const long long tiles = std::min<long long>((long long)d.T * d.k, (long long)d.E * d.C);
@@ -362,19 +336,17 @@ int launch_rows(const Dims &d, const W4Args &a, cudaStream_t st, const void *x, 
 }
 
 template <bool F8, int GS, bool GATE, typename... A>
-int launch_nt(const Dims &d, const W4Args &a, A... args) {
-    // two fragments of matrix rows to a warp halve what it spends beside the products, where the experts that can
-    // have rows give every resident block a few units all the same
+int launch_mt(const Dims &d, const W4Args &a, A... args) {
+    // Two fragments of matrix rows to a warp halve what it spends beside the products (8 tokens of 64 live experts
+    // of 2 x 2048 x 7168: 189 us, with one 209), where the experts that can have rows still give every resident
+    // block a few units.
     const long long live = std::min<long long>((long long)d.T * d.k, d.E);
-    const bool two = live * a.N / (GATE ? 16 : 32) >= 3LL * sm_count();
-    // one fragment of 8 rows of x where the experts average 4 or fewer: the few with more than 8 are read twice
-    if (std::min(d.T, d.C) <= 8 || (long long)d.T * d.k <= 4LL * d.E)
-        return two ? launch_rows<F8, GS, GATE, 1, 2>(d, a, args...) : launch_rows<F8, GS, GATE, 1, 1>(d, a, args...);
-    return two ? launch_rows<F8, GS, GATE, 2, 2>(d, a, args...) : launch_rows<F8, GS, GATE, 2, 1>(d, a, args...);
+    if (live * a.N / (GATE ? 16 : 32) >= 3LL * sm_count()) return launch_rows<F8, GS, GATE, 2>(d, a, args...);
+    return launch_rows<F8, GS, GATE, 1>(d, a, args...);
 }
 template <bool F8, int GS, typename... A>
 int launch_gate_act(const Dims &d, const W4Args &a, A... args) {
-    return a.M == 2 * a.N ? launch_nt<F8, GS, true>(d, a, args...) : launch_nt<F8, GS, false>(d, a, args...);
+    return a.M == 2 * a.N ? launch_mt<F8, GS, true>(d, a, args...) : launch_mt<F8, GS, false>(d, a, args...);
 }
 template <bool F8, typename... A>
 int launch_group(const Dims &d, const W4Args &a, A... args) {
@@ -404,7 +376,9 @@ W4Args w4_args(const Dims &d, const moe_w4 *w) {
     return a;
 }
 
-// Many rows per expert take the tiles.
+// Many rows per expert take the tiles: from 4 rows on the mean, where some expert can have over 8. 64 experts of
+// 2 x 2048 x 7168, groups of 128, us: 1 row 187 here, 199 with the tiles; 4 rows 195 and 199; 8 rows 214 and 199, and
+// past 8 rows this file's kernel reads the weights again for every 8.
 bool w4_many_rows(const Dims &d) {
     return (d.T < d.C ? d.T : d.C) > 8 && (long long)d.T * d.k >= 4LL * d.E;
 }

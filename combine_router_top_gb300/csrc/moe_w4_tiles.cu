@@ -465,16 +465,17 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
             int e, nt, tt;
             tiles.decode(t, e, nt, tt);
             const int rows = min(min(__ldg(counts + e), a.C) - tt * kTTok, kTTok);
-            float acc[kTTok];
-#pragma unroll
-            for (int i = 0; i < kTTok; ++i) acc[i] = 0.0f;
-            const auto add_up = [&](auto cap_) {
+            const auto tile = [&](auto cap_) {       // with sums for CAP columns only: registers
                 constexpr int CAP = decltype(cap_)::value;
                 using Acc = W4Acc<GPB, CAP>;
+                float acc[CAP];
+#pragma unroll
+                for (int i = 0; i < CAP; ++i) acc[i] = 0.0f;
                 for (int c = 0; c < groups; c += kTChunk, ++cg) {
                     const uint32_t buf = cg % kTChunks;
                     if (!warp_wait(smem_u32(&sc_full[buf]), (cg / kTChunks) & 1, &s_abort)) return false;
                     const uint4 s8 = *reinterpret_cast<const uint4 *>(sc + ((buf * 2 + h) * kTRows + row) * kTChunk);
+                    const uint16_t *s1 = sc + ((buf * 2 + h) * kTRows + row) * kTChunk;
                     const uint32_t s2[4] = {s8.x, s8.y, s8.z, s8.w};   // this row's 8 scales
                     const float *xr = xs + buf * kTChunk * kTTok;
                     const int n = min(kTChunk, groups - c);
@@ -482,7 +483,7 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                     // batches in a chunk are a multiple of its slots, so that each chunk begins with slot 0.
                     constexpr int kSteps = kTChunk / 2 / Acc::kBatch, kPerBlock = GPB / Acc::kBatch;
                     static_assert(kSteps % Acc::kSlots == 0, "slots");
-#pragma unroll
+#pragma unroll(CAP == 64 ? 2 : 8)
                     for (int i = 0; i < 2 * kSteps; ++i) {
                         const int p = i & 1, step = i >> 1;
                         // the batch's first group: block 2 (step / kPerBlock) + p of the chunk
@@ -494,7 +495,7 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                             tc_fence_after();
                             const uint32_t d = d0 + 64 * p + step % Acc::kSlots * (Acc::kBatch * CAP);
                             const float *xg = xr + group / GPB * kTTok;
-                            constexpr int kCols = Acc::kBatch * CAP, kNow = CAP == 64 || kCols < 32 ? 16 : 32;
+                            constexpr int kCols = Acc::kBatch * CAP, kNow = kCols < 32 ? 16 : 32;
 #pragma unroll
                             for (int b = 0; b < kCols; b += kNow) {    // some columns at a time: registers
                                 uint32_t v[kNow];
@@ -509,7 +510,7 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
 #pragma unroll
                                 for (int u = 0; u < kNow; u += 16) {
                                     const int gi = group + (b + u) / CAP;
-                                    const float ws = gi & 1 ? bf16_hi(s2[gi >> 1]) : bf16_lo(s2[gi >> 1]);
+                                    const float ws = CAP == 64 ? bf16_lo((uint32_t)s1[gi]) : gi & 1 ? bf16_hi(s2[gi >> 1]) : bf16_lo(s2[gi >> 1]);
                                     add16<F8>(acc + (b + u) % CAP, v + u, ws, xg + (b + u) % CAP);
                                 }
                             }
@@ -518,48 +519,46 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sc_empty[buf]);
                 }
+#pragma unroll
+                for (int i = 0; i < CAP; ++i) acc[i] *= kW4Unit<F8>;
+                uint16_t *const out = y + ((size_t)e * a.C + tt * kTTok) * a.N;
+                if constexpr (GATE) {
+                    // the halves' warps of the same rows trade, 16 columns at a time: each gets the other's sums of 8
+                    // of them, and finishes those
+                    const int n = nt * kOut + row;
+#pragma unroll
+                    for (int b = 0; b < CAP; b += 16) {
+                        if (b >= rows) break;
+                        if (!warp_wait(smem_u32(&ex_free[quad]), (n_ex & 1u) ^ 1u, &s_abort)) return false;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            ex[(8 * (1 - h) + i) * kTRows + row] = h == 0 ? acc[b + 8 + i] : acc[b + i];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ex_full[quad]);
+                        if (!warp_wait(smem_u32(&ex_full[quad]), n_ex & 1u, &s_abort)) return false;
+                        float o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float other = ex[(8 * h + i) * kTRows + row];
+                            o[i] = h == 0 ? silu(acc[b + i]) * other : silu(other) * acc[b + 8 + i];
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ex_free[quad]);
+                        ++n_ex;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (b + 8 * h + i < rows && n < a.N)
+                                put_bf16(out + (size_t)(b + 8 * h + i) * a.N + n, o[i]);
+                    }
+                } else {
+                    const int n = nt * kOut + h * kTRows + row;
+#pragma unroll
+                    for (int i = 0; i < CAP; ++i)
+                        if (i < rows && n < a.N) put_bf16(out + (size_t)i * a.N + n, acc[i]);
+                }
                 return true;
             };
-            ok = rows <= 16 ? add_up(Int<16>()) : rows <= 32 ? add_up(Int<32>()) : add_up(Int<64>());
-            if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < kTTok; ++i) acc[i] *= kW4Unit<F8>;
-            uint16_t *out = y + ((size_t)e * a.C + tt * kTTok) * a.N;
-            if constexpr (GATE) {
-                // the halves' warps of the same rows trade, 16 columns at a time: each gets the other's sums of 8
-                // of them, and finishes those
-                const int n = nt * kOut + row;
-#pragma unroll
-                for (int b = 0; b < kTTok; b += 16) {
-                    if (b >= rows || !ok) break;
-                    ok = warp_wait(smem_u32(&ex_free[quad]), (n_ex & 1u) ^ 1u, &s_abort);
-                    if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ex[(8 * (1 - h) + i) * kTRows + row] = h == 0 ? acc[b + 8 + i] : acc[b + i];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ex_full[quad]);
-                    ok = warp_wait(smem_u32(&ex_full[quad]), n_ex & 1u, &s_abort);
-                    if (!ok) break;
-                    float o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float other = ex[(8 * h + i) * kTRows + row];
-                        o[i] = h == 0 ? silu(acc[b + i]) * other : silu(other) * acc[b + 8 + i];
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ex_free[quad]);
-                    ++n_ex;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (b + 8 * h + i < rows && n < a.N) put_bf16(out + (size_t)(b + 8 * h + i) * a.N + n, o[i]);
-                }
-                if (!ok) break;
-            } else {
-                const int n = nt * kOut + h * kTRows + row;
-#pragma unroll
-                for (int i = 0; i < kTTok; ++i)
-                    if (i < rows && n < a.N) put_bf16(out + (size_t)i * a.N + n, acc[i]);
-            }
+            ok = rows <= 16 ? tile(Int<16>()) : rows <= 32 ? tile(Int<32>()) : tile(Int<64>());
         }
     }
     pdl_launch_dependents();

@@ -384,7 +384,7 @@ int moe_route_gated(const moe_problem *p, const moe_gate *gate, const void *logi
  * the same gate and logits; a choice that is no pair, and a masked expert, has
  * gradient 0, whatever d_topk_w holds for it. logits may be NULL for
  * a renormalised softmax, whose weights say all. Indices outside [0, E) are
- * skipped. The bounds of the gate and the alignment are those of
+ * skipped. d_logits does not overlap the inputs. The bounds of the gate and the alignment are those of
  * moe_route_gated, d_logits as logits; the capacity of p is not used. */
 int moe_route_gated_backward(const moe_problem *p, const moe_gate *gate, const void *logits,
                              const int32_t *topk_idx, const float *topk_w, const float *d_topk_w,
@@ -427,8 +427,9 @@ size_t moe_expert_w4_workspace_bytes(const moe_problem *p, const moe_w4 *w);
  *   r[m] = sum_g w_scale[e][m][g] * sum_{i in group g} x[e][c][i] * (q[e][m][i] - 8)
  *   y[e][c][n] = bf16(r[n]), or bf16(silu(r[n]) * r[N + n]),  silu(v) = v / (1 + exp(-v))
  * for c < min(counts[e], C); other rows of y are not written and other rows of
- * x not used. The products are exact, the sums in fp32 (an fp8 row's scale is
- * applied to each 128-input block's sum), rounded once.
+ * x not used. The products are exact, the sums in fp32: each group's sum is
+ * multiplied by its scale (and by the fp8 row's block scale) in fp32 and added
+ * to the row's; rounded once, to bf16.
  * x: the problem's dispatch_dtype says which: bf16 [E][C][K] with x_scale NULL,
  *   or e4m3 [E][C][K] with x_scale f32 [E][C][K/128] as moe_dispatch writes
  *   them; the hidden size of p itself is not used. Two calls make an expert's
@@ -437,8 +438,10 @@ size_t moe_expert_w4_workspace_bytes(const moe_problem *p, const moe_w4 *w);
  *   bytes): the little-endian 32-bit word 4 t + j of a block (t, j < 4) holds
  *   inputs 32 j + 8 t + i, i < 8, input i's code at bit 4 (i / 2) + 16 (i % 2).
  *   w_scale bf16 [E][M][K/group].
- * One row to many rows for an expert: for few rows the call is bound by
- * reading the weights of the experts that have any. counts is moe_route's.
+ * One row to many rows for an expert. Experts without rows are not read. counts
+ * is moe_route's. MOE_ERR_UNSUPPORTED for work past 2^31 blocks of 128 inputs x
+ * 256 matrix rows x 64 rows. Waits on the kernel's own copies are bounded (as for
+ * the grouped GEMMs; moe_device_status).
  * x, w_q, w_scale, y and workspace 16-byte aligned; max_blocks caps the grid.
  * Launched as a programmatic dependent of the previous kernel. */
 int moe_expert_w4(const moe_problem *p, const moe_w4 *w, const void *x, const float *x_scale,

@@ -122,6 +122,14 @@ def test_the_batch_that_the_problem_states_changes_no_result_past_rounding(M, T,
     check(M, [7, 0, 4, 30], 48, 896, 152, 64, True, fp8, 5, T=T)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_long_rows_and_many_tiles_to_a_block(M, group, fp8):
+    """29 blocks of inputs (an odd number, over the rings' depths) and nine or more tiles of 1 to 64 rows for each of two
+    thread blocks: what is counted per block, tile and use goes around several times."""
+    check(M, [20, 33, 5, 64, 1, 0, 17, 100], 100, 3712, 264, group, True, fp8, 6, T=4096, max_blocks=2)
+
+
 @pytest.mark.parametrize("gate", [False, True])
 def test_no_rows_at_all(M, gate):
     check(M, [0, 0, 0], 8, 256, 16, 64, gate, False)
