@@ -26,6 +26,12 @@
 //   warps 4-19  four TMEM quadrants x two halves x even and odd blocks: copy the codes
 //               of their 32 rows to rings of their own and turn them into operands;
 //   warps 20-27 four quadrants x two halves: add up the groups' sums, and write y.
+// Bound by the conversion of codes (144 instructions of a warp for 32 rows x 128
+// inputs, half of them on the half-rate ALU pipe) and by the chain operand -> MMA ->
+// sums -> accumulator; the split into these roles is what overlaps the links. 256
+// experts of 2 x 2048 x 7168 with 32 rows each, groups of 128: 969 us, 0.61 of the
+// copy bandwidth; 32 such experts 136 us with 32 rows, 122 with 16, 185 with 64;
+// groups of 32 and 16 rows 140 us.
 // Every mbarrier wait is bounded; one that gives up raises the status word and an
 // abort flag, the CTA drains what it has in flight, frees its TMEM and returns.
 #include "moe_tc.cuh"
