@@ -472,8 +472,8 @@ def run_w4_path(p: moe_problem, gate: moe_gate, x, logits, bias, gate_up, down, 
     import torch
     b, T, H, E = bufs, p.num_tokens, p.hidden, p.num_experts
     pd = problem(T, H, E, p.top_k, p.num_ranks, p.capacity, MOE_DTYPE_BF16, p.max_blocks)     # h is bf16
-    if "w4_workspace" not in b:                              # made once for the problem, kept with its buffers
-        n = max(moe_expert_w4_workspace_bytes(p, gate_up[0]), moe_expert_w4_workspace_bytes(pd, down[0]))
+    n = max(moe_expert_w4_workspace_bytes(p, gate_up[0]), moe_expert_w4_workspace_bytes(pd, down[0]))
+    if "w4_workspace" not in b or b["w4_workspace"].numel() < n:     # made once, kept with the problem's buffers
         b["w4_workspace"] = torch.empty(n, dtype=torch.uint8, device=h.device)
     moe_route_gated(p, gate, logits, bias, b["topk_idx"], b["topk_w"], b["counts"], b["offsets"], b["slot"],
                     b["rank_counts"], b["dropped"], b["workspace"], stream)

@@ -85,3 +85,22 @@ def test_forward_and_back(M, T, fp8):
     dl, _ = P.gate_backward(logits.cpu().numpy(), idx, ok, dw, True, True, 2.5)
     assert rel(d_w.double().cpu().numpy(), dw) < 2.0 ** -14
     assert rel(d_l.double().cpu().numpy(), dl) < 2.0 ** -14
+
+
+def test_buffers_of_a_larger_batch_serve_smaller_ones_and_larger_again(M):
+    """The path's workspace grows with the problem that needs more of it."""
+    H, E, k, C = 128, 4, 2, 32
+    g = torch.Generator(device=DEV).manual_seed(7)
+    w = (M.w4(H, H, 64), torch.randint(0, 256, (E, H, H // 2), dtype=torch.uint8, device=DEV, generator=g),
+         torch.full((E, H, H // 64), 0.02, dtype=torch.bfloat16, device=DEV))
+    x = torch.randn((40, H), device=DEV, generator=g).to(torch.bfloat16)
+    logits = torch.randn((40, E), device=DEV, generator=g)
+    b = M.alloc_buffers(M.problem(40, H, E, k, 1, C, 1), DEV)
+    h = torch.empty((E, C, H), dtype=torch.bfloat16, device=DEV)
+    outs = {}
+    for T in (2, 40, 2, 40):
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+        M.run_w4_path(M.problem(T, H, E, k, 1, C, 1), M.gate(), x, logits, None, w, w, b, h, out)
+        torch.cuda.synchronize()
+        assert torch.equal(outs.setdefault(T, out), out)
+    assert rel(outs[40][:2].double().cpu().numpy(), outs[2].double().cpu().numpy()) < 3 * 2.0 ** -8
