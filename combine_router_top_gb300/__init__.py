@@ -465,16 +465,33 @@ def run_path(p: moe_problem, x, logits, s, bufs: dict, out, stream=None, fused=F
     moe_combine(p, bufs["y"], bufs["topk_idx"], bufs["topk_w"], bufs["slot"], out, stream)
 
 
+def _w4_workspace(bufs: dict, n: int, device, stream: int):
+    """bufs["w4_workspace"] of at least n bytes for work on the stream with this handle: made once, kept with the
+    problem's buffers. Its memory belongs to the stream that it was made for, so that a dropped one is only handed on
+    behind that stream's work; use on another stream is recorded with the allocator."""
+    import torch
+
+    def torch_stream():                                  # ExternalStream takes no default stream
+        return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    ws = bufs.get("w4_workspace")
+    if ws is None or ws.numel() < n:
+        with torch.cuda.stream(torch_stream()):
+            bufs["w4_workspace"] = torch.empty(n, dtype=torch.uint8, device=device)
+        bufs["w4_workspace_stream"] = stream
+    elif bufs.get("w4_workspace_stream") != stream:
+        ws.record_stream(torch_stream())
+
+
 def run_w4_path(p: moe_problem, gate: moe_gate, x, logits, bias, gate_up, down, bufs: dict, h, out, stream=None):
     """moe_route_gated -> moe_dispatch -> experts with 4-bit weights (gate and up through SiLU, then down) ->
     moe_combine for one batch, on one stream. gate_up and down: (w4 shape, w_q, w_scale) of H -> I with
-    MOE_ACT_SILU_GATE and of I -> H; bufs as alloc_buffers(p) makes them; h bf16 [E][C][I], the MLP's inner rows."""
-    import torch
+    MOE_ACT_SILU_GATE and of I -> H; bufs as alloc_buffers(p) makes them, to which the path adds the experts' workspace
+    (which grows with the problem that needs more); h bf16 [E][C][I], the MLP's inner rows."""
     b, T, H, E = bufs, p.num_tokens, p.hidden, p.num_experts
     pd = problem(T, H, E, p.top_k, p.num_ranks, p.capacity, MOE_DTYPE_BF16, p.max_blocks)     # h is bf16
     n = max(moe_expert_w4_workspace_bytes(p, gate_up[0]), moe_expert_w4_workspace_bytes(pd, down[0]))
-    if "w4_workspace" not in b or b["w4_workspace"].numel() < n:     # made once, kept with the problem's buffers
-        b["w4_workspace"] = torch.empty(n, dtype=torch.uint8, device=h.device)
+    stream = _stream(stream)
+    _w4_workspace(b, n, h.device, stream)
     moe_route_gated(p, gate, logits, bias, b["topk_idx"], b["topk_w"], b["counts"], b["offsets"], b["slot"],
                     b["rank_counts"], b["dropped"], b["workspace"], stream)
     moe_dispatch(p, x, b["topk_idx"], b["slot"], b["recv"], b.get("recv_scale"), b["recv_src"], stream)
