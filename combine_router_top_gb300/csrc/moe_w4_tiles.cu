@@ -376,9 +376,10 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                         scale_chunk<W>(src1, groups, c * kTChunk, valid1, to + kTRows * kTChunk, lane);
                     };
                     // rows of a multiple of 8 scales are copied 16 bytes at a time, others as their alignment lets
+                    const bool odd_rows = GPB == 1 && groups % 2 != 0;
                     if (groups % 8 == 0) both(Int<16>());
                     else if (GPB == 4 || groups % 4 == 0) both(Int<8>());
-                    else if (GPB == 2 || groups % 2 == 0) both(Int<4>());
+                    else if (!odd_rows) both(Int<4>());
                     else both(Int<2>());
                     if constexpr (F8) {
 #pragma unroll
@@ -391,7 +392,14 @@ expert_w4_tiles_kernel(const __grid_constant__ W4Maps maps, W4Args a, const uint
                             }
                         }
                     }
-                    cp_async_arrive(&sc_full[buf]);
+                    if (odd_rows) {
+                        // scales stored by this thread itself: only an ordinary arrive releases those to the readers,
+                        // after the row scales' copies
+                        cp_async_wait_all();
+                        mbar_arrive(&sc_full[buf]);
+                    } else {
+                        cp_async_arrive(&sc_full[buf]);
+                    }
                 }
             }
             cp_async_wait_all();
