@@ -256,7 +256,8 @@ route_chunk_scan_kernel(int n_chunks, int E, const int32_t *__restrict__ chunk_s
 // chunk; slot = base + rank in tile (or -1 at or past C). The last CTA also
 // adds its own tile to get the totals and writes counts, offsets,
 // rank_counts and dropped.
-__global__ void __launch_bounds__(1024, 2)          // 32 registers: two blocks to an SM
+template <int BLOCKS_PER_SM>
+__global__ void __launch_bounds__(1024, BLOCKS_PER_SM)
 route_finalize_kernel(int T, int n_tiles, int E, int k, int R, int C, const int32_t *__restrict__ tile_counts,
                       const int32_t *__restrict__ chunk_base,
                       const int32_t *__restrict__ topk_idx, int32_t *__restrict__ slot,
@@ -398,9 +399,15 @@ int launch_route_slots_large(const Dims &d, cudaStream_t st, int32_t *wc, const 
             return MOE_ERR_CUDA;
         chunk_base = bases;
     }
-    if (launch_pdl(route_finalize_kernel, n_tiles, 1024, st, d.T, n_tiles, d.E, d.k, d.R, d.C,
-                   static_cast<const int32_t *>(wc), chunk_base, topk_idx, slot, counts, offsets, rank_counts,
-                   dropped) != cudaSuccess)
+    // The finaliser's registers by how many of its blocks an SM gets. One: 50 registers keep more of the counts'
+    // loads in flight (4096 x 256: moe_route 13.5 us, with 32 registers 15.6; 1032 x 256: 8.0 and 8.7). More than
+    // one: 32 registers let two run together (65536 x 256: 76.4 us, one at a time 88.2; 8192 x 64: 10.2 and 12.0).
+    // Past 512 experts a thread sums an expert's counts alone, and a second round of blocks still costs less than
+    // fewer loads in flight (6000 x 1024, 188 tiles: 39.8 us, two together 40.3; 8192: 41.8 and 40.3).
+    const int one_each = d.E > 512 ? sm_count() + sm_count() / 3 : sm_count();
+    const auto finalize = n_tiles <= one_each ? route_finalize_kernel<1> : route_finalize_kernel<2>;
+    if (launch_pdl(finalize, n_tiles, 1024, st, d.T, n_tiles, d.E, d.k, d.R, d.C, static_cast<const int32_t *>(wc),
+                   chunk_base, topk_idx, slot, counts, offsets, rank_counts, dropped) != cudaSuccess)
         return MOE_ERR_CUDA;
     return MOE_OK;
 }
