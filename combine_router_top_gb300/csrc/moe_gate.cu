@@ -70,6 +70,12 @@ __device__ __forceinline__ bool open_logit(float l) { return l > kMaskLogit; }
 
 // 1 / (1 + exp(-l)): expf and the correctly rounded reciprocal, 1 at +inf, 0 once exp(-l) overflows.
 __device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
+// sigmoid(l) exp(-top) for a whole number top <= 0 with l <= top, or l positive and top 0, as exp(l - top) / (1 + exp(l))
+// where l is not positive: the factor leaves quotients of a row's sigmoids as they are and keeps them from underflowing
+// with their row. l - top is exact wherever its exp is not 0: both are multiples of l's last place, or near each other.
+__device__ __forceinline__ float sigmoid_above(float l, float top) {
+    return l > 0.0f ? sigmoid(l) : __fdiv_rn(expf(__fsub_rn(l, top)), __fadd_rn(1.0f, expf(l)));
+}
 // logit_key of a number (no NaN) in three instructions: -0 becomes +0 by adding 0.
 __device__ __forceinline__ uint32_t number_key(float f) {
     const uint32_t u = __float_as_uint(__fadd_rn(f, 0.0f));
@@ -322,8 +328,7 @@ __device__ __forceinline__ void warp_gate(const T *__restrict__ row, const float
     if (a.renorm) {
         const uint32_t m = __reduce_max_sync(kFull, ok ? logit_key(f) : 0u);
         const float most = key_logit(m);                               // the largest chosen logit
-        // below -30 a sigmoid is exp(l) to the last bit, so the quotients are a softmax's, which cannot underflow
-        if (ok) s = a.sigmoid && most > -30.0f ? sigmoid(f) : exp_below(f, most);
+        if (ok) s = a.sigmoid ? sigmoid_above(f, ceilf(fminf(most, 0.0f))) : exp_below(f, most);
         const float total = lanes_sum<32>(s);                             // 0 only where nothing was chosen
         s = ok ? __fdiv_rn(s, total) : 0.0f;
     } else if (ok) {

@@ -348,7 +348,8 @@ typedef struct moe_gate {
  *   topk_idx[t][0..k-1]: the k largest keys of those groups, largest first,
  *     equal keys to the lower expert index;
  *   topk_w[t][j] = scale * s_{e_j}, divided by sum_i s_{e_i} if renormalise is
- *     set (no underflow: rows of very low logits have their quotients too).
+ *     set (the quotients, down to 2^-126, are formed in full however low the
+ *     row's logits are, also where a sigmoid itself would be 0).
  * The bias steers the choice only (balance between the experts); the weights
  * come from the scores without it. bias: device f32[E] or NULL.
  * Masked experts. An expert whose logit is -inf, NaN or at most the lowest

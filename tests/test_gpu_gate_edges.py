@@ -1,0 +1,28 @@
+"""The gated route and its gradient at the ends of their ranges, against the plain form in 64 bits.
+
+Weights of a renormalised sigmoid: a score takes exp (2 ulp, twice, the second at most halved), a sum and a division, 8
+roundings of 2^-24; the sum over the choices the same and 5 more, the quotient and the scale 2: 23 x 2^-24, under 2^-19.
+Gradients: the bar of test_gpu_gate."""
+import numpy as np
+import pytest
+
+import plain64 as P
+from test_gpu_gate import BASE, M, check_backward, route  # noqa: F401  (M is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("top", [3.0, 0.25, 0.0, -0.5, -7.0, -29.0, -29.99, -30.0, -31.5, -88.0, -1000.25])
+@pytest.mark.parametrize("below", [2.0, 40.0, 66.0, 80.0])
+def test_renormalised_sigmoids_far_below_the_best(M, top, below):  # noqa: F811
+    """The quotient of a choice e^-below under the row's best is that, although its own sigmoid may be 0 in fp32."""
+    rng = np.random.default_rng(int(below))
+    l = (top - below * rng.random((50, 16))).astype(np.float32)
+    l[:, 5], l[:, 11] = top, top - below
+    c = {**BASE, "scale": 2.5}
+    got = route(M, l, None, 16, c)
+    idx, ok, w, _ = P.gate(l, None, 16, **c)
+    assert ok.all() and np.array_equal(got["topk_idx"], idx)
+    assert (np.abs(got["topk_w"] - w) <= 2.0 ** -19 * w).all(), np.abs(got["topk_w"] / w - 1).max()
+    fwd, _, ok, ref = check_backward(M, l, None, 16, c, False, 3)
+    assert (fwd["topk_w"] > 0).all() and (ref != 0).all()
