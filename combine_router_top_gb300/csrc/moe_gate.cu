@@ -19,6 +19,8 @@
 // by the choice's instructions (16384 tokens, bf16: 36.6 us, 1126 of a warp a token).
 #include <math.h>
 
+#include <algorithm>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -396,6 +398,13 @@ gate_kernel(const T *__restrict__ logits, const float *__restrict__ bias, GateAr
 
 // ---- gradient -----------------------------------------------------------------
 
+// The factor on the weights, and its reciprocal in two steps that stay in range for every finite scale: w / scale =
+// w up inv with up a power of two (so that w up is exact) and |scale| up within [1, 4), or 2^-23 and more for subnormal
+// scales, whose own reciprocal overflows.
+struct GateScale {
+    float scale, up, inv;
+};
+
 // LP lanes to a token, NV 16-byte words of its row to a lane. The lanes form the
 // chosen experts' gradients between them, then write the row whole (zeros, or
 // -a s_e dot for a softmax over all experts) and the chosen places after it, within
@@ -405,11 +414,10 @@ template <typename T, bool DENSE, int LP, int NV>
 __global__ void __launch_bounds__(256)
 gate_backward_kernel(const T *__restrict__ logits, const int32_t *__restrict__ topk_idx,
                      const float *__restrict__ topk_w, const float *__restrict__ d_topk_w, T *__restrict__ d_logits,
-                     int T_, int E, int k, int sigm, int renorm, float scale) {
+                     int T_, int E, int k, int sigm, int renorm, GateScale by) {
     constexpr int kVec = 16 / (int)sizeof(T), kTokens = 256 / LP, kPer = LP < kMaxTopK ? kMaxTopK / LP : 1;
     pdl_enter();
     const int sub = threadIdx.x % LP;
-    const float inv = __fdiv_rn(1.0f, scale);
     const int words = E / kVec;
     for (int t0 = blockIdx.x * kTokens; t0 < T_; t0 += gridDim.x * kTokens) {
         const int t = t0 + threadIdx.x / LP;
@@ -437,9 +445,9 @@ gate_backward_kernel(const T *__restrict__ logits, const int32_t *__restrict__ t
                 if (e[i] >= 0 && sigm) f[i] = to_f32(row[e[i]]);
                 if (e[i] < 0 || w[i] == 0.0f) w[i] = gw[i] = 0.0f;     // no pair: whatever d_topk_w holds
             }
-            part = __fmaf_rn(w[i], gw[i], part);
+            part = __fmaf_rn(__fmul_rn(w[i], by.up), gw[i], part);
         }
-        const float dot = (DENSE || renorm) ? __fmul_rn(lanes_sum<LP>(part), inv) : 0.0f;
+        const float dot = (DENSE || renorm) ? __fmul_rn(lanes_sum<LP>(part), by.inv) : 0.0f;
         if constexpr (DENSE) {
             float top = -INFINITY, total = 0.0f;
 #pragma unroll
@@ -463,7 +471,7 @@ gate_backward_kernel(const T *__restrict__ logits, const int32_t *__restrict__ t
                 }
             }
             total = lanes_sum<LP>(total);
-            const float c = total > 0.0f ? __fdiv_rn(-__fmul_rn(scale, dot), total) : 0.0f;
+            const float c = total > 0.0f ? __fdiv_rn(-__fmul_rn(by.scale, dot), total) : 0.0f;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 if (live && v * LP + sub < words) {
@@ -497,10 +505,9 @@ template <typename T, bool DENSE>
 __global__ void __launch_bounds__(256)
 gate_backward_odd_kernel(const T *__restrict__ logits, const int32_t *__restrict__ topk_idx,
                          const float *__restrict__ topk_w, const float *__restrict__ d_topk_w,
-                         T *__restrict__ d_logits, int T_, int E, int k, int sigm, int renorm, float scale) {
+                         T *__restrict__ d_logits, int T_, int E, int k, int sigm, int renorm, GateScale by) {
     pdl_enter();
     const int lane = threadIdx.x & 31;
-    const float inv = __fdiv_rn(1.0f, scale);
     for (int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < T_; t += gridDim.x * (blockDim.x >> 5)) {
         const T *row = logits + (size_t)t * E;
         T *out = d_logits + (size_t)t * E;
@@ -514,7 +521,7 @@ gate_backward_odd_kernel(const T *__restrict__ logits, const int32_t *__restrict
             if (e >= 0 && sigm) f = to_f32(row[e]);
             if (e < 0 || w == 0.0f) w = gw = 0.0f;
         }
-        const float dot = (DENSE || renorm) ? __fmul_rn(lanes_sum<32>(__fmul_rn(w, gw)), inv) : 0.0f;
+        const float dot = (DENSE || renorm) ? __fmul_rn(lanes_sum<32>(__fmul_rn(__fmul_rn(w, by.up), gw)), by.inv) : 0.0f;
         if constexpr (DENSE) {
             float top = -INFINITY, total = 0.0f;
             for (int i = lane; i < E; i += 32) top = fmaxf(top, to_f32(row[i]));
@@ -524,7 +531,7 @@ gate_backward_odd_kernel(const T *__restrict__ logits, const int32_t *__restrict
                 if (open_logit(x)) total = __fadd_rn(total, exp_below(x, top));
             }
             total = lanes_sum<32>(total);
-            const float c = total > 0.0f ? __fdiv_rn(-__fmul_rn(scale, dot), total) : 0.0f;
+            const float c = total > 0.0f ? __fdiv_rn(-__fmul_rn(by.scale, dot), total) : 0.0f;
             for (int i = lane; i < E; i += 32) {
                 const float x = to_f32(row[i]);
                 from_f32(out + i, open_logit(x) ? __fmul_rn(exp_below(x, top), c) : 0.0f);
@@ -638,9 +645,11 @@ int launch_backward(const Dims &d, const GateArgs &a, cudaStream_t st, const voi
                     const float *w, const float *dw, void *out) {
     const T *l = static_cast<const T *>(logits);
     T *o = static_cast<T *>(out);
+    const float up = ldexpf(1.0f, -std::max(-126, std::min(126, ilogbf(a.scale))));
+    const GateScale by = {a.scale, up, 1.0f / (a.scale * up)};
     if (!a.sigmoid && !a.renorm)
-        return launch_backward_rows<T, true>(d, st, l, idx, w, dw, o, d.T, d.E, d.k, a.sigmoid, a.renorm, a.scale);
-    return launch_backward_rows<T, false>(d, st, l, idx, w, dw, o, d.T, d.E, d.k, a.sigmoid, a.renorm, a.scale);
+        return launch_backward_rows<T, true>(d, st, l, idx, w, dw, o, d.T, d.E, d.k, a.sigmoid, a.renorm, by);
+    return launch_backward_rows<T, false>(d, st, l, idx, w, dw, o, d.T, d.E, d.k, a.sigmoid, a.renorm, by);
 }
 
 }  // namespace

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 import plain64 as P
-from test_gpu_gate import BASE, M, check_backward, route  # noqa: F401  (M is a fixture)
+from test_gpu_gate import BASE, M, backward, check_backward, route  # noqa: F401  (M is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +26,23 @@ def test_renormalised_sigmoids_far_below_the_best(M, top, below):  # noqa: F811
     assert (np.abs(got["topk_w"] - w) <= 2.0 ** -19 * w).all(), np.abs(got["topk_w"] / w - 1).max()
     fwd, _, ok, ref = check_backward(M, l, None, 16, c, False, 3)
     assert (fwd["topk_w"] > 0).all() and (ref != 0).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E", [24, 27])
+@pytest.mark.parametrize("scale", [1e-30, 1e-38, -1.1e-39, 1e-44, 1e30, -3e38])
+def test_gradients_at_scales_of_any_size(M, scale, E, renorm, sigmoid):  # noqa: F811
+    """Every finite scale but 0 has finite gradients. Below 2^-126 the weights themselves are held to 2^-149, which moves
+    dot by that over the scale: the bar takes one such step of each weight, for the gradient and for dot."""
+    rng = np.random.default_rng(5)
+    T, k = 60, 5
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    scale = float(np.float32(scale))
+    c = {**BASE, "sigmoid": sigmoid, "renorm": renorm, "scale": scale}
+    fwd = route(M, l, None, k, c)
+    d_w = (0.1 * rng.standard_normal((T, k))).astype(np.float32)
+    got = backward(M, l, fwd["topk_idx"], fwd["topk_w"], d_w, c, False)
+    ref, mag = P.gate_backward(l, fwd["topk_idx"], np.ones((T, k), bool), d_w, sigmoid, renorm, scale)
+    step = 2.0 ** -149 * np.abs(d_w).sum(1)[:, None] * 2 + 4 * 2.0 ** -149
+    assert (np.abs(got - ref) <= (48 + E / 32) * 2.0 ** -24 * mag + step).all(), np.abs(got - ref).max()
