@@ -382,8 +382,10 @@ int moe_route_gated(const moe_problem *p, const moe_gate *gate, const void *logi
  *   softmax:               d_logits[e]   = a s_e ((g_j if e = e_j, else 0) - dot), every e
  * and 0 elsewhere: every element of d_logits[T][E] (logits_type) is written,
  * rounded once from fp32. topk_idx and topk_w are moe_route_gated's outputs for
- * the same gate and logits; a choice that is no pair, and a masked expert, has
- * gradient 0, whatever d_topk_w holds for it. logits may be NULL for
+ * the same gate and logits. A choice that is no pair takes no part, whatever
+ * d_topk_w holds for it. An expert masked by its logit has gradient 0. One that
+ * only its bias masks is not chosen either, but is a part of the softmax over
+ * all experts, and has that one's gradient, -a s_e dot. logits may be NULL for
  * a renormalised softmax, whose weights say all. Indices outside [0, E) are
  * skipped. d_logits does not overlap the inputs. The bounds of the gate and the alignment are those of
  * moe_route_gated, d_logits as logits; the capacity of p is not used. */

@@ -46,3 +46,32 @@ def test_gradients_at_scales_of_any_size(M, scale, E, renorm, sigmoid):  # noqa:
     ref, mag = P.gate_backward(l, fwd["topk_idx"], np.ones((T, k), bool), d_w, sigmoid, renorm, scale)
     step = 2.0 ** -149 * np.abs(d_w).sum(1)[:, None] * 2 + 4 * 2.0 ** -149
     assert (np.abs(got - ref) <= (48 + E / 32) * 2.0 ** -24 * mag + step).all(), np.abs(got - ref).max()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E", [24, 27])
+@pytest.mark.parametrize("left", [21, 3])
+def test_an_expert_that_only_the_bias_masks_stays_in_the_softmax(M, left, E, bf16):  # noqa: F811
+    """Weights s_e over all experts: a bias of -inf takes an expert out of the choice, not out of the sum, so its logit has
+    a gradient. Against the formula, and against central differences of the weights (second order under 1e-9, fp32 and
+    bf16 roundings of the gradient by the formula's bar). With 3 experts left of k = 5 the last choices are no pairs."""
+    rng = np.random.default_rng(left)
+    bias = 0.1 * rng.standard_normal(E)
+    masked = rng.permutation(E)[:E - left]
+    bias[masked] = -np.inf
+    c = {**BASE, "sigmoid": False, "renorm": False, "scale": 2.5}
+    l = rng.standard_normal((20, E)).astype(np.float32)
+    l[:, masked[0]] = 4.0                               # the largest score of all
+    l[3, masked[0]] = -np.inf                           # masked both ways
+    fwd, d_w, ok, ref = check_backward(M, l, bias, 5, c, bf16, 4)
+    assert (ok.sum(1) == min(left, 5)).all() and not np.isin(fwd["topk_idx"][ok], masked).any()
+    assert ref[3, masked[0]] == 0 and (ref[:3, masked[0]] != 0).all()
+    x = P.bf16_round(l) if bf16 else l
+    for t, e in [(0, masked[0]), (5, masked[-1]), (7, fwd["topk_idx"][7, 0])]:
+        f = []
+        for s in (1e-5, -1e-5):
+            v = x[t].astype(np.float64)
+            v[e] += s
+            f.append(P.weights_of(v, fwd["topk_idx"][t], ok[t], False, False, 2.5))
+        slope = ((f[0] - f[1])[ok[t]] * d_w[t][ok[t]]).sum() / 2e-5
+        assert abs(slope - ref[t, e]) < 1e-7
