@@ -5,9 +5,10 @@ roundings of 2^-24; the sum over the choices the same and 5 more, the quotient a
 Gradients: the bar of test_gpu_gate."""
 import numpy as np
 import pytest
+import torch
 
 import plain64 as P
-from test_gpu_gate import BASE, M, backward, check_backward, route  # noqa: F401  (M is a fixture)
+from test_gpu_gate import BASE, DEV, M, backward, check_backward, route  # noqa: F401  (M is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +76,38 @@ def test_an_expert_that_only_the_bias_masks_stays_in_the_softmax(M, left, E, bf1
             f.append(P.weights_of(v, fwd["topk_idx"][t], ok[t], False, False, 2.5))
         slope = ((f[0] - f[1])[ok[t]] * d_w[t][ok[t]]).sum() / 2e-5
         assert abs(slope - ref[t, e]) < 1e-7
+
+
+@pytest.mark.parametrize("T,E,k,C", [(1, 16, 4, 4), (70, 16, 4, 12), (500, 64, 8, 40)])
+def test_the_gradient_of_a_bf16_dispatch_is_the_combine_with_weights_of_one(M, T, E, k, C):  # noqa: F811
+    """x[t] is copied to the rows of its kept pairs, so its gradient is the sum of those rows' gradients: at most k fp32
+    roundings of the magnitudes and one to bf16 (half an ulp, doubled across a binade). Checked against <d_rows, rows>,
+    linear in x, too: a step of 1 in an element of x moves it by the element's exact gradient."""
+    H = 136
+    torch.manual_seed(T)
+    rng = np.random.default_rng(T)
+    l = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).to(DEV)
+    p = M.problem(T, H, E, k, 1, C)
+    b = M.alloc_buffers(p, DEV)
+    x = torch.randn((T, H), device=DEV).to(torch.bfloat16)
+    M.moe_route_gated(p, M.gate(), l, None, b["topk_idx"], b["topk_w"], b["counts"], b["offsets"], b["slot"],
+                      b["rank_counts"], b["dropped"], b["workspace"])
+    d_rows = torch.randn((E, C, H), device=DEV).to(torch.bfloat16)
+    d_x = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+    M.moe_combine(p, d_rows, b["topk_idx"], torch.ones((T, k), device=DEV), b["slot"], d_x)
+
+    def rows_of(x):
+        b["recv"].zero_()
+        M.moe_dispatch(p, x, b["topk_idx"], b["slot"], b["recv"], None, b["recv_src"])
+        return b["recv"].view(torch.bfloat16).double()
+    ref, mag = torch.zeros((T, H), dtype=torch.float64, device=DEV), torch.zeros((T, H), dtype=torch.float64, device=DEV)
+    idx, slot = b["topk_idx"].long(), b["slot"].long()
+    for j in range(k):
+        rows = torch.where((slot[:, j] >= 0)[:, None], d_rows[idx[:, j], slot[:, j].clamp(min=0)].double(), 0.0)
+        ref += rows
+        mag += rows.abs()
+    assert ((d_x.double() - ref).abs() <= k * 2.0 ** -24 * mag + 2.0 ** -8 * ref.abs()).all()
+    x[0, 5] = 1.0                                       # exact steps: 1 to 2
+    before = rows_of(x)
+    x[0, 5] = 2.0
+    assert abs(((rows_of(x) - before) * d_rows.double()).sum() - ref[0, 5]) < 1e-12
