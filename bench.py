@@ -142,7 +142,7 @@ def kernel_source_sha(files) -> str:
 
 TRAFFIC_SOURCES = {"combine": ["moe_combine.cu", "moe_internal.cuh"],
                    "dispatch": ["moe_dispatch.cu", "moe_internal.cuh"],
-                   "gemm": ["moe_gemm.cu", "moe_internal.cuh"]}
+                   "gemm": ["moe_gemm.cu", "moe_tc.cuh", "moe_internal.cuh"]}
 
 
 def ncu_traffic(kernel: str, workload: str):
