@@ -378,7 +378,8 @@ W4Args w4_args(const Dims &d, const moe_w4 *w) {
 
 // Many rows per expert take the tiles: from 4 rows on the mean, where some expert can have over 8. 64 experts of
 // 2 x 2048 x 7168, groups of 128, us: 1 row 187 here, 199 with the tiles; 4 rows 195 and 199; 8 rows 214 and 199, and
-// past 8 rows this file's kernel reads the weights again for every 8.
+// past 8 rows this file's kernel reads the weights again for every 8. The figures are for even loads: the mean is all that
+// is known on the host, and an expert far above it pays that way here.
 bool w4_many_rows(const Dims &d) {
     return (d.T < d.C ? d.T : d.C) > 8 && (long long)d.T * d.k >= 4LL * d.E;
 }

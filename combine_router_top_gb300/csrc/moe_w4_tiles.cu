@@ -29,7 +29,7 @@
 // Bound by the conversion of codes (144 instructions of a warp for 32 rows x 128
 // inputs, half of them on the half-rate ALU pipe) and by the chain operand -> MMA ->
 // sums -> accumulator; the split into these roles is what overlaps the links. 256
-// experts of 2 x 2048 x 7168 with 32 rows each, groups of 128: 969 us, 0.61 of the
+// experts of 2 x 2048 x 7168 with 32 rows each, groups of 128: 964 us, 0.61 of the
 // copy bandwidth; 32 such experts 136 us with 32 rows, 122 with 16, 185 with 64;
 // groups of 32 and 16 rows 140 us.
 // Every mbarrier wait is bounded; one that gives up raises the status word and an
