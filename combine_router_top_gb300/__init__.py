@@ -34,6 +34,12 @@ MOE_LOGITS_BF16 = 1
 MOE_ACT_NONE = 0
 MOE_ACT_SILU_GATE = 1
 
+MOE_VALUE_BF16 = 0
+MOE_VALUE_F32 = 1
+MOE_BRANCH_PLAIN = 0
+MOE_BRANCH_CHANNEL = 1
+MOE_BRANCH_TOKEN = 2
+
 
 class moe_problem(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("num_tokens", "hidden", "num_experts", "top_k", "num_ranks",
@@ -47,6 +53,11 @@ class moe_gate(C.Structure):
 
 class moe_w4(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("n_in", "n_out", "group", "act")]
+
+
+class moe_norm(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("branch_gate", "residual_type", "param_type")] + \
+        [(n, C.c_float) for n in ("eps", "scale")]
 
 
 class moe_ubatch_bufs(C.Structure):
@@ -88,6 +99,7 @@ def lib() -> C.CDLL:
         P, i = C.c_void_p, C.c_int
         pp = C.POINTER(moe_problem)
         gp, wp = C.POINTER(moe_gate), C.POINTER(moe_w4)
+        np_ = C.POINTER(moe_norm)
         sig = {
             "moe_status_string": ([i], C.c_char_p),
             "moe_validate": ([pp], i),
@@ -111,6 +123,10 @@ def lib() -> C.CDLL:
             "moe_combine_backward": ([pp, P, P, P, P, P, P, P, P], i),
             "moe_expert_w4_workspace_bytes": ([pp, wp], C.c_size_t),
             "moe_expert_w4": ([pp, wp, P, P, P, P, P, P, P, C.c_size_t, P], i),
+            "moe_block_norm": ([pp, np_, P, P, P, P, P, P, P, P], i),
+            "moe_combine_norm": ([pp, np_, P, P, P, P, P, P, P, P, P, P, P, P], i),
+            "moe_block_norm_backward_workspace_bytes": ([pp, np_], C.c_size_t),
+            "moe_block_norm_backward": ([pp, np_, P, P, P, P, P, P, P, P, P, P, P, P, P, C.c_size_t, P], i),
             "dbo_create": ([C.POINTER(P)], i),
             "dbo_destroy": ([P], None),
             "dbo_step": ([P, pp, P, P, P, C.POINTER(moe_ubatch_bufs), P, P, P, i], i),
@@ -131,7 +147,8 @@ EXPORTS = ("moe_status_string", "moe_validate", "moe_device_status", "moe_route_
            "moe_dispatch", "moe_src_offsets", "moe_route_dispatch_workspace_bytes", "moe_route_dispatch",
            "moe_expert_synthetic", "moe_expert_gemm_fp8", "moe_expert_gemm_bf16", "moe_ready_flags_bytes", "moe_expert_combine", "moe_path_host",
            "moe_route_gated", "moe_route_gated_backward", "moe_combine_backward", "moe_expert_w4_workspace_bytes",
-           "moe_expert_w4",
+           "moe_expert_w4", "moe_block_norm", "moe_combine_norm", "moe_block_norm_backward_workspace_bytes",
+           "moe_block_norm_backward",
            "moe_combine", "dbo_create", "dbo_destroy", "dbo_step", "dbo_read_timing",
            "moe_layer_stand_in", "dbo_layers", "dbo_layers_capture", "dbo_graph_launch")
 
@@ -340,6 +357,42 @@ def moe_expert_w4(p, w, x, x_scale, counts, w_q, w_scale, y, workspace, stream=N
     rc = lib().moe_expert_w4(C.byref(p), C.byref(w), _ptr(x), _ptr(x_scale), _ptr(counts), _ptr(w_q), _ptr(w_scale),
                              _ptr(y), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     _check("moe_expert_w4", rc)
+
+
+def norm(eps=1e-6, scale=1.0, gate=MOE_BRANCH_PLAIN, residual=MOE_VALUE_BF16, params=MOE_VALUE_BF16) -> moe_norm:
+    """How a block's output joins the residual stream; residual and params: the types of its rows and of the weights."""
+    return moe_norm(gate, residual, params, eps, scale)
+
+
+def moe_block_norm(p, norm, y, residual, w_post, w_pre, gate, r, n, stream=None):
+    """r = residual + scale * gate * N(y; w_post), n = N(r; w_pre) in one pass. w_post None: y as it is; y None: n of
+    the residual alone; r or n may be left out (n together with w_pre)."""
+    rc = lib().moe_block_norm(C.byref(p), C.byref(norm), _ptr(y), _ptr(residual), _ptr(w_post), _ptr(w_pre), _ptr(gate),
+                              _ptr(r), _ptr(n), _stream(stream))
+    _check("moe_block_norm", rc)
+
+
+def moe_combine_norm(p, norm, y, topk_idx, topk_w, slot, residual, w_post, w_pre, gate, out, r, n, stream=None):
+    """moe_combine and moe_block_norm in one pass; out (the combine's sum in bf16) may be None."""
+    rc = lib().moe_combine_norm(C.byref(p), C.byref(norm), _ptr(y), _ptr(topk_idx), _ptr(topk_w), _ptr(slot),
+                                _ptr(residual), _ptr(w_post), _ptr(w_pre), _ptr(gate), _ptr(out), _ptr(r), _ptr(n),
+                                _stream(stream))
+    _check("moe_combine_norm", rc)
+
+
+def moe_block_norm_backward_workspace_bytes(p: moe_problem, norm: moe_norm) -> int:
+    return lib().moe_block_norm_backward_workspace_bytes(C.byref(p), C.byref(norm))
+
+
+def moe_block_norm_backward(p, norm, y, r, d_r, d_n, w_post, w_pre, gate, d_y, d_residual, d_w_post, d_w_pre, d_gate,
+                            workspace, stream=None):
+    """Gradient of moe_block_norm from y and the forward pass's r: d_y, d_residual, and where they are wanted the
+    weights' and the gate's (f32). d_r None: no gradient reaches r directly."""
+    rc = lib().moe_block_norm_backward(C.byref(p), C.byref(norm), _ptr(y), _ptr(r), _ptr(d_r), _ptr(d_n), _ptr(w_post),
+                                       _ptr(w_pre), _ptr(gate), _ptr(d_y), _ptr(d_residual), _ptr(d_w_post),
+                                       _ptr(d_w_pre), _ptr(d_gate), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("moe_block_norm_backward", rc)
 
 
 class DboContext:

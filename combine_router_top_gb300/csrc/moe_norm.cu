@@ -1,0 +1,736 @@
+// moe_norm.cu -- the norms around a block of the residual stream, fused with the
+// block's gate and residual scale, alone or behind the combine; and their gradient.
+//
+//   b = y  or  N(y; w_post)          N(v; w) = v (mean(v^2) + eps)^(-1/2) w
+//   r = residual + a g b             g: 1, a factor for each channel or for each token
+//   n = N(r; w_pre)
+//
+// y is read (moe_block_norm) or formed as the combine forms it (moe_combine_norm). Everything
+// between the loads and the stores is fp32: n comes from the r before it is rounded.
+//
+// Gradient, with ^ for a row divided by its root mean square and 1/s for that root's inverse:
+//   D   = d_r + (w_pre d_n - r^ mean(r^ w_pre d_n)) / s_r                 = d_residual
+//   d_y = (w_post c - y^ mean(y^ w_post c)) / s_y,  c = a g D
+//   d_w_pre = sum_t d_n r^    d_w_post = sum_t c y^    d_gate = a sum D b  (over t, or over h)
+// Both norms' statistics come from the row itself again, which is in registers: the forward
+// pass keeps nothing but y and r.
+#include <math.h>
+
+#include <algorithm>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kNormMaxHidden = 16384;
+
+struct NormArgs {
+    int T, H8, k, C;                   // H8 chunks of 8 elements to a row
+    float eps, scale, inv_h;
+    int channel, token;                // the gate's kind
+};
+
+// Eight elements of a row as they are stored, and as fp32.
+template <bool F32>
+struct Raw8;
+template <>
+struct Raw8<false> {
+    uint4 a;
+};
+template <>
+struct Raw8<true> {
+    uint4 a, b;
+};
+__device__ __forceinline__ void to_floats(const Raw8<false> &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+__device__ __forceinline__ void to_floats(const Raw8<true> &v, float (&f)[8]) {
+    const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+}
+// Chunk c of a row that is read once.
+__device__ __forceinline__ void load_row8(const void *row, int c, Raw8<false> &v) {
+    v.a = ld_stream_v4(static_cast<const uint4 *>(row) + c);
+}
+__device__ __forceinline__ void load_row8(const void *row, int c, Raw8<true> &v) {
+    v.a = ld_stream_v4(static_cast<const uint4 *>(row) + 2 * c);
+    v.b = ld_stream_v4(static_cast<const uint4 *>(row) + 2 * c + 1);
+}
+// The residual's: the same memory may be written as r, by the thread that read it.
+__device__ __forceinline__ uint4 ld_once_v4(const uint4 *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ void load_residual8(const void *row, int c, Raw8<false> &v) {
+    v.a = ld_once_v4(static_cast<const uint4 *>(row) + c);
+}
+__device__ __forceinline__ void load_residual8(const void *row, int c, Raw8<true> &v) {
+    v.a = ld_once_v4(static_cast<const uint4 *>(row) + 2 * c);
+    v.b = ld_once_v4(static_cast<const uint4 *>(row) + 2 * c + 1);
+}
+// Chunk c of a vector that every row uses.
+__device__ __forceinline__ void load_param8(const void *p, int c, Raw8<false> &v) {
+    v.a = __ldg(static_cast<const uint4 *>(p) + c);
+}
+__device__ __forceinline__ void load_param8(const void *p, int c, Raw8<true> &v) {
+    v.a = __ldg(static_cast<const uint4 *>(p) + 2 * c);
+    v.b = __ldg(static_cast<const uint4 *>(p) + 2 * c + 1);
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void *row, int c, const float (&f)[8]) {
+    if constexpr (F32) {
+        uint4 *o = static_cast<uint4 *>(row) + 2 * c;
+        st_v4(o, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+        st_v4(o + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+    } else {
+        st_v4(static_cast<uint4 *>(row) + c, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                        pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+    }
+}
+
+// Sums of N values over the block, every thread the same result: by a butterfly over the warp,
+// then by one over the warps' sums. `turn` alternates between two buffers: a thread writes to one
+// again only behind the next sum's barrier, which all reach after reading it.
+template <int N>
+struct BlockSum {
+    float part[2][N][32];
+};
+template <int N>
+__device__ __forceinline__ void block_sum(BlockSum<N> &s, float (&v)[N], unsigned &turn) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
+    if (warps == 1) return;
+    const unsigned b = turn & 1u;
+    ++turn;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s.part[b][i][warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = lane < warps ? s.part[b][i][lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
+    }
+}
+
+__device__ __forceinline__ float inv_rms(float sum_sq, const NormArgs &a) {
+    return __frsqrt_rn(__fmaf_rn(sum_sq, a.inv_h, a.eps));
+}
+
+// Where the block's output comes from: no block at all, its rows, or KMAX gathers at a time
+// of the experts' rows.
+constexpr int kNoBlock = 0, kRows = -1;
+
+// A block of at most MAXT threads takes a row at a time, NC chunks of 8 elements to a thread.
+template <int SRC, bool RES32, bool PAR32, int NC, int MAXT>
+__global__ void __launch_bounds__(MAXT)
+norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__restrict__ topk_idx,
+            const float *__restrict__ topk_w, const int32_t *__restrict__ slot, const void *residual,
+            const void *__restrict__ w_post, const void *__restrict__ w_pre, const void *__restrict__ gate, void *out,
+            void *r_out, void *n_out) {
+    __shared__ BlockSum<1> sums;
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    unsigned turn = 0;
+    const size_t res_row = (size_t)a.H8 * (RES32 ? 32 : 16), bf_row = (size_t)a.H8 * 16;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+        int c[NC];
+        Raw8<RES32> res[NC];
+        Raw8<false> yy[NC];
+        float v[NC][8];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            c[i] = i * (int)blockDim.x + (int)threadIdx.x;
+            if (c[i] < a.H8) load_residual8(static_cast<const char *>(residual) + t * res_row, c[i], res[i]);
+        }
+        if constexpr (SRC == kRows) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (c[i] < a.H8) load_row8(static_cast<const char *>(y) + t * bf_row, c[i], yy[i]);
+        }
+        // one row at a time is latency: the vectors come along with it
+        Raw8<PAR32> p_post[NC], p_pre[NC], p_gate[NC];
+        const auto params = [&](bool early) {
+            if (early != (NC == 1)) return;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                if (c[i] < a.H8) {
+                    if (SRC != kNoBlock && w_post) load_param8(w_post, c[i], p_post[i]);
+                    if (SRC != kNoBlock && a.channel) load_param8(gate, c[i], p_gate[i]);
+                    if (w_pre) load_param8(w_pre, c[i], p_pre[i]);
+                }
+            }
+        };
+        params(true);
+        float g = a.scale;
+        if (SRC != kNoBlock && a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
+
+        if constexpr (SRC > 0) {
+            float w = 0.0f;
+            int row = -1;
+            if (lane < a.k) {
+                const int s = __ldg(slot + (size_t)t * a.k + lane);
+                const int e = __ldg(topk_idx + (size_t)t * a.k + lane);
+                w = __ldg(topk_w + (size_t)t * a.k + lane);
+                if (s >= 0) row = e * a.C + s;
+            }
+            unsigned rem = __ballot_sync(kFull, row >= 0);
+            int left = __popc(rem);
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+            while (left > 0) {                                         // once, or twice past 8 choices
+                Raw8<false> in[SRC][NC];
+                float wj[SRC];
+#pragma unroll
+                for (int j = 0; j < SRC; ++j) {
+                    if (j < left) {                                    // warp-uniform
+                        const int src = __ffs(rem) - 1;
+                        rem &= rem - 1;
+                        const size_t at = (size_t)__shfl_sync(kFull, row, src) * bf_row;
+                        wj[j] = __shfl_sync(kFull, w, src);
+#pragma unroll
+                        for (int i = 0; i < NC; ++i)
+                            if (c[i] < a.H8) load_row8(static_cast<const char *>(y) + at, c[i], in[j][i]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < SRC; ++j) {
+                    if (j < left) {
+#pragma unroll
+                        for (int i = 0; i < NC; ++i) {
+                            float f[8];
+                            to_floats(in[j][i], f);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) v[i][q] = __fmaf_rn(wj[j], f[q], v[i][q]);
+                        }
+                    }
+                }
+                left -= SRC;
+            }
+            if (out != nullptr) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (c[i] < a.H8) store8<false>(static_cast<char *>(out) + t * bf_row, c[i], v[i]);
+            }
+        } else if constexpr (SRC == kRows) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) to_floats(yy[i], v[i]);
+        }
+
+        float f[1];
+        if (SRC != kNoBlock && w_post) {
+            f[0] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (c[i] < a.H8)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) f[0] = __fmaf_rn(v[i][q], v[i][q], f[0]);
+            block_sum(sums, f, turn);
+            g = __fmul_rn(g, inv_rms(f[0], a));
+        }
+        params(false);
+        f[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            if (c[i] < a.H8) {
+                float x[8];
+                to_floats(res[i], x);
+                if constexpr (SRC != kNoBlock) {
+                    if (w_post) {
+                        float p[8];
+                        to_floats(p_post[i], p);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], p[q]);
+                    }
+                    if (a.channel) {
+                        float p[8];
+                        to_floats(p_gate[i], p);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], p[q]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(v[i][q], g, x[q]);
+                }
+                if (r_out) store8<RES32>(static_cast<char *>(r_out) + t * res_row, c[i], x);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    f[0] = __fmaf_rn(x[q], x[q], f[0]);
+                    v[i][q] = x[q];
+                }
+            }
+        }
+        if (w_pre) {
+            block_sum(sums, f, turn);
+            const float s = inv_rms(f[0], a);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                if (c[i] < a.H8) {
+                    float p[8];
+                    to_floats(p_pre[i], p);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) p[q] = __fmul_rn(__fmul_rn(v[i][q], s), p[q]);
+                    store8<false>(static_cast<char *>(n_out) + t * bf_row, c[i], p);
+                }
+            }
+        }
+    }
+}
+
+struct NormPtrs {
+    const void *y;
+    const int32_t *idx;
+    const float *w;
+    const int32_t *slot;
+    const void *residual, *w_post, *w_pre, *gate;
+    void *out, *r, *n;
+};
+
+template <int SRC, bool RES32, bool PAR32, int NC, int MAXT>
+int launch_norm(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    const int threads = ((a.H8 + NC - 1) / NC + 31) / 32 * 32;
+    // blocks do not wait on one another: a few more than an SM holds even out its end
+    const int grid = persistent_grid(d.T, sm_count() * std::min(32, 2048 / threads), d.max_blocks);
+    return launch_pdl(norm_kernel<SRC, RES32, PAR32, NC, MAXT>, grid, threads, st, a, p.y, p.idx, p.w, p.slot,
+                      p.residual, p.w_post, p.w_pre, p.gate, p.out, p.r, p.n) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+template <int SRC, bool RES32, bool PAR32>
+int launch_norm_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    if constexpr (SRC <= 0) {
+        if (a.H8 <= 1024) return launch_norm<SRC, RES32, PAR32, 1, 1024>(d, a, st, p);
+        return launch_norm<SRC, RES32, PAR32, 2, 1024>(d, a, st, p);
+    } else {
+        if (a.H8 <= 256) return launch_norm<SRC, RES32, PAR32, 1, 256>(d, a, st, p);
+        if (a.H8 <= 1024) return launch_norm<SRC, RES32, PAR32, 2, 512>(d, a, st, p);
+        return launch_norm<(SRC < 4 ? SRC : 4), RES32, PAR32, 4, 512>(d, a, st, p);
+    }
+}
+template <int SRC>
+int launch_norm_types(const Dims &d, const moe_norm *n, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    const bool res = n->residual_type == MOE_VALUE_F32, par = n->param_type == MOE_VALUE_F32;
+    if (res) return par ? launch_norm_nc<SRC, true, true>(d, a, st, p) : launch_norm_nc<SRC, true, false>(d, a, st, p);
+    return par ? launch_norm_nc<SRC, false, true>(d, a, st, p) : launch_norm_nc<SRC, false, false>(d, a, st, p);
+}
+
+int check_norm(const Dims &d, const moe_norm *n, NormArgs *a) {
+    if (n == nullptr) return MOE_ERR_INVALID_ARG;
+    if (n->branch_gate < MOE_BRANCH_PLAIN || n->branch_gate > MOE_BRANCH_TOKEN) return MOE_ERR_INVALID_ARG;
+    if (n->residual_type != MOE_VALUE_BF16 && n->residual_type != MOE_VALUE_F32) return MOE_ERR_INVALID_ARG;
+    if (n->param_type != MOE_VALUE_BF16 && n->param_type != MOE_VALUE_F32) return MOE_ERR_INVALID_ARG;
+    if (!(n->eps > 0.0f && n->eps <= 3.4028234e38f) || !(fabsf(n->scale) <= 3.4028234e38f)) return MOE_ERR_INVALID_ARG;
+    if (d.H > kNormMaxHidden) return MOE_ERR_UNSUPPORTED;
+    a->T = d.T;
+    a->H8 = d.H / 8;
+    a->k = d.k;
+    a->C = d.C;
+    a->eps = n->eps;
+    a->scale = n->scale;
+    a->inv_h = 1.0f / (float)d.H;
+    a->channel = n->branch_gate == MOE_BRANCH_CHANNEL;
+    a->token = n->branch_gate == MOE_BRANCH_TOKEN;
+    return MOE_OK;
+}
+
+// What the two forward calls have in common; has_y: there is a block's output.
+int check_forward(const moe_norm *n, bool has_y, const NormPtrs &p) {
+    if (!p.residual || (!p.r && !p.n)) return MOE_ERR_INVALID_ARG;
+    if ((p.w_pre != nullptr) != (p.n != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!has_y && (p.w_post || n->branch_gate != MOE_BRANCH_PLAIN || p.r)) return MOE_ERR_INVALID_ARG;
+    if ((p.gate != nullptr) != (n->branch_gate != MOE_BRANCH_PLAIN)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(p.y, 16) || !aligned(p.residual, 16) || !aligned(p.w_post, 16) || !aligned(p.w_pre, 16) ||
+        !aligned(p.gate, n->branch_gate == MOE_BRANCH_TOKEN ? 4 : 16) || !aligned(p.out, 16) || !aligned(p.r, 16) ||
+        !aligned(p.n, 16))
+        return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// ---- gradient -----------------------------------------------------------------
+
+constexpr int kBwdMaxDepth = 4;                    // rows on their way or at hand
+
+struct NormBwdPtrs {
+    const void *y, *r, *d_r, *d_n, *w_post, *w_pre, *gate;
+    void *d_y, *d_residual;
+    float *d_gate_token, *part;
+    unsigned *status;
+};
+
+// A block takes the rows of one part (rows p, p + parts, ...) at a time and keeps that part's column
+// sums in registers: NC chunks of 8 columns to a thread. The rows of y, r, d_r and d_n come by
+// bulk copies into a ring, `depth` rows deep, so that loads run on while a row's two sums meet.
+template <bool RES32, bool PAR32, int NC>
+__global__ void __launch_bounds__(NC == 1 ? 1024 : 512)
+norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
+    extern __shared__ __align__(128) char bwd_ring[];
+    __shared__ __align__(8) uint64_t full[kBwdMaxDepth];
+    __shared__ BlockSum<3> sums3;
+    __shared__ BlockSum<1> sums1;
+    const int tid = threadIdx.x;
+    const unsigned bf_row = (unsigned)a.H8 * 16u, res_row = RES32 ? 2u * bf_row : bf_row;
+    const unsigned y_bytes = p.y ? bf_row : 0u, r_bytes = p.w_pre ? res_row : 0u;
+    const unsigned dr_bytes = p.d_r ? res_row : 0u, dn_bytes = p.w_pre ? bf_row : 0u;
+    const unsigned at_r = y_bytes, at_dr = at_r + r_bytes, at_dn = at_dr + dr_bytes, stage = at_dn + dn_bytes;
+    if (tid < depth) {
+        mbar_init(&full[tid], 1u);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_enter();
+
+    // the rows that this block reads, in order
+    int f_part = blockIdx.x, f_row = blockIdx.x;
+    unsigned fetched = 0;
+    bool alive = true;
+    const auto fetch = [&]() {                       // thread 0
+        if (f_part >= parts || !alive) return;
+        const unsigned s = fetched % (unsigned)depth;
+        char *to = bwd_ring + (size_t)s * stage;
+        mbar_expect_tx(&full[s], stage);
+        if (y_bytes) bulk_g2s(to, static_cast<const char *>(p.y) + (size_t)f_row * bf_row, y_bytes, &full[s]);
+        if (r_bytes) bulk_g2s(to + at_r, static_cast<const char *>(p.r) + (size_t)f_row * res_row, r_bytes, &full[s]);
+        if (dr_bytes) bulk_g2s(to + at_dr, static_cast<const char *>(p.d_r) + (size_t)f_row * res_row, dr_bytes, &full[s]);
+        if (dn_bytes) bulk_g2s(to + at_dn, static_cast<const char *>(p.d_n) + (size_t)f_row * bf_row, dn_bytes, &full[s]);
+        ++fetched;
+        f_row += parts;
+        if (f_row >= a.T) {
+            f_part += gridDim.x;
+            f_row = f_part;
+        }
+    };
+    if (tid == 0)
+        for (int i = 0; i < depth; ++i) fetch();
+
+    unsigned turn3 = 0, turn1 = 0, n_row = 0, n_lost = 0;
+    for (int part = blockIdx.x; part < parts; part += gridDim.x) {
+        float sum_pre[NC][8], sum_post[NC][8];
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) sum_pre[i][q] = sum_post[i][q] = 0.0f;
+        for (int t = part; t < a.T; t += parts, ++n_row) {
+            const unsigned s = n_row % (unsigned)depth;
+            if (alive && !mbar_wait_bounded(&full[s], (n_row / (unsigned)depth) & 1u)) {
+                alive = false;                       // outputs stay wrong; the barriers below still meet
+                n_lost = n_row;
+                atomicOr(p.status, kStatusWaitGaveUp);
+            }
+            const char *in = bwd_ring + (size_t)s * stage;
+            Raw8<false> y[NC], dn[NC];
+            Raw8<RES32> r[NC], dr[NC];
+            float v[NC][8], f[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = i * (int)blockDim.x + tid;
+                if (c < a.H8) {
+                    float x[8];
+                    if (y_bytes) {
+                        y[i] = *reinterpret_cast<const Raw8<false> *>(in + (size_t)c * 16);
+                        to_floats(y[i], x);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) f[2] = __fmaf_rn(x[q], x[q], f[2]);
+                    }
+                    if (dr_bytes) dr[i] = *reinterpret_cast<const Raw8<RES32> *>(in + at_dr + (size_t)c * sizeof(Raw8<RES32>));
+                    if (r_bytes) {
+                        r[i] = *reinterpret_cast<const Raw8<RES32> *>(in + at_r + (size_t)c * sizeof(Raw8<RES32>));
+                        dn[i] = *reinterpret_cast<const Raw8<false> *>(in + at_dn + (size_t)c * 16);
+                        Raw8<PAR32> w;
+                        load_param8(p.w_pre, c, w);
+                        float wf[8];
+                        to_floats(w, wf);
+                        to_floats(dn[i], v[i]);
+                        to_floats(r[i], x);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            v[i][q] = __fmul_rn(v[i][q], wf[q]);
+                            f[0] = __fmaf_rn(x[q], x[q], f[0]);
+                            f[1] = __fmaf_rn(x[q], v[i][q], f[1]);
+                        }
+                    }
+                }
+            }
+            block_sum(sums3, f, turn3);
+            if (blockDim.x == 32) __syncwarp();
+            if (tid == 0) fetch();                   // all have read the row's place in the ring
+
+            const float rs = inv_rms(f[0], a), ys = p.w_post ? inv_rms(f[2], a) : 1.0f;
+            const float mean = __fmul_rn(__fmul_rn(f[1], rs), a.inv_h);         // of r^ w_pre d_n
+            const float g = a.token ? __ldg(static_cast<const float *>(p.gate) + t) : 1.0f;
+            float e[1] = {0.0f};
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = i * (int)blockDim.x + tid;
+                if (c < a.H8) {
+                    float D[8], x[8];
+                    if (dr_bytes) to_floats(dr[i], D);
+                    else
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) D[q] = 0.0f;
+                    if (r_bytes) {
+                        float n[8];
+                        to_floats(r[i], x);
+                        to_floats(dn[i], n);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float rh = __fmul_rn(x[q], rs);
+                            sum_pre[i][q] = __fmaf_rn(n[q], rh, sum_pre[i][q]);
+                            D[q] = __fmaf_rn(rs, __fmaf_rn(-rh, mean, v[i][q]), D[q]);
+                        }
+                    }
+                    store8<RES32>(static_cast<char *>(p.d_residual) + (size_t)t * res_row, c, D);
+                    if (y_bytes) {
+                        to_floats(y[i], x);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            sum_post[i][q] = __fmaf_rn(__fmul_rn(D[q], g), __fmul_rn(x[q], ys), sum_post[i][q]);
+                        if (a.channel) {
+                            Raw8<PAR32> w;
+                            float wf[8];
+                            load_param8(p.gate, c, w);
+                            to_floats(w, wf);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) D[q] = __fmul_rn(D[q], wf[q]);
+                        }
+                        if (p.w_post) {
+                            Raw8<PAR32> w;
+                            float wf[8];
+                            load_param8(p.w_post, c, w);
+                            to_floats(w, wf);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) D[q] = __fmul_rn(D[q], wf[q]);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            v[i][q] = D[q];
+                            e[0] = __fmaf_rn(D[q], x[q], e[0]);
+                        }
+                    }
+                }
+            }
+            if (y_bytes) {
+                if (p.w_post || p.d_gate_token) block_sum(sums1, e, turn1);
+                const float by = __fmul_rn(a.scale, g);
+                if (p.d_gate_token && tid == 0) p.d_gate_token[t] = __fmul_rn(__fmul_rn(a.scale, ys), e[0]);
+                const float m = __fmul_rn(__fmul_rn(e[0], ys), a.inv_h);        // of y^ w_post D
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const int c = i * (int)blockDim.x + tid;
+                    if (c < a.H8) {
+                        float x[8];
+                        to_floats(y[i], x);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float u = p.w_post ? __fmul_rn(ys, __fmaf_rn(-__fmul_rn(x[q], ys), m, v[i][q])) : v[i][q];
+                            x[q] = __fmul_rn(u, by);
+                        }
+                        store8<false>(static_cast<char *>(p.d_y) + (size_t)t * bf_row, c, x);
+                    }
+                }
+            }
+        }
+        float *to = p.part + (size_t)part * 16 * a.H8;                          // [part][pre, post][H]
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = i * (int)blockDim.x + tid;
+            if (c < a.H8) {
+                store8<true>(to, c, sum_pre[i]);
+                store8<true>(to + 8 * a.H8, c, sum_post[i]);
+            }
+        }
+    }
+    if (tid == 0 && !alive)                          // no copy outlives the block
+        for (unsigned i = n_lost; i < fetched; ++i) mbar_wait_bounded(&full[i % (unsigned)depth], (i / (unsigned)depth) & 1u);
+}
+
+// The parts' column sums into the gradients of the norms' weights and of a gate for each channel.
+// A block takes 32 columns of one of the two sums, 32 warps the parts in turn, joined in order.
+template <bool PAR32>
+__global__ void __launch_bounds__(1024)
+norm_columns_kernel(NormArgs a, const float *__restrict__ part, int parts, const void *__restrict__ w_post,
+                    const void *__restrict__ gate, float *__restrict__ d_w_post, float *__restrict__ d_w_pre,
+                    float *__restrict__ d_gate) {
+    __shared__ float sums[32][33];
+    pdl_enter();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = a.H8 * 8;
+    const bool post = blockIdx.y != 0;
+    if (post ? !d_w_post && !d_gate : !d_w_pre) return;
+    const int h = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (h < H) {
+        const float *from = part + (post ? H : 0) + h;
+#pragma unroll 8
+        for (int i = warp; i < parts; i += 32) s += from[(size_t)i * 2 * H];
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && h < H) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += sums[i][lane];
+        if (!post) {
+            d_w_pre[h] = s;
+        } else {
+            const auto at = [&](const void *p) {
+                return PAR32 ? static_cast<const float *>(p)[h] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[h]);
+            };
+            s = __fmul_rn(s, a.scale);
+            if (d_w_post) d_w_post[h] = a.channel ? __fmul_rn(s, at(gate)) : s;
+            if (d_gate) d_gate[h] = w_post ? __fmul_rn(s, at(w_post)) : s;
+        }
+    }
+}
+
+// Parts of the column sums: by the sizes alone, so that neither the grid nor the device changes a
+// sum's order. About as many as blocks that GB300's 152 SMs hold at once.
+int norm_parts(long long T, int H) {
+    const long long most = 152LL * std::max(1, std::min(8, 8192 / H));
+    return (int)std::max(1LL, std::min(most, (T + 1) / 2));
+}
+
+template <bool PAR32>
+int launch_columns(const Dims &d, const NormArgs &a, cudaStream_t st, const float *part, int parts, const void *w_post,
+                   const void *gate, float *d_w_post, float *d_w_pre, float *d_gate) {
+    if (!d_w_post && !d_w_pre && !d_gate) return MOE_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((d.H + 31) / 32), 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_columns_kernel<PAR32>, a, part, parts, w_post, gate, d_w_post, d_w_pre, d_gate) ==
+                   cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+template <bool RES32, bool PAR32, int NC>
+int launch_backward_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormBwdPtrs &p, float *d_w_post,
+                       float *d_w_pre, float *d_gate) {
+    const auto kernel = norm_backward_kernel<RES32, PAR32, NC>;
+    const int threads = ((a.H8 + NC - 1) / NC + 31) / 32 * 32;
+    const int row = d.H * ((p.y ? 2 : 0) + (p.w_pre ? (RES32 ? 6 : 4) : 0) + (p.d_r ? (RES32 ? 4 : 2) : 0));
+    const int parts = norm_parts(d.T, d.H);
+    constexpr int kMaxSmem = 200 * 1024;
+    const int blocks_per_sm = std::max(1, std::min(8, 8192 / d.H));
+    const int depth = std::max(1, std::min(kBwdMaxDepth, kMaxSmem / blocks_per_sm / row));
+    static PerContext<int> smem_done;
+    if (!set_smem_once(smem_done, kernel, kMaxSmem)) return MOE_ERR_CUDA;
+    const size_t smem = (size_t)depth * row;
+    const int grid = persistent_grid(parts, sm_count() * blocks_per_sm, d.max_blocks);
+    if (launch_pdl_smem(kernel, grid, threads, smem, st, a, p, parts, depth) != cudaSuccess) return MOE_ERR_CUDA;
+    return launch_columns<PAR32>(d, a, st, p.part, parts, p.w_post, p.gate, d_w_post, d_w_pre, d_gate);
+}
+template <bool RES32, bool PAR32, typename... A>
+int launch_norm_backward(const Dims &d, const NormArgs &a, A... args) {
+    if (a.H8 <= 256) return launch_backward_nc<RES32, PAR32, 1>(d, a, args...);
+    if (a.H8 <= 1024) return launch_backward_nc<RES32, PAR32, 2>(d, a, args...);
+    return launch_backward_nc<RES32, PAR32, 4>(d, a, args...);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" int moe_block_norm(const moe_problem *p, const moe_norm *norm, const void *y, const void *residual,
+                              const void *w_post, const void *w_pre, const void *gate, void *r, void *n,
+                              void *stream) {
+    using namespace moe;
+    Dims d;
+    NormArgs a;
+    int rc = check_problem(p, &d);
+    if (rc == MOE_OK) rc = check_norm(d, norm, &a);
+    if (rc != MOE_OK) return rc;
+    if (d.T == 0) return MOE_OK;
+    const NormPtrs ptrs = {y, nullptr, nullptr, nullptr, residual, w_post, w_pre, gate, nullptr, r, n};
+    rc = check_forward(norm, y != nullptr, ptrs);
+    if (rc != MOE_OK) return rc;
+    if (y == nullptr) return launch_norm_types<kNoBlock>(d, norm, a, as_stream(stream), ptrs);
+    return launch_norm_types<kRows>(d, norm, a, as_stream(stream), ptrs);
+}
+
+extern "C" int moe_combine_norm(const moe_problem *p, const moe_norm *norm, const void *y, const int32_t *topk_idx,
+                                const float *topk_w, const int32_t *slot, const void *residual, const void *w_post,
+                                const void *w_pre, const void *gate, void *out, void *r, void *n, void *stream) {
+    using namespace moe;
+    Dims d;
+    NormArgs a;
+    int rc = check_problem(p, &d);
+    if (rc == MOE_OK) rc = check_norm(d, norm, &a);
+    if (rc != MOE_OK) return rc;
+    if (d.T == 0) return MOE_OK;
+    if (!y || !topk_idx || !topk_w || !slot) return MOE_ERR_INVALID_ARG;
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(slot, 4)) return MOE_ERR_INVALID_ARG;
+    const NormPtrs ptrs = {y, topk_idx, topk_w, slot, residual, w_post, w_pre, gate, out, r, n};
+    rc = check_forward(norm, true, ptrs);
+    if (rc != MOE_OK) return rc;
+    cudaStream_t st = as_stream(stream);
+    if (d.k <= 2) return launch_norm_types<2>(d, norm, a, st, ptrs);
+    if (d.k <= 4) return launch_norm_types<4>(d, norm, a, st, ptrs);
+    return launch_norm_types<8>(d, norm, a, st, ptrs);
+}
+
+extern "C" size_t moe_block_norm_backward_workspace_bytes(const moe_problem *p, const moe_norm *norm) {
+    using namespace moe;
+    Dims d;
+    NormArgs a;
+    if (check_problem(p, &d) != MOE_OK || check_norm(d, norm, &a) != MOE_OK) return 0;
+    return ((size_t)norm_parts(d.T, d.H) * 2 * d.H * sizeof(float) + 255) & ~(size_t)255;
+}
+
+extern "C" int moe_block_norm_backward(const moe_problem *p, const moe_norm *norm, const void *y, const void *r,
+                                       const void *d_r, const void *d_n, const void *w_post, const void *w_pre,
+                                       const void *gate, void *d_y, void *d_residual, float *d_w_post, float *d_w_pre,
+                                       float *d_gate, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace moe;
+    Dims d;
+    NormArgs a;
+    int rc = check_problem(p, &d);
+    if (rc == MOE_OK) rc = check_norm(d, norm, &a);
+    if (rc != MOE_OK) return rc;
+    if (d.T == 0) {                                                    // the sums of no rows
+        if (!aligned(d_w_post, 4) || !aligned(d_w_pre, 4) || !aligned(d_gate, 4)) return MOE_ERR_INVALID_ARG;
+        NormArgs none = a;
+        none.channel = 0;
+        return launch_columns<true>(d, none, as_stream(stream), nullptr, 0, nullptr, nullptr, d_w_post, d_w_pre,
+                                    a.channel ? d_gate : nullptr);
+    }
+    const bool gated = norm->branch_gate != MOE_BRANCH_PLAIN;
+    if ((!y && (w_post || gated)) || (y != nullptr) != (d_y != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!d_residual || (!w_pre && !d_r) || (w_pre != nullptr) != (d_n != nullptr) || (w_pre && !r)) return MOE_ERR_INVALID_ARG;
+    if ((gate != nullptr) != gated || (d_w_post && !w_post) || (d_w_pre && !w_pre) || (d_gate && !gate)) return MOE_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < moe_block_norm_backward_workspace_bytes(p, norm)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(y, 16) || !aligned(r, 16) || !aligned(d_r, 16) || !aligned(d_n, 16) || !aligned(w_post, 16) ||
+        !aligned(w_pre, 16) || !aligned(gate, a.token ? 4 : 16) || !aligned(d_y, 16) || !aligned(d_residual, 16) ||
+        !aligned(d_w_post, 4) || !aligned(d_w_pre, 4) || !aligned(d_gate, 4) || !aligned(workspace, 16))
+        return MOE_ERR_INVALID_ARG;
+    NormBwdPtrs b = {y, r, d_r, d_n, w_post, w_pre, gate, d_y, d_residual, a.token ? d_gate : nullptr,
+                     static_cast<float *>(workspace), device_status_word()};
+    if (b.status == nullptr) return MOE_ERR_CUDA;
+    cudaStream_t st = as_stream(stream);
+    if (a.token) d_gate = nullptr;                                     // a token's comes from its row
+    const bool res = norm->residual_type == MOE_VALUE_F32, par = norm->param_type == MOE_VALUE_F32;
+    if (res) return par ? launch_norm_backward<true, true>(d, a, st, b, d_w_post, d_w_pre, d_gate)
+                        : launch_norm_backward<true, false>(d, a, st, b, d_w_post, d_w_pre, d_gate);
+    return par ? launch_norm_backward<false, true>(d, a, st, b, d_w_post, d_w_pre, d_gate)
+               : launch_norm_backward<false, false>(d, a, st, b, d_w_post, d_w_pre, d_gate);
+}

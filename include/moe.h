@@ -451,6 +451,86 @@ int moe_expert_w4(const moe_problem *p, const moe_w4 *w, const void *x, const fl
                   const int32_t *counts, const void *w_q, const void *w_scale, void *y,
                   void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Norms around a block ----------------------------------------------------- */
+
+typedef enum moe_value_type {
+    MOE_VALUE_BF16 = 0,
+    MOE_VALUE_F32 = 1
+} moe_value_type;
+
+typedef enum moe_branch_gate {
+    MOE_BRANCH_PLAIN = 0,       /* no gate                                         */
+    MOE_BRANCH_CHANNEL = 1,     /* a factor for each of the H channels              */
+    MOE_BRANCH_TOKEN = 2        /* a factor for each of the T tokens                */
+} moe_branch_gate;
+
+/* How a block's output joins the residual stream. */
+typedef struct moe_norm {
+    int32_t branch_gate;     /* moe_branch_gate: what `gate` holds                  */
+    int32_t residual_type;   /* moe_value_type of residual, r, d_r and d_residual   */
+    int32_t param_type;      /* moe_value_type of w_post, w_pre and a channel gate  */
+    float eps;               /* added to the mean square: finite, > 0               */
+    float scale;             /* a, the factor on the block's output: finite          */
+} moe_norm;
+
+/* The norm after a block, its gate and residual scale, the sum with the residual
+ * stream, and the norm before the next block, in one pass. With
+ *   N(v; w)[h] = v[h] w[h] / sqrt(mean_i v[i]^2 + eps)
+ * and per token, in fp32 throughout:
+ *   b = N(y; w_post), or y itself where w_post is NULL
+ *   r = residual + scale * g * b      g: 1, gate[h] or gate[t]
+ *   n = N(r; w_pre), from r before it is rounded
+ * r is rounded once to residual_type, n to bf16.
+ * y bf16 [T][H], or NULL where there is no block before the norm (r is then the
+ *   residual, w_post, gate and r are NULL, and n alone is written); residual
+ *   [T][H]; r [T][H] or NULL where it is not wanted; n bf16 [T][H] exactly where
+ *   w_pre is given; at least one of r and n. w_post, w_pre and a channel gate
+ *   [H] of param_type; a token gate f32 [T].
+ * r may be residual itself; the other outputs overlap no input. Only T and H of
+ * p are used (its other sizes have to be valid). H <= 16384 (else
+ * MOE_ERR_UNSUPPORTED). Rows whose sum of squares passes fp32 (entries from
+ * about 2^60 on) are outside the norm's range. Row buffers, weights and a
+ * channel gate 16-byte aligned, a token gate 4-byte. */
+int moe_block_norm(const moe_problem *p, const moe_norm *norm, const void *y, const void *residual,
+                   const void *w_post, const void *w_pre, const void *gate, void *r, void *n, void *stream);
+
+/* moe_combine and moe_block_norm in one pass: y[T][H] there is the sum
+ *   sum_j topk_w[t][j] * y[topk_idx[t][j]][slot[t][j]]   over slot >= 0, j ascending, fp32,
+ * of the experts' rows y bf16 [E][C][H] here, not rounded on the way (0 for a
+ * token without pairs). out bf16 [T][H]: the sum, rounded, as moe_combine writes
+ * it (what moe_block_norm_backward takes as y), or NULL where it is not wanted.
+ * The rest is as for moe_block_norm. */
+int moe_combine_norm(const moe_problem *p, const moe_norm *norm, const void *y, const int32_t *topk_idx,
+                     const float *topk_w, const int32_t *slot, const void *residual, const void *w_post,
+                     const void *w_pre, const void *gate, void *out, void *r, void *n, void *stream);
+
+/* Bytes of device workspace moe_block_norm_backward needs (host-only); 0 if p or
+ * norm is invalid. Contents need no initialisation. */
+size_t moe_block_norm_backward_workspace_bytes(const moe_problem *p, const moe_norm *norm);
+
+/* Gradient of moe_block_norm (and, with its `out` as y, of moe_combine_norm, whose
+ * experts' rows then follow by moe_combine_backward of d_y). From y and the
+ * forward pass's r, whose norms are formed again, with r^ = N(r; 1) and y^ = N(y; 1),
+ * s_r and s_y the roots that they were divided by, f = w_pre d_n:
+ *   D   = d_r + (f - r^ mean(r^ f)) / s_r                        d_residual = D
+ *   c   = scale g D
+ *   d_y = (w_post c - y^ mean(y^ w_post c)) / s_y, or c itself without w_post
+ *   d_w_pre = sum_t d_n r^,  d_w_post = sum_t c y^
+ *   d_gate[h] = scale sum_t D b, or d_gate[t] = scale sum_h D b
+ * in fp32; d_y bf16, d_residual of residual_type, the others f32 and written, not
+ * added to. d_r NULL: no gradient reaches r directly. d_n exactly where w_pre is
+ * given, and r with it; one of d_r and w_pre. y NULL: no block; w_post, gate and
+ * d_y are then NULL. d_w_post, d_w_pre and d_gate may be NULL where they are not
+ * wanted. d_residual may be d_r itself; no other outputs overlap inputs. The order
+ * of the sums depends on the sizes alone. An empty batch writes zeros for the
+ * sums over tokens. Bounds and alignment are those of moe_block_norm; d_w_post,
+ * d_w_pre and d_gate 4-byte, workspace 16-byte aligned and not shared with a
+ * concurrent call. Waits on the kernel's own copies are bounded (moe_device_status). */
+int moe_block_norm_backward(const moe_problem *p, const moe_norm *norm, const void *y, const void *r,
+                            const void *d_r, const void *d_n, const void *w_post, const void *w_pre,
+                            const void *gate, void *d_y, void *d_residual, float *d_w_post, float *d_w_pre,
+                            float *d_gate, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- Dual batch overlap ------------------------------------------------- */
 
 /* Buffers of one micro-batch, each sized for its token count (see dbo_step). */

@@ -1,0 +1,95 @@
+"""Plain forms in 64 bits of the norms around a block, their gradient and the whole layer for a few tokens, with bounds
+on what fp32 arithmetic may be off by. numpy, from the formulas; nothing here comes from the package.
+
+Bounds. u = 2^-24 is half a step of fp32. A row's sum takes at most 32 terms in a thread's chain, 5 steps of a
+butterfly, and 5 more over at most 32 warps: at most 42 roundings, 64 with room for the terms' own products. So a mean
+of squares (terms of one sign) is off by at most 64 u of itself, its inverse root by 32 u and the 2 u of the root's own
+rounding: ROOT = 40 u. Every other step is a product or a fused sum, counted one u each."""
+import numpy as np
+
+U = 2.0 ** -24
+ROOT = 40 * U
+
+
+def inv_rms(v, eps):
+    return 1.0 / np.sqrt((v * v).mean(1, keepdims=True) + eps)
+
+
+def gate_of(gate, kind, T):
+    if kind == "none":
+        return np.ones((T, 1))
+    g = gate.astype(np.float64)
+    return g[:, None] if kind == "token" else g[None, :]
+
+
+def forward(y, dy, residual, w_post, w_pre, gate, kind, scale, eps):
+    """r, n and the bounds on their errors before the final rounding. dy: the bound on y's own error (or 0)."""
+    f = gate_of(gate, kind, residual.shape[0]) * scale
+    if y is None:
+        r, dr = residual, np.zeros_like(residual)
+    else:
+        b, db = y, dy + np.zeros_like(y)
+        if w_post is not None:
+            s = inv_rms(y, eps)
+            # the root follows y's errors by their share of its norm
+            moved = np.sqrt((db * db).sum(1, keepdims=True)) / np.sqrt((y * y).sum(1, keepdims=True) + y.shape[1] * eps)
+            b = y * s * w_post
+            db = np.abs(s * w_post) * db + np.abs(b) * (ROOT + moved)
+        r = residual + f * b
+        dr = np.abs(f) * (db + 4 * U * np.abs(b)) + U * np.abs(r)
+    if w_pre is None:
+        return r, dr, None, None
+    s = inv_rms(r, eps)
+    n = r * s * w_pre
+    moved = np.sqrt((dr * dr).sum(1, keepdims=True)) / np.sqrt((r * r).sum(1, keepdims=True) + r.shape[1] * eps)
+    return r, dr, n, np.abs(s * w_pre) * dr + np.abs(n) * (ROOT + moved + 2 * U)
+
+
+def backward(y, r, d_r, d_n, w_post, w_pre, gate, kind, scale, eps):
+    """The gradients by the formulas, each with a bound: (value, bound) by name. m* are sums of magnitudes: every
+    result is linear in the magnitudes that it is formed from, and each of its at most 4 sums and roots adds 64 u of
+    them, each of its at most 20 other steps one u: 300 u covers all; a sum over T tokens adds T + 100."""
+    T, H = r.shape if r is not None else d_r.shape
+    out = {}
+    D = np.zeros((T, H)) if d_r is None else d_r
+    mD = np.abs(D)
+    if w_pre is not None:
+        s = inv_rms(r, eps)
+        rh, v = r * s, w_pre * d_n
+        D = D + s * (v - rh * (rh * v).mean(1, keepdims=True))
+        mD = mD + s * (np.abs(v) + np.abs(rh) * np.abs(rh * v).mean(1, keepdims=True))
+        m = np.abs(d_n * rh).sum(0)
+        out["d_w_pre"] = ((d_n * rh).sum(0), (T + 200) * U * m)
+    out["d_residual"] = (D, 300 * U * mD)
+    if y is None:
+        return out
+    g = gate_of(gate, kind, T)
+    c, mc = scale * g * D, np.abs(scale * g) * mD
+    b = y
+    if w_post is None:
+        out["d_y"] = (c, 300 * U * mc)
+    else:
+        s = inv_rms(y, eps)
+        yh, v, mv = y * s, w_post * c, np.abs(w_post) * mc
+        b = yh * w_post
+        out["d_y"] = (s * (v - yh * (yh * v).mean(1, keepdims=True)),
+                      300 * U * s * (mv + np.abs(yh) * (np.abs(yh) * mv).mean(1, keepdims=True)))
+        out["d_w_post"] = ((c * yh).sum(0), (T + 400) * U * (mc * np.abs(yh)).sum(0))
+    if kind == "channel":
+        out["d_gate"] = (scale * (D * b).sum(0), (T + 400) * U * abs(scale) * (mD * np.abs(b)).sum(0))
+    if kind == "token":
+        out["d_gate"] = (scale * (D * b).sum(1), 400 * U * abs(scale) * (mD * np.abs(b)).sum(1))
+    return out
+
+
+def combine(y, idx, w, slot):
+    """The weighted sum of the experts' rows, and the bound of its fp32 form: a rounding a choice."""
+    T, k = idx.shape
+    out, mag = np.zeros((T, y.shape[2])), np.zeros((T, y.shape[2]))
+    for t in range(T):
+        for j in range(k):
+            if slot[t, j] >= 0:
+                v = w[t, j] * y[idx[t, j], slot[t, j]]
+                out[t] += v
+                mag[t] += np.abs(v)
+    return out, k * U * mag
