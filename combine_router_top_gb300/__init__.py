@@ -39,6 +39,9 @@ MOE_VALUE_F32 = 1
 MOE_BRANCH_PLAIN = 0
 MOE_BRANCH_CHANNEL = 1
 MOE_BRANCH_TOKEN = 2
+MOE_WEIGHTS_BF16 = 0
+MOE_WEIGHTS_FP8_B128 = 1
+MOE_WEIGHTS_W4 = 2
 
 
 class moe_problem(C.Structure):
@@ -58,6 +61,10 @@ class moe_w4(C.Structure):
 class moe_norm(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("branch_gate", "residual_type", "param_type")] + \
         [(n, C.c_float) for n in ("eps", "scale")]
+
+
+class moe_mlp(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("inner", "weights", "group", "shared")]
 
 
 class moe_ubatch_bufs(C.Structure):
@@ -99,7 +106,7 @@ def lib() -> C.CDLL:
         P, i = C.c_void_p, C.c_int
         pp = C.POINTER(moe_problem)
         gp, wp = C.POINTER(moe_gate), C.POINTER(moe_w4)
-        np_ = C.POINTER(moe_norm)
+        np_, mp = C.POINTER(moe_norm), C.POINTER(moe_mlp)
         sig = {
             "moe_status_string": ([i], C.c_char_p),
             "moe_validate": ([pp], i),
@@ -127,6 +134,8 @@ def lib() -> C.CDLL:
             "moe_combine_norm": ([pp, np_, P, P, P, P, P, P, P, P, P, P, P, P], i),
             "moe_block_norm_backward_workspace_bytes": ([pp, np_], C.c_size_t),
             "moe_block_norm_backward": ([pp, np_, P, P, P, P, P, P, P, P, P, P, P, P, P, C.c_size_t, P], i),
+            "moe_layer_few_workspace_bytes": ([pp, mp], C.c_size_t),
+            "moe_layer_few": ([pp, gp, mp, P, P, P, P, P, P, P, P, P, P, P, C.c_size_t, P], i),
             "dbo_create": ([C.POINTER(P)], i),
             "dbo_destroy": ([P], None),
             "dbo_step": ([P, pp, P, P, P, C.POINTER(moe_ubatch_bufs), P, P, P, i], i),
@@ -148,7 +157,7 @@ EXPORTS = ("moe_status_string", "moe_validate", "moe_device_status", "moe_route_
            "moe_expert_synthetic", "moe_expert_gemm_fp8", "moe_expert_gemm_bf16", "moe_ready_flags_bytes", "moe_expert_combine", "moe_path_host",
            "moe_route_gated", "moe_route_gated_backward", "moe_combine_backward", "moe_expert_w4_workspace_bytes",
            "moe_expert_w4", "moe_block_norm", "moe_combine_norm", "moe_block_norm_backward_workspace_bytes",
-           "moe_block_norm_backward",
+           "moe_block_norm_backward", "moe_layer_few_workspace_bytes", "moe_layer_few",
            "moe_combine", "dbo_create", "dbo_destroy", "dbo_step", "dbo_read_timing",
            "moe_layer_stand_in", "dbo_layers", "dbo_layers_capture", "dbo_graph_launch")
 
@@ -393,6 +402,25 @@ def moe_block_norm_backward(p, norm, y, r, d_r, d_n, w_post, w_pre, gate, d_y, d
                                        _ptr(d_w_pre), _ptr(d_gate), _ptr(workspace),
                                        workspace.numel() * workspace.element_size(), _stream(stream))
     _check("moe_block_norm_backward", rc)
+
+
+def mlp(inner, weights=MOE_WEIGHTS_BF16, group=128, shared=0) -> moe_mlp:
+    """Shape of the experts' MLPs: H -> inner -> H; shared 1: one more expert, which every token has."""
+    return moe_mlp(inner, weights, group, int(shared))
+
+
+def moe_layer_few_workspace_bytes(p: moe_problem, mlp: moe_mlp) -> int:
+    return lib().moe_layer_few_workspace_bytes(C.byref(p), C.byref(mlp))
+
+
+def moe_layer_few(p, gate, mlp, x, logits, bias, w_up, up_scale, w_down, down_scale, topk_idx, topk_w, out, workspace,
+                  stream=None):
+    """The whole layer for up to 32 tokens in two launches: choice, gate and up products, SiLU, down product and
+    weighted sum. Scales None for bf16 weights; topk_idx and topk_w may be None."""
+    rc = lib().moe_layer_few(C.byref(p), C.byref(gate), C.byref(mlp), _ptr(x), _ptr(logits), _ptr(bias), _ptr(w_up),
+                             _ptr(up_scale), _ptr(w_down), _ptr(down_scale), _ptr(topk_idx), _ptr(topk_w), _ptr(out),
+                             _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("moe_layer_few", rc)
 
 
 class DboContext:

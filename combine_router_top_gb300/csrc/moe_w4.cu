@@ -30,19 +30,6 @@ constexpr int kW4Depth = 4;            // blocks of codes that a warp has in fli
 constexpr int kW4Stage = 1024 + 128;   // a block of 16 rows: 64 bytes of codes and up to 8 of scales each
 constexpr int kW4TileMap = 1024;       // token tiles whose expert is looked up instead of searched
 
-template <bool F16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    if constexpr (F16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // Eight inputs of one row as four 16-bit pairs.
 template <bool F8>
 __device__ __forceinline__ void load_x8(const uint8_t *p, uint32_t (&b)[4]) {

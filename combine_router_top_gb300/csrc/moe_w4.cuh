@@ -1,5 +1,6 @@
-// moe_w4.cuh -- what the two kernels of moe_expert_w4 share: sizes, the 4-bit
-// codes as 16-bit numbers, and the gated SiLU.
+// moe_w4.cuh -- what the two kernels of moe_expert_w4 (and the layer for a few
+// tokens) share: sizes, the 4-bit codes as 16-bit numbers, the 16-row tensor-core
+// product, and the gated SiLU.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -42,6 +43,19 @@ __device__ __forceinline__ void w4_pairs(uint32_t word, uint32_t (&r)[4]) {
     r[1] = w4_fma<F16>(word & 0x00F000F0u, kBy16, kLess);
     r[2] = w4_fma<F16>(up & 0x000F000Fu, kBy, kLess);
     r[3] = w4_fma<F16>(up & 0x00F000F0u, kBy16, kLess);
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Two e4m3 codes -> two fp16 (exact).

@@ -531,6 +531,60 @@ int moe_block_norm_backward(const moe_problem *p, const moe_norm *norm, const vo
                             const void *gate, void *d_y, void *d_residual, float *d_w_post, float *d_w_pre,
                             float *d_gate, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- The whole layer for a few tokens -------------------------------------------- */
+
+typedef enum moe_weights {
+    MOE_WEIGHTS_BF16 = 0,
+    MOE_WEIGHTS_FP8_B128 = 1,   /* e4m3, one f32 scale for each 128 x 128 block     */
+    MOE_WEIGHTS_W4 = 2          /* 4-bit codes and group scales, as moe_expert_w4's */
+} moe_weights;
+
+/* The experts' MLPs: H -> inner (gate and up, SiLU) -> H. */
+typedef struct moe_mlp {
+    int32_t inner;           /* I, 64 <= I <= 65536, a multiple of 64 (bf16) or 128 */
+    int32_t weights;         /* moe_weights                                         */
+    int32_t group;           /* MOE_WEIGHTS_W4: inputs per scale, 32, 64 or 128      */
+    int32_t shared;          /* 1: matrix E is an expert of every token, with weight 1;
+                                0: none                                             */
+} moe_mlp;
+
+/* Bytes of device workspace moe_layer_few needs (host-only); 0 if p or mlp is
+ * invalid. Contents need no initialisation. */
+size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
+
+/* A whole mixture-of-experts layer for up to 32 tokens, in two launches: the
+ * choice as moe_route_gated makes it, then for every pair (t, j), e = topk_idx[t][j],
+ *   u = x[t] Wup_e^T (2I values: the gate's I, then the up's)
+ *   h[i] = bf16(silu(u[i]) u[I + i]),   silu(v) = v / (1 + exp(-v))
+ *   out[t] = bf16(sum_j topk_w[t][j] h Wdown_e^T)
+ * with the shared expert's term of weight 1 behind the pairs'. Products are exact,
+ * sums fp32; h is rounded to bf16 (the products' operand type) and out once. There
+ * is no capacity: no pair is dropped, and choices that are no pair take no part (a
+ * token without pairs and without a shared expert has out 0). Each chosen expert's weights
+ * are read once, the others' not at all.
+ * x bf16 [T][H] (p's dispatch_dtype must be MOE_DTYPE_BF16); logits [T][E] of the
+ *   gate's type; bias f32 [E] or NULL; topk_idx i32 [T][k] and topk_w f32 [T][k],
+ *   as moe_route_gated writes them, or NULL where they are not wanted; out bf16 [T][H].
+ * Matrices, output index major, of S = E + shared experts; M = 2I, K = H for w_up
+ *   (the gate's I rows, then the up's) and M = H, K = I for w_down:
+ *   MOE_WEIGHTS_BF16: bf16 [S][M][K], scales NULL;
+ *   MOE_WEIGHTS_FP8_B128: e4m3 u8 [S][M][K], scale f32 [S][M/128][K/128] (the codes
+ *     0x7f and 0xff, e4m3's NaN, count as +-480);
+ *   MOE_WEIGHTS_W4: codes u8 [S][M][K/2] packed as for moe_expert_w4 (w4_pack),
+ *     scale bf16 [S][M][K/group].
+ * T > 32, H or I no multiple of 64 (bf16) or 128 (fp8, 4-bit): MOE_ERR_UNSUPPORTED.
+ * R and C of p are not used; max_blocks caps the grids. Deterministic, and
+ * independent of max_blocks. Buffers 16-byte aligned (logits as for
+ * moe_route_gated; bias, topk_idx, topk_w and fp8 scales 4-byte, 4-bit scales
+ * 2-byte); outputs and workspace overlap no input. workspace: at least
+ * moe_layer_few_workspace_bytes, not shared with a concurrent call. Waits on the
+ * kernels' own copies are bounded (moe_device_status). Launched as programmatic
+ * dependents. */
+int moe_layer_few(const moe_problem *p, const moe_gate *gate, const moe_mlp *mlp, const void *x,
+                  const void *logits, const float *bias, const void *w_up, const void *up_scale,
+                  const void *w_down, const void *down_scale, int32_t *topk_idx, float *topk_w, void *out,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- Dual batch overlap ------------------------------------------------- */
 
 /* Buffers of one micro-batch, each sized for its token count (see dbo_step). */

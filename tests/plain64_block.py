@@ -93,3 +93,33 @@ def combine(y, idx, w, slot):
                 out[t] += v
                 mag[t] += np.abs(v)
     return out, k * U * mag
+
+
+def bf16(a):
+    """The bf16 values that float64 values round to (through fp32, which moves a value by 2^-24 of it at most)."""
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).float().to(torch.bfloat16).double().numpy()
+
+
+def mlp(x, up, down, inner):
+    """One expert's MLP of rows x in float64, up [2 inner][H], down [H][inner], with h rounded to bf16 as the layer's
+    definition has it; and a bound on what the fp32 sums may move the result by.
+
+    A product of K inputs: an MMA step of 16 rounds its sum and its add into the accumulator (2), at most K/16 steps; a
+    group's sum is scaled and added (2 for each of K/32 groups at most); 8 partial sums are joined: (K/8 + K/16 + 16) u
+    of the sum of magnitudes =: B. silu moves by at most 1.1 of its argument's error and is formed in 4 roundings more,
+    2^-21 in all. Where that reach crosses a rounding border of bf16, h may be the neighbour: its reach is the difference
+    of the rounded ends. Down, h's reach goes through the magnitudes, and the product's own B is added."""
+    def product(v, w):
+        K = w.shape[1]
+        return v @ w.T, (K / 8 + K / 16 + 16) * U * (np.abs(v) @ np.abs(w).T)
+    r, B = product(x, up)
+    g, u, Bg, Bu = r[:, :inner], r[:, inner:], B[:, :inner], B[:, inner:]
+    with np.errstate(over="ignore"):
+        s = g / (1.0 + np.exp(-g))
+    h = s * u
+    reach = 1.1 * Bg * np.abs(u) + np.abs(s) * Bu + Bg * Bu + 2.0 ** -21 * np.abs(h)
+    hr = bf16(h)
+    reach = np.maximum(np.abs(bf16(h + reach) - hr), np.abs(bf16(h - reach) - hr))
+    out, Bo = product(hr, down)
+    return out, Bo + reach @ np.abs(down).T
