@@ -24,13 +24,14 @@ namespace moe {
 namespace {
 
 constexpr int kFewTokens = 32;
-constexpr int kFewWarps = 8;                       // that multiply; one more fetches
-constexpr int kFewThreads = (kFewWarps + 1) * 32;
-constexpr int kFewRows = 16;                       // matrix rows of a tile
-constexpr int kFewPiece = 1024;                    // bytes of a row in a stage of the ring: 128 for each warp
+constexpr int kFewWarps = 8;
+constexpr int kFewThreads = kFewWarps * 32;
+constexpr int kFewRows = 16;                       // matrix rows of a unit
+constexpr int kFewPiece = 256;                     // bytes of each row in a slot of a warp's ring
 constexpr int kFewPitch = kFewPiece + 64;          // rows 64 bytes apart in the banks: two rows' 64 bytes meet no twice
-constexpr int kFewStage = kFewRows * kFewPitch;
-constexpr int kFewStages = 5;
+constexpr int kFewSlot = kFewRows * kFewPitch;
+constexpr int kFewSlots = 2;                       // for each warp
+constexpr int kFewRing = kFewWarps * kFewSlots * kFewSlot;
 constexpr int kFewMaxPairs = kFewTokens * kMaxTopK + kFewTokens;       // with the shared expert's
 constexpr int kFewMaxLists = kFewTokens * kMaxTopK + 1;                // experts with rows
 
@@ -39,11 +40,12 @@ struct FewArgs {
     int H, I, E, T, k, shared, group, logits_bf16;
 };
 
-// Inputs of a row in a warp's 128 bytes, and in one step of its loop.
+// A block of a row: the 64 bytes that the four lanes of a fragment's row read at once.
 template <int WT>
-constexpr int kFewWarpInputs = WT == MOE_WEIGHTS_BF16 ? 64 : WT == MOE_WEIGHTS_FP8_B128 ? 128 : 256;
+constexpr int kFewBlockInputs = WT == MOE_WEIGHTS_BF16 ? 32 : WT == MOE_WEIGHTS_FP8_B128 ? 64 : 128;
+// Blocks whose inputs a lane loads together, one such step ahead of the products.
 template <int WT>
-constexpr int kFewStepInputs = WT == MOE_WEIGHTS_BF16 ? 64 : 128;
+constexpr int kFewStepBlocks = WT == MOE_WEIGHTS_BF16 ? 4 : WT == MOE_WEIGHTS_FP8_B128 ? 2 : 1;
 
 // The choice by whatever lane width the experts need. Not inlined: one copy of each serves every kernel here.
 template <typename T, int V>
@@ -69,14 +71,13 @@ __device__ __forceinline__ void few_gate(const void *logits, const float *bias, 
 }
 
 // The experts that have rows, in the order of their first pair, the shared one last; list d holds rows off[d] .. off[d + 1] - 1.
-struct FewLists {
+struct alignas(16) FewLists {
     uint16_t expert[kFewMaxLists + 1];
     uint16_t off[kFewMaxLists + 2];
     uint16_t pair[kFewMaxPairs];                   // t (k + shared) + j of a row
     uint8_t token[kFewMaxPairs];
     float weight[kFewMaxPairs];
     int n;
-    int dead;                                      // a wait gave up
 };
 // Needed only while the lists are made; lies where the ring is later.
 struct FewScratch {
@@ -85,15 +86,15 @@ struct FewScratch {
     int16_t chosen[kFewTokens * kMaxTopK];         // expert of a pair, -1: no pair
     float w[kFewTokens * kMaxTopK];
 };
-static_assert(sizeof(FewScratch) <= kFewStages * kFewStage, "the scratch lies within the ring");
+static_assert(sizeof(FewScratch) <= kFewRing, "the scratch lies within the ring");
 
 __device__ __forceinline__ void few_lists(const FewArgs &a, const void *logits, const float *bias, FewLists &l,
                                           FewScratch &s, int32_t *topk_idx, float *topk_w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < a.E; e += kFewThreads) s.mask[e] = 0u;
-    if (tid == 0) l.dead = 0;
+    for (int i = tid; i < (int)(sizeof(FewLists) / 16); i += kFewThreads) reinterpret_cast<uint4 *>(&l)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    for (int t = warp; t < a.T; t += kFewWarps + 1) {
+    for (int t = warp; t < a.T; t += kFewWarps) {
         int e;
         float w;
         bool ok;
@@ -164,32 +165,29 @@ __device__ __forceinline__ void few_lists(const FewArgs &a, const void *logits, 
     __syncthreads();
 }
 
-// The stages of a block's work, in order: for its tiles of 16 matrix rows (up: of one list's expert; down: of each list's
-// expert in turn), the rows' inputs in pieces.
+// The pieces of one warp's work, in order. A unit is 16 matrix rows: up, 8 of the gate's and 8 of the up's of a list's
+// expert; down, 16 of each list's expert in turn. A unit belongs to a team of `team` warps, which take its pieces in
+// turn.
+struct FewPlan {
+    int units, lists, pieces, per, all, first, team, stride;
+};
 template <bool DOWN>
 struct FewWalk {
-    int tile, d, c;                                // up: tile runs over (list, tile of the list's expert)
-    int tiles, lists, pieces, per, stride;
-    __device__ __forceinline__ FewWalk(int lists_, int per_, int pieces_)
-        : d(0), c(0), lists(lists_), pieces(pieces_), per(per_), stride(gridDim.x) {
-        tile = blockIdx.x;
-        tiles = DOWN ? per : per * lists;
-        if (!DOWN) d = tile / per;
+    int unit, q, d, c;                             // q: piece of the unit; d: its list, c: its place in the rows
+    __device__ __forceinline__ void start(const FewPlan &p) {
+        q = c = p.first;
+        d = DOWN ? 0 : unit / p.per;
+        if (DOWN) wrap(p);
     }
-    __device__ __forceinline__ bool more() const { return tile < tiles && lists > 0; }
-    __device__ __forceinline__ int row() const { return DOWN ? tile : tile - d * per; }      // tile within the matrix
-    __device__ __forceinline__ void next() {
-        if (++c < pieces) return;
-        c = 0;
-        if (DOWN) {
-            if (++d < lists) return;
-            d = 0;
-            tile += stride;
-        } else {
-            tile += stride;
-            d = tile / per;
-        }
+    __device__ __forceinline__ bool wrap(const FewPlan &p) {
+        if (c < p.pieces) return false;
+        do {
+            c -= p.pieces;
+            ++d;
+        } while (c >= p.pieces);
+        return true;
     }
+    __device__ __forceinline__ int row(const FewPlan &p) const { return DOWN ? unit : unit - d * p.per; }
 };
 
 // Two bytes of e4m3 at a time -> two bf16: a code's exponent and mantissa bits under a bf16's are its value times
@@ -202,34 +200,114 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w, uint32_t pick) 
     return r;
 }
 
-// What a step needs from global memory besides the weights: 8 columns' inputs and the scales.
+// What a step needs from global memory besides the weights: 8 columns' inputs, and the scales of the fragment's rows g
+// and g + 8.
 template <int WT>
 struct FewOperand {
-    uint4 x[WT == MOE_WEIGHTS_BF16 ? 2 : 4];
-    uint2 sa, sb;                                  // scales of the fragment's rows g and g + 8
+    uint4 x[4];
+    uint2 sa, sb;
 };
 
-__device__ __forceinline__ uint4 ld_l2_v4(const void *p) { return __ldcg(static_cast<const uint4 *>(p)); }
+// Loads whose addresses are only good where the program order comes to them: volatile, so that none is made earlier.
+__device__ __forceinline__ uint32_t ld_u16(const void *p) {
+    uint16_t r;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_u32(const void *p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint2 ld_v2(const void *p) {
+    uint2 r;
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint4 ld_v4(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// A step's products: the fragment rows' blocks at pa (rows g) and pb (rows g + 8) with the inputs of o.
+template <int WT>
+__device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o, const uint8_t *pa, const uint8_t *pb,
+                                         int blocks, int group) {
+    if constexpr (WT == MOE_WEIGHTS_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i >= blocks) break;
+            const uint4 va = *reinterpret_cast<const uint4 *>(pa + 64 * i), vb = *reinterpret_cast<const uint4 *>(pb + 64 * i);
+            mma16816<false>(c, va.x, vb.x, va.y, vb.y, o.x[i].x, o.x[i].y);
+            mma16816<false>(c, va.z, vb.z, va.w, vb.w, o.x[i].z, o.x[i].w);
+        }
+    } else if constexpr (WT == MOE_WEIGHTS_FP8_B128) {
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 va = *reinterpret_cast<const uint4 *>(pa + 64 * i), vb = *reinterpret_cast<const uint4 *>(pb + 64 * i);
+            const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 b = o.x[2 * i + q / 2];
+                mma16816<false>(part, e4m3x2_to_bf16x2(wa[q], 0x1404), e4m3x2_to_bf16x2(wb[q], 0x1404),
+                                e4m3x2_to_bf16x2(wa[q], 0x3424), e4m3x2_to_bf16x2(wb[q], 0x3424), q % 2 ? b.z : b.x,
+                                q % 2 ? b.w : b.y);
+            }
+        }
+        const float sa = __uint_as_float(o.sa.x), sb = __uint_as_float(o.sb.x);
+        c[0] = fmaf(part[0], sa, c[0]);
+        c[1] = fmaf(part[1], sa, c[1]);
+        c[2] = fmaf(part[2], sb, c[2]);
+        c[3] = fmaf(part[3], sb, c[3]);
+    } else {
+        const uint4 va = *reinterpret_cast<const uint4 *>(pa), vb = *reinterpret_cast<const uint4 *>(pb);
+        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+        // the scale of each 32 inputs
+        float sa[4], sb[4];
+        if (group == 32) {
+            sa[0] = bf16_lo(o.sa.x), sa[1] = bf16_hi(o.sa.x), sa[2] = bf16_lo(o.sa.y), sa[3] = bf16_hi(o.sa.y);
+            sb[0] = bf16_lo(o.sb.x), sb[1] = bf16_hi(o.sb.x), sb[2] = bf16_lo(o.sb.y), sb[3] = bf16_hi(o.sb.y);
+        } else {
+            sa[0] = sa[1] = bf16_lo(o.sa.x);
+            sb[0] = sb[1] = bf16_lo(o.sb.x);
+            sa[2] = sa[3] = group == 64 ? bf16_hi(o.sa.x) : sa[0];
+            sb[2] = sb[3] = group == 64 ? bf16_hi(o.sb.x) : sb[0];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t ra[4], rb[4];
+            w4_pairs<false>(wa[j], ra);
+            w4_pairs<false>(wb[j], rb);
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma16816<false>(part, ra[0], rb[0], ra[1], rb[1], o.x[j].x, o.x[j].y);
+            mma16816<false>(part, ra[2], rb[2], ra[3], rb[3], o.x[j].z, o.x[j].w);
+            c[0] = fmaf(part[0], sa[j], c[0]);
+            c[1] = fmaf(part[1], sa[j], c[1]);
+            c[2] = fmaf(part[2], sb[j], c[2]);
+            c[3] = fmaf(part[3], sb[j], c[3]);
+        }
+    }
+}
 
 template <int WT, bool DOWN>
 __global__ void __launch_bounds__(kFewThreads, 2)
-few_kernel(const __grid_constant__ FewArgs a, const uint16_t *__restrict__ x, const void *__restrict__ logits, const float *__restrict__ bias,
-           const uint8_t *__restrict__ w, const void *__restrict__ w_scale, uint16_t *h, int32_t *__restrict__ topk_idx,
-           float *__restrict__ topk_w, uint16_t *__restrict__ out, unsigned *status) {
+few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const void *__restrict__ logits,
+           const float *__restrict__ bias, const uint8_t *__restrict__ w, const void *__restrict__ w_scale, uint16_t *h,
+           int32_t *__restrict__ topk_idx, float *__restrict__ topk_w, uint16_t *__restrict__ out, unsigned *status) {
     extern __shared__ __align__(128) uint8_t few_smem[];
-    __shared__ __align__(8) uint64_t full[kFewStages], empty[kFewStages];
+    __shared__ __align__(8) uint64_t full[kFewWarps][kFewSlots];
     __shared__ FewLists lists;
-    __shared__ float4 red[DOWN ? 1 : 2][DOWN ? 1 : kFewWarps][32];
-    uint8_t *ring = few_smem;
-    // down: each warp's share of out's tile, [warp][token][16]
-    float *acc_out = reinterpret_cast<float *>(few_smem + kFewStages * kFewStage);
-    constexpr int kWarpIn = kFewWarpInputs<WT>, kStep = kFewStepInputs<WT>, kPieceIn = kWarpIn * kFewWarps;
+    __shared__ float4 red[DOWN ? 1 : kFewWarps][32];
+    // down: each warp's share of its unit's outputs, [warp][token][16]
+    float *acc_out = reinterpret_cast<float *>(few_smem + kFewRing);
+    constexpr int kBlockIn = kFewBlockInputs<WT>, kPieceIn = kBlockIn * (kFewPiece / 64);
+    constexpr int kStep = kFewStepBlocks<WT>, kSteps = kFewPiece / 64 / kStep;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    constexpr int kAhead = WT == MOE_WEIGHTS_W4 ? 1 : 2;
     const int K = DOWN ? a.I : a.H, M = DOWN ? a.H : 2 * a.I;
-    if (tid < kFewStages) {
-        mbar_init(&full[tid], 1u);
-        mbar_init(&empty[tid], kFewWarps);
+    if (lane < kFewSlots) {
+        mbar_init(&full[warp][lane], 1u);
         fence_mbar_init();
     }
     if constexpr (!DOWN) {
@@ -237,261 +315,240 @@ few_kernel(const __grid_constant__ FewArgs a, const uint16_t *__restrict__ x, co
         pdl_launch_dependents();
     }
     // The up kernel lets this one start once it has itself waited for all before it: the inputs of the call are there.
-    few_lists(a, logits, bias, lists, *reinterpret_cast<FewScratch *>(ring), DOWN || blockIdx.x != 0 ? nullptr : topk_idx,
-              DOWN || blockIdx.x != 0 ? nullptr : topk_w);
-    const int pieces = (K + kPieceIn - 1) / kPieceIn;
-    const size_t row_bytes = WT == MOE_WEIGHTS_BF16 ? 2 * (size_t)K : WT == MOE_WEIGHTS_FP8_B128 ? (size_t)K : (size_t)K / 2;
-    FewWalk<DOWN> walk(lists.n, DOWN ? a.H / 16 : a.I / 8, pieces);
+    few_lists(a, logits, bias, lists, *reinterpret_cast<FewScratch *>(few_smem),
+              DOWN || blockIdx.x != 0 ? nullptr : topk_idx, DOWN || blockIdx.x != 0 ? nullptr : topk_w);
 
-    if (warp == kFewWarps) {
-        // lane r fetches row r of the tile
-        unsigned n = 0;
-        bool alive = true;
-        for (; walk.more() && alive; walk.next(), ++n) {
-            const unsigned s = n % kFewStages;
-            if (n >= kFewStages && !mbar_wait_bounded(&empty[s], (n / kFewStages - 1u) & 1u)) {
-                alive = false;
-                if (lane == 0) atomicOr(status, kStatusWaitGaveUp);
-                break;
-            }
-            const unsigned bytes = (unsigned)min((size_t)kFewPiece, row_bytes - (size_t)walk.c * kFewPiece);
-            if (lane == 0) mbar_expect_tx(&full[s], kFewRows * bytes);
-            __syncwarp();
-            const int r = lane & 15;
-            const int m = DOWN ? walk.row() * 16 + r : (r < 8 ? 0 : a.I) + walk.row() * 8 + (r & 7);
-            const size_t row = (size_t)lists.expert[walk.d] * M + m;
-            if (lane < 16)
-                bulk_g2s(ring + s * kFewStage + r * kFewPitch, w + row * row_bytes + (size_t)walk.c * kFewPiece, bytes, &full[s]);
-            if (WT == MOE_WEIGHTS_W4 && lane >= 16) {
-                const char *p = static_cast<const char *>(w_scale) + 2 * (row * (size_t)(K / a.group) + (size_t)walk.c * (kPieceIn / a.group));
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-            }
+    FewPlan plan;
+    plan.lists = lists.n;
+    plan.pieces = (K + kPieceIn - 1) / kPieceIn;
+    plan.per = DOWN ? a.H / 16 : a.I / 8;
+    plan.units = DOWN ? (plan.lists > 0 ? plan.per : 0) : plan.per * plan.lists;
+    plan.all = DOWN ? plan.lists * plan.pieces : plan.pieces;
+    plan.team = team;
+    plan.first = warp & (team - 1);
+    plan.stride = gridDim.x * (kFewWarps / team);
+    const unsigned row_bytes = (unsigned)(K / kBlockIn) * 64u, scale_row = (unsigned)(K / 32 / (a.group / 32)) * 2u;
+    // from the unit's row 0 to its row 8
+    const unsigned row8 = DOWN ? 8u : (unsigned)a.I;
+
+    // Fetching: lane r < 16 the unit's row r; with 4-bit weights lane 16 + r that row's scales, as far as L2.
+    FewWalk<DOWN> fw;
+    fw.unit = blockIdx.x + gridDim.x * (warp / team);
+    const uint8_t *from = w;
+    const auto aim = [&]() {                       // `from` for the walk's list and place
+        if (fw.unit >= plan.units || fw.q >= plan.all) return;
+        const size_t row = (size_t)lists.expert[fw.d] * M + fw.row(plan) * (DOWN ? 16 : 8) + (lane & 7) + (lane & 8 ? row8 : 0u);
+        if (WT == MOE_WEIGHTS_W4 && lane >= 16)
+            from = static_cast<const uint8_t *>(w_scale) + row * scale_row + (size_t)fw.c * (kPieceIn * 2 / a.group);
+        else
+            from = w + row * row_bytes + (size_t)fw.c * kFewPiece;
+    };
+    fw.start(plan);
+    aim();
+    unsigned fetched = 0;
+    const auto fetch = [&]() {
+        if (fw.unit >= plan.units || fw.q >= plan.all) return;
+        const unsigned s = fetched % kFewSlots;
+        const unsigned bytes = min((unsigned)kFewPiece, row_bytes - (unsigned)fw.c * kFewPiece);
+        if (lane == 0) mbar_expect_tx(&full[warp][s], kFewRows * bytes);
+        __syncwarp();
+        if (lane < 16)
+            bulk_g2s(few_smem + (warp * kFewSlots + s) * kFewSlot + lane * kFewPitch, from, bytes, &full[warp][s]);
+        else if (WT == MOE_WEIGHTS_W4)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
+        ++fetched;
+        fw.q += plan.team;
+        fw.c += plan.team;
+        if (fw.q >= plan.all) {
+            fw.unit += plan.stride;
+            fw.start(plan);
+            aim();
+        } else if (DOWN && fw.wrap(plan)) {
+            aim();
+        } else {
+            from += plan.team * (WT == MOE_WEIGHTS_W4 && lane >= 16 ? kPieceIn * 2 / a.group : kFewPiece);
         }
-        // no copy outlives the block
-        for (unsigned i = n > kFewStages ? n - kFewStages : 0u; i < n; ++i)
-            mbar_wait_bounded(&full[i % kFewStages], (i / kFewStages) & 1u);
-        return;
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kFewSlots; ++i) fetch();
 
     if constexpr (DOWN) {
-        for (int i = tid; i < kFewWarps * a.T * 16; i += kFewWarps * 32) acc_out[i] = 0.0f;
+        for (int i = lane; i < a.T * 16; i += 32) acc_out[warp * a.T * 16 + i] = 0.0f;
         pdl_wait();                                // h is there
         pdl_launch_dependents();
-        asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory");
+        __syncwarp();
     }
-    // The steps of the loop, two ahead of the products: a stage's inputs of this warp, for each 8 rows of the list.
-    FewWalk<DOWN> at = walk;
-    int at_nt = 0, at_h = 0;
-    const auto load = [&](FewOperand<WT> &o) {
-        // to the next step that has inputs
-        int k0 = 0;
-        for (; at.more(); at.next()) {
-            k0 = at.c * kPieceIn + warp * kWarpIn + at_h * kStep;
-            if (k0 < K) break;
-        }
-        if (!at.more()) return;
-        const int first = lists.off[at.d], rows = lists.off[at.d + 1] - first;
-        const int r = at_nt * 8 + g;
-        constexpr int kVec = WT == MOE_WEIGHTS_BF16 ? 2 : 4;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) o.x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-            const uint16_t *p = (DOWN ? h + (size_t)lists.pair[first + r] * K : x + (size_t)lists.token[first + r] * K) + k0;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const uint16_t *q = p + (WT == MOE_WEIGHTS_FP8_B128 ? 64 * (i / 2) + 16 * t + 8 * (i % 2) : 32 * i + 8 * t);
-                o.x[i] = DOWN ? ld_l2_v4(q) : __ldg(reinterpret_cast<const uint4 *>(q));
-            }
-        }
-        const size_t e = lists.expert[at.d];
-        if constexpr (WT == MOE_WEIGHTS_FP8_B128) {
-            const float *sc = static_cast<const float *>(w_scale) + e * (size_t)(M / 128) * (K / 128) + k0 / 128;
-            const int ma = DOWN ? at.row() * 16 : at.row() * 8, mb = DOWN ? ma : a.I + ma;
-            o.sa.x = __float_as_uint(__ldg(sc + (size_t)(ma / 128) * (K / 128)));
-            o.sb.x = __float_as_uint(__ldg(sc + (size_t)(mb / 128) * (K / 128)));
-        }
-        if constexpr (WT == MOE_WEIGHTS_W4) {
-            const int ma = DOWN ? at.row() * 16 + g : at.row() * 8 + g, mb = DOWN ? ma + 8 : a.I + ma;
-            const uint16_t *sc = static_cast<const uint16_t *>(w_scale) + k0 / a.group;
-            const uint16_t *pa = sc + (e * M + ma) * (size_t)(K / a.group), *pb = sc + (e * M + mb) * (size_t)(K / a.group);
-            if (a.group == 128) {
-                o.sa.x = __ldg(pa);
-                o.sb.x = __ldg(pb);
-            } else if (a.group == 64) {
-                o.sa.x = __ldg(reinterpret_cast<const uint32_t *>(pa));
-                o.sb.x = __ldg(reinterpret_cast<const uint32_t *>(pb));
-            } else {
-                o.sa = __ldg(reinterpret_cast<const uint2 *>(pa));
-                o.sb = __ldg(reinterpret_cast<const uint2 *>(pb));
-            }
-        }
-        // the step after it: the warp's second block of 128, the next 8 rows, the next stage
-        if (WT == MOE_WEIGHTS_W4 && at_h == 0 && k0 + kStep < K) {
-            at_h = 1;
-            return;
-        }
-        at_h = 0;
-        if (8 * ++at_nt < rows) return;
-        at_nt = 0;
-        at.next();
-    };
-    FewOperand<WT> o0, o1, o2;
-    load(o0);
-    if (kAhead == 2) load(o1);
-
-    unsigned n = 0, turn = 0;
-    bool alive = true;
+    constexpr float kUnit = WT == MOE_WEIGHTS_W4 ? kW4Unit<false> : 1.0f;
+    const int first_warp = warp & ~(team - 1);
+    const auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + first_warp), "r"(team * 32) : "memory"); };
     float acc[kFewTokens / 8][4];
 #pragma unroll
     for (int i = 0; i < kFewTokens / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-    for (; walk.more(); ++n) {
-        const unsigned s = n % kFewStages;
-        if (alive && !mbar_wait_bounded(&full[s], (n / kFewStages) & 1u)) {
-            alive = false;                         // outputs stay wrong; the barriers below still meet
-            if (lane == 0) atomicOr(status, kStatusWaitGaveUp);
-        }
-        const int first = lists.off[walk.d], rows = lists.off[walk.d + 1] - first;
-        const uint8_t *base = ring + s * kFewStage + 128 * warp + 16 * t;
-        const int kw = walk.c * kPieceIn + warp * kWarpIn;
+    unsigned n = 0, lost = 0;
+    bool alive = true;
+    int first = 0, rows = 0;
+    // down: the list's rows into this warp's sums of their tokens
+    const auto fold = [&]() {
+        float *mine = acc_out + warp * a.T * 16;
 #pragma unroll
         for (int nt = 0; nt < kFewTokens / 8; ++nt) {
-            if (8 * nt >= rows || kw >= K) continue;                   // warp-uniform
-            float(&c)[4] = acc[nt];
+            if (8 * nt >= rows) break;
+            const int r = 8 * nt + 2 * t;
 #pragma unroll
-            for (int hh = 0; hh < kWarpIn / kStep; ++hh) {
-                if (kw + hh * kStep >= K) continue;
-                load(kAhead == 2 ? o2 : o1);
-                const uint8_t *pa = base + g * kFewPitch + 64 * hh, *pb = pa + 8 * kFewPitch;
-                if constexpr (WT == MOE_WEIGHTS_BF16) {
+            for (int q = 0; q < 2; ++q) {
+                if (r + q < rows) {
+                    const float by = lists.weight[first + r + q] * kUnit;
+                    float *to = mine + lists.token[first + r + q] * 16 + g;
+                    to[0] = fmaf(acc[nt][q], by, to[0]);
+                    to[8] = fmaf(acc[nt][2 + q], by, to[8]);
+                }
+            }
+            acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+        }
+    };
+
+    FewWalk<DOWN> walk;
+    for (walk.unit = blockIdx.x + gridDim.x * (warp / team); walk.unit < plan.units; walk.unit += plan.stride) {
+        walk.start(plan);
+        bool fresh = true;                         // the list is new
+        const uint16_t *px = x;
+        const uint8_t *psa = static_cast<const uint8_t *>(w_scale), *psb = psa;
+        for (; walk.q < plan.all;) {
+            const int k0 = walk.c * kPieceIn;
+            if (fresh) {
+                first = lists.off[walk.d];
+                rows = lists.off[walk.d + 1] - first;
+                const size_t e = lists.expert[walk.d];
+                if constexpr (WT == MOE_WEIGHTS_FP8_B128) {
+                    const int ma = walk.row(plan) * (DOWN ? 16 : 8), mb = DOWN ? ma : a.I + ma;
+                    const uint8_t *sc = static_cast<const uint8_t *>(w_scale) + 4 * (e * (M / 128) * (K / 128));
+                    psa = sc + 4 * (size_t)((ma / 128) * (K / 128));
+                    psb = sc + 4 * (size_t)((mb / 128) * (K / 128));
+                }
+                if constexpr (WT == MOE_WEIGHTS_W4) {
+                    psa = static_cast<const uint8_t *>(w_scale) + (e * M + walk.row(plan) * (DOWN ? 16 : 8) + g) * scale_row;
+                    psb = psa + (size_t)row8 * scale_row;
+                }
+                fresh = false;
+            }
+            FewOperand<WT> o;
+            const auto load = [&](FewOperand<WT> &to, int nt, int step) {
+                if (step == 0) {                   // columns past the rows read the last one, and are not stored
+                    const int r = first + min(8 * nt + g, rows - 1);
+                    px = (DOWN ? h + (size_t)lists.pair[r] * K : x + (size_t)lists.token[r] * K) + k0 +
+                         (WT == MOE_WEIGHTS_FP8_B128 ? 16 : 8) * t;
+                }
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 va = *reinterpret_cast<const uint4 *>(pa + 64 * i);
-                        const uint4 vb = *reinterpret_cast<const uint4 *>(pb + 64 * i);
-                        mma16816<false>(c, va.x, vb.x, va.y, vb.y, o0.x[i].x, o0.x[i].y);
-                        mma16816<false>(c, va.z, vb.z, va.w, vb.w, o0.x[i].z, o0.x[i].w);
-                    }
-                } else if constexpr (WT == MOE_WEIGHTS_FP8_B128) {
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 va = *reinterpret_cast<const uint4 *>(pa + 64 * i);
-                        const uint4 vb = *reinterpret_cast<const uint4 *>(pb + 64 * i);
-                        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint4 b = o0.x[2 * i + q / 2];
-                            mma16816<false>(part, e4m3x2_to_bf16x2(wa[q], 0x1404), e4m3x2_to_bf16x2(wb[q], 0x1404),
-                                            e4m3x2_to_bf16x2(wa[q], 0x3424), e4m3x2_to_bf16x2(wb[q], 0x3424),
-                                            q % 2 ? b.z : b.x, q % 2 ? b.w : b.y);
-                        }
-                    }
-                    const float sa = __uint_as_float(o0.sa.x), sb = __uint_as_float(o0.sb.x);
-                    c[0] = fmaf(part[0], sa, c[0]);
-                    c[1] = fmaf(part[1], sa, c[1]);
-                    c[2] = fmaf(part[2], sb, c[2]);
-                    c[3] = fmaf(part[3], sb, c[3]);
-                } else {
-                    const uint4 va = *reinterpret_cast<const uint4 *>(pa), vb = *reinterpret_cast<const uint4 *>(pb);
-                    const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-                    // the scale of each 32 inputs
-                    float sa[4], sb[4];
-                    if (a.group == 32) {
-                        sa[0] = bf16_lo(o0.sa.x), sa[1] = bf16_hi(o0.sa.x), sa[2] = bf16_lo(o0.sa.y), sa[3] = bf16_hi(o0.sa.y);
-                        sb[0] = bf16_lo(o0.sb.x), sb[1] = bf16_hi(o0.sb.x), sb[2] = bf16_lo(o0.sb.y), sb[3] = bf16_hi(o0.sb.y);
+                for (int i = 0; i < 4; ++i) {
+                    if (WT != MOE_WEIGHTS_BF16 || k0 + 32 * i < K)
+                        to.x[i] = ld_v4(px + step * kStep * kBlockIn +
+                                        (WT == MOE_WEIGHTS_FP8_B128 ? 64 * (i / 2) + 8 * (i % 2) : 32 * i));
+                }
+                const int at = k0 / 128 + step;    // block of 128 inputs
+                if constexpr (WT == MOE_WEIGHTS_FP8_B128) {
+                    to.sa.x = ld_u32(psa + 4 * at);
+                    to.sb.x = ld_u32(psb + 4 * at);
+                }
+                if constexpr (WT == MOE_WEIGHTS_W4) {
+                    if (a.group == 128) {
+                        to.sa.x = ld_u16(psa + 2 * at);
+                        to.sb.x = ld_u16(psb + 2 * at);
+                    } else if (a.group == 64) {
+                        to.sa.x = ld_u32(psa + 4 * at);
+                        to.sb.x = ld_u32(psb + 4 * at);
                     } else {
-                        sa[0] = sa[1] = bf16_lo(o0.sa.x);
-                        sb[0] = sb[1] = bf16_lo(o0.sb.x);
-                        sa[2] = sa[3] = a.group == 64 ? bf16_hi(o0.sa.x) : sa[0];
-                        sb[2] = sb[3] = a.group == 64 ? bf16_hi(o0.sb.x) : sb[0];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t ra[4], rb[4];
-                        w4_pairs<false>(wa[j], ra);
-                        w4_pairs<false>(wb[j], rb);
-                        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16816<false>(part, ra[0], rb[0], ra[1], rb[1], o0.x[j].x, o0.x[j].y);
-                        mma16816<false>(part, ra[2], rb[2], ra[3], rb[3], o0.x[j].z, o0.x[j].w);
-                        c[0] = fmaf(part[0], sa[j], c[0]);
-                        c[1] = fmaf(part[1], sa[j], c[1]);
-                        c[2] = fmaf(part[2], sb[j], c[2]);
-                        c[3] = fmaf(part[3], sb[j], c[3]);
+                        to.sa = ld_v2(psa + 8 * at);
+                        to.sb = ld_v2(psb + 8 * at);
                     }
                 }
-                o0 = o1;
-                if (kAhead == 2) o1 = o2;
+            };
+            load(o, 0, 0);
+            const unsigned s = n % kFewSlots;
+            if (alive && !__all_sync(kFull, mbar_wait_bounded(&full[warp][s], (n / kFewSlots) & 1u))) {
+                alive = false;                     // outputs stay wrong; the barriers below still meet
+                lost = n;
+                if (lane == 0) atomicOr(status, kStatusWaitGaveUp);
+            }
+            const uint8_t *pa = few_smem + (warp * kFewSlots + s) * kFewSlot + g * kFewPitch + 16 * t, *pb = pa + 8 * kFewPitch;
+            const int blocks = min(kFewPiece / 64, (K - k0) / kBlockIn);
+#pragma unroll
+            for (int nt = 0; nt < kFewTokens / 8; ++nt) {
+                if (8 * nt >= rows) break;         // warp-uniform
+                if constexpr (kSteps == 1) {
+                    few_step<WT>(acc[nt], o, pa, pb, blocks, a.group);
+                    if (8 * (nt + 1) < rows) load(o, nt + 1, 0);
+                } else {
+#pragma unroll 2
+                    for (int step = 0; step < kSteps; ++step) {
+                        if (step * kStep >= blocks) break;
+                        FewOperand<WT> next;
+                        if ((step + 1) * kStep < blocks) load(next, nt, step + 1);
+                        else if (8 * (nt + 1) < rows) load(next, nt + 1, 0);
+                        few_step<WT>(acc[nt], o, pa + 64 * kStep * step, pb + 64 * kStep * step, blocks, a.group);
+                        o = next;
+                    }
+                }
+            }
+            ++n;
+            __syncwarp();                          // every lane has read the slot
+            if (alive) fetch();
+            walk.q += plan.team;
+            walk.c += plan.team;
+            if (DOWN && walk.wrap(plan)) {
+                fold();
+                fresh = true;
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
 
-        const FewWalk<DOWN> was = walk;
-        walk.next();
-        if (was.c + 1 < was.pieces) continue;      // the rows go on
-        constexpr float kUnit = WT == MOE_WEIGHTS_W4 ? kW4Unit<false> : 1.0f;
         if constexpr (!DOWN) {
-            // the warps' sums joined by one of them in turn, which makes h of them. Two buffers: who writes one again
-            // has passed the barrier of the other, which its readers pass after reading
+            // h from the sums of the unit's list, joined over the team's warps
+            first = lists.off[walk.d];
+            rows = lists.off[walk.d + 1] - first;
 #pragma unroll
             for (int nt = 0; nt < kFewTokens / 8; ++nt) {
-                if (8 * nt >= rows) continue;
-                red[turn & 1u][warp][lane] = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+                if (8 * nt >= rows) break;
+                float4 v = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
                 acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-                asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory");
-                if ((unsigned)warp == turn % kFewWarps) {
-                    float4 v = red[turn & 1u][0][lane];
-#pragma unroll
-                    for (int i = 1; i < kFewWarps; ++i) {
-                        const float4 u = red[turn & 1u][i][lane];
-                        v.x += u.x;
-                        v.y += u.y;
-                        v.z += u.z;
-                        v.w += u.w;
+                if (team > 1) {
+                    red[warp][lane] = v;
+                    team_sync();
+                    if (warp == first_warp) {
+                        for (int i = 1; i < team; ++i) {
+                            const float4 u = red[warp + i][lane];
+                            v.x += u.x;
+                            v.y += u.y;
+                            v.z += u.z;
+                            v.w += u.w;
+                        }
                     }
-                    const int r = 8 * nt + 2 * t, o = was.row() * 8 + g;
-                    if (r < rows) put_bf16(h + (size_t)lists.pair[first + r] * a.I + o, silu(v.x * kUnit) * (v.z * kUnit));
-                    if (r + 1 < rows)
-                        put_bf16(h + (size_t)lists.pair[first + r + 1] * a.I + o, silu(v.y * kUnit) * (v.w * kUnit));
+                    team_sync();
+                    if (warp != first_warp) continue;
                 }
-                ++turn;
+                const int r = 8 * nt + 2 * t, o = walk.row(plan) * 8 + g;
+                if (r < rows) put_bf16(h + (size_t)lists.pair[first + r] * a.I + o, silu(v.x * kUnit) * (v.z * kUnit));
+                if (r + 1 < rows) put_bf16(h + (size_t)lists.pair[first + r + 1] * a.I + o, silu(v.y * kUnit) * (v.w * kUnit));
             }
         } else {
-            // this list's rows into the warp's sums of their tokens
-            float *mine = acc_out + warp * a.T * 16;
-#pragma unroll
-            for (int nt = 0; nt < kFewTokens / 8; ++nt) {
-                if (8 * nt >= rows) continue;
-                const int r = 8 * nt + 2 * t;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (r + q < rows) {
-                        const float by = lists.weight[first + r + q] * kUnit;
-                        float *to = mine + lists.token[first + r + q] * 16 + g;
-                        to[0] = fmaf(acc[nt][q], by, to[0]);
-                        to[8] = fmaf(acc[nt][2 + q], by, to[8]);
-                    }
-                }
-                acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-            }
-            __syncwarp();
-            if (was.d + 1 < was.lists) continue;
-            asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory");
-            for (int i = tid; i < a.T * 16; i += kFewWarps * 32) {
+            if (!fresh) fold();
+            team_sync();
+            const float *sums = acc_out + first_warp * a.T * 16;
+            for (int i = (warp - first_warp) * 32 + lane; i < a.T * 16; i += team * 32) {
                 float v = 0.0f;
-#pragma unroll
-                for (int j = 0; j < kFewWarps; ++j) {
-                    v += acc_out[j * a.T * 16 + i];
-                    acc_out[j * a.T * 16 + i] = 0.0f;
-                }
-                put_bf16(out + (size_t)(i >> 4) * a.H + was.row() * 16 + (i & 15), v);
+                for (int j = 0; j < team; ++j) v += sums[j * a.T * 16 + i];
+                put_bf16(out + (size_t)(i >> 4) * a.H + walk.row(plan) * 16 + (i & 15), v);
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(kFewWarps * 32) : "memory");
+            team_sync();
+            for (int i = lane; i < a.T * 16; i += 32) acc_out[warp * a.T * 16 + i] = 0.0f;
+            __syncwarp();
         }
     }
     if constexpr (DOWN) {
         if (lists.n == 0)                          // not one pair in the whole batch
-            for (int i = blockIdx.x * kFewWarps * 32 + tid; i < a.T * a.H; i += gridDim.x * kFewWarps * 32) out[i] = 0;
+            for (int i = blockIdx.x * kFewThreads + tid; i < a.T * a.H; i += gridDim.x * kFewThreads) out[i] = 0;
     }
+    // after a wait that gave up: no copy outlives the block
+    if (!alive)
+        for (; lost < fetched; ++lost) mbar_wait_bounded(&full[warp][lost % kFewSlots], (lost / kFewSlots) & 1u);
 }
 
 int check_mlp(const moe_mlp *m) {
@@ -508,23 +565,38 @@ int check_few(const Dims &d, const moe_mlp *m) {
     return MOE_OK;
 }
 
+// Blocks, and warps to a unit: as many as all units at work at once leave it of the warps of GB300's 152 SMs, two blocks on
+// each. By the sizes alone: the grid does not change a sum's order.
+int few_team(long long units) {
+    int team = 1;
+    while (team < kFewWarps && units * team * 2 <= 2LL * 152 * kFewWarps) team *= 2;
+    return team;
+}
+int few_grid(long long units, int max_blocks) {
+    const long long blocks = (units * few_team(units) + kFewWarps - 1) / kFewWarps;
+    return persistent_grid(std::min(blocks, units), 2 * sm_count(), max_blocks);
+}
+
 template <int WT>
 int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, const void *logits, const float *bias,
                const void *w_up, const void *up_scale, const void *w_down, const void *down_scale, int32_t *idx, float *w,
                void *out, void *h, unsigned *status) {
     static PerContext<int> up_done, down_done;
-    const size_t ring = (size_t)kFewStages * kFewStage, most = ring + kFewWarps * kFewTokens * 16 * sizeof(float);
+    const size_t ring = kFewRing, most = ring + kFewWarps * kFewTokens * 16 * sizeof(float);
     if (!set_smem_once(up_done, few_kernel<WT, false>, (int)ring) || !set_smem_once(down_done, few_kernel<WT, true>, (int)most))
         return MOE_ERR_CUDA;
     const long long lists = std::min<long long>((long long)d.T * d.k, d.E) + a.shared;
-    int grid = persistent_grid(lists * (a.I / 8), sm_count(), d.max_blocks);
-    if (launch_pdl_smem(few_kernel<WT, false>, grid, kFewThreads, ring, st, a, static_cast<const uint16_t *>(x), logits, bias,
-                        static_cast<const uint8_t *>(w_up), up_scale, static_cast<uint16_t *>(h), idx, w,
+    long long units = lists * (a.I / 8);
+    int grid = few_grid(units, d.max_blocks), team = few_team(units);
+    if (launch_pdl_smem(few_kernel<WT, false>, grid, kFewThreads, ring, st, a, team, static_cast<const uint16_t *>(x), logits,
+                        bias, static_cast<const uint8_t *>(w_up), up_scale, static_cast<uint16_t *>(h), idx, w,
                         static_cast<uint16_t *>(out), status) != cudaSuccess)
         return MOE_ERR_CUDA;
-    grid = persistent_grid(d.H / 16, sm_count(), d.max_blocks);
+    units = d.H / 16;
+    grid = few_grid(units, d.max_blocks);
+    team = few_team(units);
     if (launch_pdl_smem(few_kernel<WT, true>, grid, kFewThreads, ring + (size_t)kFewWarps * d.T * 16 * sizeof(float), st, a,
-                        static_cast<const uint16_t *>(x), logits, bias, static_cast<const uint8_t *>(w_down), down_scale,
+                        team, static_cast<const uint16_t *>(x), logits, bias, static_cast<const uint8_t *>(w_down), down_scale,
                         static_cast<uint16_t *>(h), idx, w, static_cast<uint16_t *>(out), status) != cudaSuccess)
         return MOE_ERR_CUDA;
     return MOE_OK;
@@ -569,7 +641,7 @@ extern "C" int moe_layer_few(const moe_problem *p, const moe_gate *gate, const m
     a.T = d.T;
     a.k = d.k;
     a.shared = mlp->shared;
-    a.group = mlp->group;
+    a.group = mlp->weights == MOE_WEIGHTS_W4 ? mlp->group : 128;
     a.logits_bf16 = gate->logits_type == MOE_LOGITS_BF16;
     unsigned *status = device_status_word();
     if (status == nullptr) return MOE_ERR_CUDA;
