@@ -16,6 +16,7 @@
 //   - every block forms the choice itself, from the logits: no launch and no wait between
 //     the router and the products.
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_gate.cuh"
 #include "moe_w4.cuh"
@@ -37,15 +38,22 @@ constexpr int kFewMaxLists = kFewTokens * kMaxTopK + 1;                // expert
 
 struct FewArgs {
     GateArgs gate;
-    int H, I, E, T, k, shared, group, logits_bf16;
+    int H, I, E, T, k, shared, logits_bf16;
 };
+
+// The kernels' kind of weights: moe_weights, the 4-bit ones by their group.
+enum FewKind { kBf16, kFp8, kW4G32, kW4G64, kW4G128 };
+template <int WT>
+constexpr bool kIsW4 = WT >= kW4G32;
+template <int WT>
+constexpr int kFewGroup = WT == kW4G32 ? 32 : WT == kW4G64 ? 64 : 128;
 
 // A block of a row: the 64 bytes that the four lanes of a fragment's row read at once.
 template <int WT>
-constexpr int kFewBlockInputs = WT == MOE_WEIGHTS_BF16 ? 32 : WT == MOE_WEIGHTS_FP8_B128 ? 64 : 128;
+constexpr int kFewBlockInputs = WT == kBf16 ? 32 : WT == kFp8 ? 64 : 128;
 // Blocks whose inputs a lane loads together, one such step ahead of the products.
 template <int WT>
-constexpr int kFewStepBlocks = WT == MOE_WEIGHTS_BF16 ? 4 : WT == MOE_WEIGHTS_FP8_B128 ? 2 : 1;
+constexpr int kFewStepBlocks = WT == kBf16 ? 4 : WT == kFp8 ? 2 : 1;
 
 // The choice by whatever lane width the experts need. Not inlined: one copy of each serves every kernel here.
 template <typename T, int V>
@@ -230,11 +238,25 @@ __device__ __forceinline__ uint4 ld_v4(const void *p) {
     return r;
 }
 
+// The first product of a sum: d = A B.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void add_scaled(float (&c)[4], const float (&part)[4], float sa, float sb) {
+    c[0] = fmaf(part[0], sa, c[0]);
+    c[1] = fmaf(part[1], sa, c[1]);
+    c[2] = fmaf(part[2], sb, c[2]);
+    c[3] = fmaf(part[3], sb, c[3]);
+}
+
 // A step's products: the fragment rows' blocks at pa (rows g) and pb (rows g + 8) with the inputs of o.
 template <int WT>
 __device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o, const uint8_t *pa, const uint8_t *pb,
-                                         int blocks, int group) {
-    if constexpr (WT == MOE_WEIGHTS_BF16) {
+                                         int blocks) {
+    if constexpr (WT == kBf16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= blocks) break;
@@ -242,8 +264,8 @@ __device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o,
             mma16816<false>(c, va.x, vb.x, va.y, vb.y, o.x[i].x, o.x[i].y);
             mma16816<false>(c, va.z, vb.z, va.w, vb.w, o.x[i].z, o.x[i].w);
         }
-    } else if constexpr (WT == MOE_WEIGHTS_FP8_B128) {
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    } else if constexpr (WT == kFp8) {
+        float part[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint4 va = *reinterpret_cast<const uint4 *>(pa + 64 * i), vb = *reinterpret_cast<const uint4 *>(pb + 64 * i);
@@ -251,42 +273,31 @@ __device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o,
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint4 b = o.x[2 * i + q / 2];
-                mma16816<false>(part, e4m3x2_to_bf16x2(wa[q], 0x1404), e4m3x2_to_bf16x2(wb[q], 0x1404),
-                                e4m3x2_to_bf16x2(wa[q], 0x3424), e4m3x2_to_bf16x2(wb[q], 0x3424), q % 2 ? b.z : b.x,
-                                q % 2 ? b.w : b.y);
+                const uint32_t a0 = e4m3x2_to_bf16x2(wa[q], 0x1404), a1 = e4m3x2_to_bf16x2(wb[q], 0x1404);
+                const uint32_t a2 = e4m3x2_to_bf16x2(wa[q], 0x3424), a3 = e4m3x2_to_bf16x2(wb[q], 0x3424);
+                if (i == 0 && q == 0) mma16816_first(part, a0, a1, a2, a3, b.x, b.y);
+                else mma16816<false>(part, a0, a1, a2, a3, q % 2 ? b.z : b.x, q % 2 ? b.w : b.y);
             }
         }
-        const float sa = __uint_as_float(o.sa.x), sb = __uint_as_float(o.sb.x);
-        c[0] = fmaf(part[0], sa, c[0]);
-        c[1] = fmaf(part[1], sa, c[1]);
-        c[2] = fmaf(part[2], sb, c[2]);
-        c[3] = fmaf(part[3], sb, c[3]);
+        add_scaled(c, part, __uint_as_float(o.sa.x), __uint_as_float(o.sb.x));
     } else {
         const uint4 va = *reinterpret_cast<const uint4 *>(pa), vb = *reinterpret_cast<const uint4 *>(pb);
         const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-        // the scale of each 32 inputs
-        float sa[4], sb[4];
-        if (group == 32) {
-            sa[0] = bf16_lo(o.sa.x), sa[1] = bf16_hi(o.sa.x), sa[2] = bf16_lo(o.sa.y), sa[3] = bf16_hi(o.sa.y);
-            sb[0] = bf16_lo(o.sb.x), sb[1] = bf16_hi(o.sb.x), sb[2] = bf16_lo(o.sb.y), sb[3] = bf16_hi(o.sb.y);
-        } else {
-            sa[0] = sa[1] = bf16_lo(o.sa.x);
-            sb[0] = sb[1] = bf16_lo(o.sb.x);
-            sa[2] = sa[3] = group == 64 ? bf16_hi(o.sa.x) : sa[0];
-            sb[2] = sb[3] = group == 64 ? bf16_hi(o.sb.x) : sb[0];
-        }
+        constexpr int kPer = kFewGroup<WT> / 32;                       // blocks of 32 inputs to a group
+        float part[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t ra[4], rb[4];
             w4_pairs<false>(wa[j], ra);
             w4_pairs<false>(wb[j], rb);
-            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16816<false>(part, ra[0], rb[0], ra[1], rb[1], o.x[j].x, o.x[j].y);
+            if (j % kPer == 0) mma16816_first(part, ra[0], rb[0], ra[1], rb[1], o.x[j].x, o.x[j].y);
+            else mma16816<false>(part, ra[0], rb[0], ra[1], rb[1], o.x[j].x, o.x[j].y);
             mma16816<false>(part, ra[2], rb[2], ra[3], rb[3], o.x[j].z, o.x[j].w);
-            c[0] = fmaf(part[0], sa[j], c[0]);
-            c[1] = fmaf(part[1], sa[j], c[1]);
-            c[2] = fmaf(part[2], sb[j], c[2]);
-            c[3] = fmaf(part[3], sb[j], c[3]);
+            if (j % kPer == kPer - 1) {
+                const uint32_t sa = j / kPer < 2 ? o.sa.x : o.sa.y, sb = j / kPer < 2 ? o.sb.x : o.sb.y;
+                if (j / kPer % 2 == 0) add_scaled(c, part, bf16_lo(sa), bf16_lo(sb));
+                else add_scaled(c, part, bf16_hi(sa), bf16_hi(sb));
+            }
         }
     }
 }
@@ -303,7 +314,7 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
     // down: each warp's share of its unit's outputs, [warp][token][16]
     float *acc_out = reinterpret_cast<float *>(few_smem + kFewRing);
     constexpr int kBlockIn = kFewBlockInputs<WT>, kPieceIn = kBlockIn * (kFewPiece / 64);
-    constexpr int kStep = kFewStepBlocks<WT>, kSteps = kFewPiece / 64 / kStep;
+    constexpr int kGroup = kFewGroup<WT>, kStep = kFewStepBlocks<WT>, kSteps = kFewPiece / 64 / kStep;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int K = DOWN ? a.I : a.H, M = DOWN ? a.H : 2 * a.I;
     if (lane < kFewSlots) {
@@ -327,7 +338,7 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
     plan.team = team;
     plan.first = warp & (team - 1);
     plan.stride = gridDim.x * (kFewWarps / team);
-    const unsigned row_bytes = (unsigned)(K / kBlockIn) * 64u, scale_row = (unsigned)(K / 32 / (a.group / 32)) * 2u;
+    const unsigned row_bytes = (unsigned)(K / kBlockIn) * 64u, scale_row = (unsigned)(K / kGroup) * 2u;
     // from the unit's row 0 to its row 8
     const unsigned row8 = DOWN ? 8u : (unsigned)a.I;
 
@@ -338,8 +349,8 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
     const auto aim = [&]() {                       // `from` for the walk's list and place
         if (fw.unit >= plan.units || fw.q >= plan.all) return;
         const size_t row = (size_t)lists.expert[fw.d] * M + fw.row(plan) * (DOWN ? 16 : 8) + (lane & 7) + (lane & 8 ? row8 : 0u);
-        if (WT == MOE_WEIGHTS_W4 && lane >= 16)
-            from = static_cast<const uint8_t *>(w_scale) + row * scale_row + (size_t)fw.c * (kPieceIn * 2 / a.group);
+        if (kIsW4<WT> && lane >= 16)
+            from = static_cast<const uint8_t *>(w_scale) + row * scale_row + (size_t)fw.c * (kPieceIn * 2 / kGroup);
         else
             from = w + row * row_bytes + (size_t)fw.c * kFewPiece;
     };
@@ -354,7 +365,7 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
         __syncwarp();
         if (lane < 16)
             bulk_g2s(few_smem + (warp * kFewSlots + s) * kFewSlot + lane * kFewPitch, from, bytes, &full[warp][s]);
-        else if (WT == MOE_WEIGHTS_W4)
+        else if (kIsW4<WT>)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
         ++fetched;
         fw.q += plan.team;
@@ -366,7 +377,7 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
         } else if (DOWN && fw.wrap(plan)) {
             aim();
         } else {
-            from += plan.team * (WT == MOE_WEIGHTS_W4 && lane >= 16 ? kPieceIn * 2 / a.group : kFewPiece);
+            from += plan.team * (kIsW4<WT> && lane >= 16 ? kPieceIn * 2 / kGroup : kFewPiece);
         }
     };
 #pragma unroll
@@ -378,7 +389,7 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
         pdl_launch_dependents();
         __syncwarp();
     }
-    constexpr float kUnit = WT == MOE_WEIGHTS_W4 ? kW4Unit<false> : 1.0f;
+    constexpr float kUnit = kIsW4<WT> ? kW4Unit<false> : 1.0f;
     const int first_warp = warp & ~(team - 1);
     const auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + first_warp), "r"(team * 32) : "memory"); };
     float acc[kFewTokens / 8][4];
@@ -411,58 +422,56 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
     for (walk.unit = blockIdx.x + gridDim.x * (warp / team); walk.unit < plan.units; walk.unit += plan.stride) {
         walk.start(plan);
         bool fresh = true;                         // the list is new
+        // at the piece: a lane's inputs of its column of the first eight, and its rows' scales. Columns past the rows read
+        // the last row, and are not stored.
         const uint16_t *px = x;
         const uint8_t *psa = static_cast<const uint8_t *>(w_scale), *psb = psa;
         for (; walk.q < plan.all;) {
             const int k0 = walk.c * kPieceIn;
+            const auto column = [&](int nt) {
+                const int r = first + min(8 * nt + g, rows - 1);
+                return (DOWN ? h + (size_t)lists.pair[r] * K : x + (size_t)lists.token[r] * K) + k0 + (WT == kFp8 ? 16 : 8) * t;
+            };
             if (fresh) {
                 first = lists.off[walk.d];
                 rows = lists.off[walk.d + 1] - first;
                 const size_t e = lists.expert[walk.d];
-                if constexpr (WT == MOE_WEIGHTS_FP8_B128) {
+                if constexpr (WT == kFp8) {
                     const int ma = walk.row(plan) * (DOWN ? 16 : 8), mb = DOWN ? ma : a.I + ma;
-                    const uint8_t *sc = static_cast<const uint8_t *>(w_scale) + 4 * (e * (M / 128) * (K / 128));
+                    const uint8_t *sc = static_cast<const uint8_t *>(w_scale) + 4 * (e * (M / 128) * (K / 128) + k0 / 128);
                     psa = sc + 4 * (size_t)((ma / 128) * (K / 128));
                     psb = sc + 4 * (size_t)((mb / 128) * (K / 128));
                 }
-                if constexpr (WT == MOE_WEIGHTS_W4) {
-                    psa = static_cast<const uint8_t *>(w_scale) + (e * M + walk.row(plan) * (DOWN ? 16 : 8) + g) * scale_row;
+                if constexpr (kIsW4<WT>) {
+                    psa = static_cast<const uint8_t *>(w_scale) + (e * M + walk.row(plan) * (DOWN ? 16 : 8) + g) * scale_row +
+                          k0 / kGroup * 2;
                     psb = psa + (size_t)row8 * scale_row;
                 }
+                px = column(0);
                 fresh = false;
             }
-            FewOperand<WT> o;
-            const auto load = [&](FewOperand<WT> &to, int nt, int step) {
-                if (step == 0) {                   // columns past the rows read the last one, and are not stored
-                    const int r = first + min(8 * nt + g, rows - 1);
-                    px = (DOWN ? h + (size_t)lists.pair[r] * K : x + (size_t)lists.token[r] * K) + k0 +
-                         (WT == MOE_WEIGHTS_FP8_B128 ? 16 : 8) * t;
-                }
+            const auto load = [&](FewOperand<WT> &to, const uint16_t *p, int step, bool whole) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (WT != MOE_WEIGHTS_BF16 || k0 + 32 * i < K)
-                        to.x[i] = ld_v4(px + step * kStep * kBlockIn +
-                                        (WT == MOE_WEIGHTS_FP8_B128 ? 64 * (i / 2) + 8 * (i % 2) : 32 * i));
-                }
-                const int at = k0 / 128 + step;    // block of 128 inputs
-                if constexpr (WT == MOE_WEIGHTS_FP8_B128) {
-                    to.sa.x = ld_u32(psa + 4 * at);
-                    to.sb.x = ld_u32(psb + 4 * at);
-                }
-                if constexpr (WT == MOE_WEIGHTS_W4) {
-                    if (a.group == 128) {
-                        to.sa.x = ld_u16(psa + 2 * at);
-                        to.sb.x = ld_u16(psb + 2 * at);
-                    } else if (a.group == 64) {
-                        to.sa.x = ld_u32(psa + 4 * at);
-                        to.sb.x = ld_u32(psb + 4 * at);
-                    } else {
-                        to.sa = ld_v2(psa + 8 * at);
-                        to.sb = ld_v2(psb + 8 * at);
-                    }
+                for (int i = 0; i < 4; ++i)
+                    if (WT != kBf16 || whole || k0 + (step * kStep + i) * kBlockIn < K)
+                        to.x[i] = ld_v4(p + step * kStep * kBlockIn + (WT == kFp8 ? 64 * (i / 2) + 8 * (i % 2) : 32 * i));
+                if constexpr (WT == kFp8) {
+                    to.sa.x = ld_u32(psa + 4 * step);
+                    to.sb.x = ld_u32(psb + 4 * step);
+                } else if constexpr (WT == kW4G128) {
+                    to.sa.x = ld_u16(psa + 2 * step);
+                    to.sb.x = ld_u16(psb + 2 * step);
+                } else if constexpr (WT == kW4G64) {
+                    to.sa.x = ld_u32(psa + 4 * step);
+                    to.sb.x = ld_u32(psb + 4 * step);
+                } else if constexpr (WT == kW4G32) {
+                    to.sa = ld_v2(psa + 8 * step);
+                    to.sb = ld_v2(psb + 8 * step);
                 }
             };
-            load(o, 0, 0);
+            const int blocks = min(kFewPiece / 64, (K - k0) / kBlockIn);
+            FewOperand<WT> o;
+            load(o, px, 0, false);
             const unsigned s = n % kFewSlots;
             if (alive && !__all_sync(kFull, mbar_wait_bounded(&full[warp][s], (n / kFewSlots) & 1u))) {
                 alive = false;                     // outputs stay wrong; the barriers below still meet
@@ -470,22 +479,28 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
                 if (lane == 0) atomicOr(status, kStatusWaitGaveUp);
             }
             const uint8_t *pa = few_smem + (warp * kFewSlots + s) * kFewSlot + g * kFewPitch + 16 * t, *pb = pa + 8 * kFewPitch;
-            const int blocks = min(kFewPiece / 64, (K - k0) / kBlockIn);
+            if (rows <= 8 && blocks == kFewPiece / 64) {               // most pieces: steps and offsets known
 #pragma unroll
-            for (int nt = 0; nt < kFewTokens / 8; ++nt) {
-                if (8 * nt >= rows) break;         // warp-uniform
-                if constexpr (kSteps == 1) {
-                    few_step<WT>(acc[nt], o, pa, pb, blocks, a.group);
-                    if (8 * (nt + 1) < rows) load(o, nt + 1, 0);
-                } else {
-#pragma unroll 2
-                    for (int step = 0; step < kSteps; ++step) {
-                        if (step * kStep >= blocks) break;
-                        FewOperand<WT> next;
-                        if ((step + 1) * kStep < blocks) load(next, nt, step + 1);
-                        else if (8 * (nt + 1) < rows) load(next, nt + 1, 0);
-                        few_step<WT>(acc[nt], o, pa + 64 * kStep * step, pb + 64 * kStep * step, blocks, a.group);
-                        o = next;
+                for (int step = 0; step < kSteps; ++step) {
+                    FewOperand<WT> next;
+                    if (step + 1 < kSteps) load(next, px, step + 1, true);
+                    few_step<WT>(acc[0], o, pa + 64 * kStep * step, pb + 64 * kStep * step, kStep);
+                    if (step + 1 < kSteps) o = next;
+                }
+            } else {
+                const uint16_t *p = px;
+#pragma unroll
+                for (int nt = 0; nt < kFewTokens / 8; ++nt) {
+                    if (8 * nt >= rows) break;     // warp-uniform
+#pragma unroll 1
+                    for (int step = 0; step * kStep < blocks; ++step) {
+                        few_step<WT>(acc[nt], o, pa + 64 * kStep * step, pb + 64 * kStep * step, blocks - step * kStep);
+                        if ((step + 1) * kStep < blocks) {
+                            load(o, p, step + 1, false);
+                        } else if (8 * (nt + 1) < rows) {
+                            p = column(nt + 1);
+                            load(o, p, 0, false);
+                        }
                     }
                 }
             }
@@ -494,6 +509,15 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
             if (alive) fetch();
             walk.q += plan.team;
             walk.c += plan.team;
+            px += plan.team * kPieceIn;
+            if (WT == kFp8) {
+                psa += plan.team * (kPieceIn / 128) * 4;
+                psb += plan.team * (kPieceIn / 128) * 4;
+            }
+            if (kIsW4<WT>) {
+                psa += plan.team * (kPieceIn * 2 / kGroup);
+                psb += plan.team * (kPieceIn * 2 / kGroup);
+            }
             if (DOWN && walk.wrap(plan)) {
                 fold();
                 fresh = true;
@@ -641,17 +665,17 @@ extern "C" int moe_layer_few(const moe_problem *p, const moe_gate *gate, const m
     a.T = d.T;
     a.k = d.k;
     a.shared = mlp->shared;
-    a.group = mlp->weights == MOE_WEIGHTS_W4 ? mlp->group : 128;
     a.logits_bf16 = gate->logits_type == MOE_LOGITS_BF16;
     unsigned *status = device_status_word();
     if (status == nullptr) return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    if (mlp->weights == MOE_WEIGHTS_BF16)
-        return launch_few<MOE_WEIGHTS_BF16>(d, a, st, x, logits, bias, w_up, up_scale, w_down, down_scale, topk_idx, topk_w,
-                                            out, workspace, status);
-    if (mlp->weights == MOE_WEIGHTS_FP8_B128)
-        return launch_few<MOE_WEIGHTS_FP8_B128>(d, a, st, x, logits, bias, w_up, up_scale, w_down, down_scale, topk_idx,
-                                                topk_w, out, workspace, status);
-    return launch_few<MOE_WEIGHTS_W4>(d, a, st, x, logits, bias, w_up, up_scale, w_down, down_scale, topk_idx, topk_w, out,
-                                      workspace, status);
+    const auto go = [&](auto kind) {
+        return launch_few<decltype(kind)::value>(d, a, st, x, logits, bias, w_up, up_scale, w_down, down_scale, topk_idx, topk_w,
+                                                 out, workspace, status);
+    };
+    if (mlp->weights == MOE_WEIGHTS_BF16) return go(std::integral_constant<int, kBf16>{});
+    if (mlp->weights == MOE_WEIGHTS_FP8_B128) return go(std::integral_constant<int, kFp8>{});
+    if (mlp->group == 32) return go(std::integral_constant<int, kW4G32>{});
+    if (mlp->group == 64) return go(std::integral_constant<int, kW4G64>{});
+    return go(std::integral_constant<int, kW4G128>{});
 }
