@@ -1,24 +1,24 @@
-// moe_few.cu -- a whole mixture-of-experts layer for up to 32 tokens, in two kernels.
+// moe_few.cu -- a whole mixture-of-experts layer for up to 32 tokens: the choice by one block,
+// and two kernels for the products.
 //
-//   up:    choice; h[t][j] = bf16(silu(x Wg_e^T) (x Wu_e^T)) of every pair (t, j), e its expert
-//   down:  choice; out[t] = bf16(sum_j w_j h[t][j] Wd_e^T)
+//   up:    h[t][j] = bf16(silu(x Wg_e^T) (x Wu_e^T)) of every pair (t, j), e its expert
+//   down:  out[t] = bf16(sum_j w_j h[t][j] Wd_e^T)
 //
 // With few tokens every chosen expert's weights are read once for a handful of rows: the
-// layer is bound by HBM, then by latency. So
+// layer is bound by HBM, then by what it costs to make operands of 8- and 4-bit weights. So
 //   - the weights are the 16-row operand of mma.m16n8k16 and up to 8 of an expert's tokens its 8
 //     columns (a tcgen05 tile of 128 rows would leave most SMs without work, and its tensor
 //     rate is not what is short). In the up kernel 8 of the rows are the gate's and 8 the up's,
 //     so that a lane holds both factors of its h;
-//   - they come by bulk copies into a ring in shared memory that one warp keeps full, over the
-//     end of one tile of rows into the next, and that leaves room for a second block on the SM:
-//     the down kernel's blocks start while the up kernel's are at work, choose for themselves
-//     (the choice costs a warp about a microsecond a token) and fill their rings before h is there;
-//   - every block forms the choice itself, from the logits: no launch and no wait between
-//     the router and the products.
+//   - every warp fetches its own weights, a 5-d TMA box of 16 rows x 256 bytes at a time, laid out
+//     so that a fragment's 64 bytes of each row are contiguous, into a ring of its own: no barrier
+//     between warps but where several share a tile of rows;
+//   - the down kernel's blocks start as the up kernel's end and fill their rings before h is there.
 #include <algorithm>
 #include <type_traits>
 
 #include "moe_gate.cuh"
+#include "moe_tc.cuh"
 #include "moe_w4.cuh"
 
 namespace moe {
@@ -28,17 +28,16 @@ constexpr int kFewTokens = 32;
 constexpr int kFewWarps = 8;
 constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewRows = 16;                       // matrix rows of a unit
-constexpr int kFewPiece = 256;                     // bytes of each row in a slot of a warp's ring
-constexpr int kFewPitch = kFewPiece + 64;          // rows 64 bytes apart in the banks: two rows' 64 bytes meet no twice
-constexpr int kFewSlot = kFewRows * kFewPitch;
-constexpr int kFewSlots = 2;                       // for each warp
+constexpr int kFewBlocks = 4;                      // blocks (64 bytes of each row) in a slot of a warp's ring
+constexpr int kFewSlot = kFewBlocks * kFewRows * 64;
+constexpr int kFewSlots = 3;                       // for each warp
 constexpr int kFewRing = kFewWarps * kFewSlots * kFewSlot;
 constexpr int kFewMaxPairs = kFewTokens * kMaxTopK + kFewTokens;       // with the shared expert's
 constexpr int kFewMaxLists = kFewTokens * kMaxTopK + 1;                // experts with rows
 
 struct FewArgs {
     GateArgs gate;
-    int H, I, E, T, k, shared, logits_bf16;
+    int H, I, E, T, k, shared;
 };
 
 // The kernels' kind of weights: moe_weights, the 4-bit ones by their group.
@@ -55,29 +54,6 @@ constexpr int kFewBlockInputs = WT == kBf16 ? 32 : WT == kFp8 ? 64 : 128;
 template <int WT>
 constexpr int kFewStepBlocks = WT == kBf16 ? 4 : WT == kFp8 ? 2 : 1;
 
-// The choice by whatever lane width the experts need. Not inlined: one copy of each serves every kernel here.
-template <typename T, int V>
-__device__ __noinline__ void few_gate_v(const void *logits, const float *bias, const GateArgs *a, int token, int lane,
-                                        int *e, float *w, bool *ok) {
-    int my_e;
-    float my_w;
-    bool my_ok;
-    warp_gate<T, V>(static_cast<const T *>(logits) + (size_t)token * a->E, bias, *a, lane, my_e, my_w, my_ok);
-    *e = my_e;
-    *w = my_w;
-    *ok = my_ok;
-}
-template <typename T>
-__device__ __forceinline__ void few_gate(const void *logits, const float *bias, const GateArgs *a, int token, int lane,
-                                         int *e, float *w, bool *ok) {
-    if (a->v <= 2) few_gate_v<T, 2>(logits, bias, a, token, lane, e, w, ok);
-    else if (a->v <= 4) few_gate_v<T, 4>(logits, bias, a, token, lane, e, w, ok);
-    else if (a->v <= 8) few_gate_v<T, 8>(logits, bias, a, token, lane, e, w, ok);
-    else if (a->v <= 16) few_gate_v<T, 16>(logits, bias, a, token, lane, e, w, ok);
-    else if (a->v <= 32) few_gate_v<T, 32>(logits, bias, a, token, lane, e, w, ok);
-    else few_gate_v<T, 64>(logits, bias, a, token, lane, e, w, ok);
-}
-
 // The experts that have rows, in the order of their first pair, the shared one last; list d holds rows off[d] .. off[d + 1] - 1.
 struct alignas(16) FewLists {
     uint16_t expert[kFewMaxLists + 1];
@@ -87,31 +63,31 @@ struct alignas(16) FewLists {
     float weight[kFewMaxPairs];
     int n;
 };
-// Needed only while the lists are made; lies where the ring is later.
-struct FewScratch {
-    uint32_t mask[kMaxExperts];                    // the expert's tokens
-    uint16_t list_of[kMaxExperts];
-    int16_t chosen[kFewTokens * kMaxTopK];         // expert of a pair, -1: no pair
-    float w[kFewTokens * kMaxTopK];
-};
-static_assert(sizeof(FewScratch) <= kFewRing, "the scratch lies within the ring");
+constexpr size_t kFewListsBytes = (sizeof(FewLists) + 255) / 256 * 256;
 
-__device__ __forceinline__ void few_lists(const FewArgs &a, const void *logits, const float *bias, FewLists &l,
-                                          FewScratch &s, int32_t *topk_idx, float *topk_w) {
+// The choice of all tokens, a warp to a token, and the lists: one block. The other kernels' blocks read the lists; the
+// down kernel's may do so before the up kernel has ended, which lets them start only once this one has.
+template <typename T, int V>
+__global__ void __launch_bounds__(V <= 16 ? 1024 : 256)
+few_choice_kernel(const __grid_constant__ FewArgs a, const T *__restrict__ logits, const float *__restrict__ bias,
+                  int32_t *__restrict__ topk_idx, float *__restrict__ topk_w, FewLists *__restrict__ l) {
+    __shared__ uint32_t mask[kMaxExperts];         // an expert's tokens
+    __shared__ uint16_t off_of[kMaxExperts];       // its first row
+    __shared__ int16_t chosen[kFewTokens * kMaxTopK];                  // expert of a pair, -1: no pair
+    __shared__ float weight[kFewTokens * kMaxTopK];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < a.E; e += kFewThreads) s.mask[e] = 0u;
-    for (int i = tid; i < (int)(sizeof(FewLists) / 16); i += kFewThreads) reinterpret_cast<uint4 *>(&l)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int e = tid; e < a.E; e += blockDim.x) mask[e] = 0u;
     __syncthreads();
-    for (int t = warp; t < a.T; t += kFewWarps) {
+    pdl_enter();
+    for (int t = warp; t < a.T; t += blockDim.x >> 5) {
         int e;
         float w;
         bool ok;
-        if (a.logits_bf16) few_gate<__nv_bfloat16>(logits, bias, &a.gate, t, lane, &e, &w, &ok);
-        else few_gate<float>(logits, bias, &a.gate, t, lane, &e, &w, &ok);
+        warp_gate<T, V>(logits + (size_t)t * a.E, bias, a.gate, lane, e, w, ok);
         if (lane < a.k) {
-            s.chosen[t * a.k + lane] = (int16_t)(ok ? e : -1);
-            s.w[t * a.k + lane] = w;
-            if (ok) atomicOr(&s.mask[e], 1u << t);
+            chosen[t * a.k + lane] = (int16_t)(ok ? e : -1);
+            weight[t * a.k + lane] = w;
+            if (ok) atomicOr(&mask[e], 1u << t);
             if (topk_idx) topk_idx[t * a.k + lane] = e;
             if (topk_w) topk_w[t * a.k + lane] = w;
         }
@@ -121,8 +97,8 @@ __device__ __forceinline__ void few_lists(const FewArgs &a, const void *logits, 
         int n = 0, rows = 0;
         for (int i0 = 0; i0 < a.T * a.k; i0 += 32) {
             const int i = i0 + lane;
-            const int e = i < a.T * a.k ? s.chosen[i] : -1;
-            const uint32_t m = e >= 0 ? s.mask[e] : 0u;
+            const int e = i < a.T * a.k ? chosen[i] : -1;
+            const uint32_t m = e >= 0 ? mask[e] : 0u;
             const bool first = e >= 0 && (m & ((1u << (i / a.k)) - 1u)) == 0u;
             const unsigned all = __ballot_sync(kFull, first);
             int incl = first ? __popc(m) : 0;
@@ -134,43 +110,41 @@ __device__ __forceinline__ void few_lists(const FewArgs &a, const void *logits, 
             }
             if (first) {
                 const int d = n + __popc(all & ((1u << lane) - 1u));
-                l.expert[d] = (uint16_t)e;
-                l.off[d] = (uint16_t)(rows + incl - own);
-                s.list_of[e] = (uint16_t)d;
+                l->expert[d] = (uint16_t)e;
+                l->off[d] = (uint16_t)(rows + incl - own);
+                off_of[e] = (uint16_t)(rows + incl - own);
             }
             n += __popc(all);
             rows += __shfl_sync(kFull, incl, 31);
         }
         if (a.shared) {
             if (lane < a.T) {
-                l.pair[rows + lane] = (uint16_t)(lane * (a.k + 1) + a.k);
-                l.token[rows + lane] = (uint8_t)lane;
-                l.weight[rows + lane] = 1.0f;
+                l->pair[rows + lane] = (uint16_t)(lane * (a.k + 1) + a.k);
+                l->token[rows + lane] = (uint8_t)lane;
+                l->weight[rows + lane] = 1.0f;
             }
             if (lane == 0) {
-                l.expert[n] = (uint16_t)a.E;
-                l.off[n] = (uint16_t)rows;
+                l->expert[n] = (uint16_t)a.E;
+                l->off[n] = (uint16_t)rows;
             }
             ++n;
             rows += a.T;
         }
         if (lane == 0) {
-            l.off[n] = (uint16_t)rows;
-            l.n = n;
+            l->off[n] = (uint16_t)rows;
+            l->n = n;
         }
     }
     __syncthreads();
-    for (int i = tid; i < a.T * a.k; i += kFewThreads) {
-        const int e = s.chosen[i];
+    for (int i = tid; i < a.T * a.k; i += blockDim.x) {
+        const int e = chosen[i];
         if (e < 0) continue;
         const int t = i / a.k;
-        const int r = l.off[s.list_of[e]] + __popc(s.mask[e] & ((1u << t) - 1u));
-        l.pair[r] = (uint16_t)(t * (a.k + a.shared) + (i - t * a.k));
-        l.token[r] = (uint8_t)t;
-        l.weight[r] = s.w[i];
+        const int r = off_of[e] + __popc(mask[e] & ((1u << t) - 1u));
+        l->pair[r] = (uint16_t)(t * (a.k + a.shared) + (i - t * a.k));
+        l->token[r] = (uint8_t)t;
+        l->weight[r] = weight[i];
     }
-    fence_proxy_async_smem();                      // the ring's copies come over the scratch
-    __syncthreads();
 }
 
 // The pieces of one warp's work, in order. A unit is 16 matrix rows: up, 8 of the gate's and 8 of the up's of a list's
@@ -216,6 +190,15 @@ struct FewOperand {
     uint2 sa, sb;
 };
 
+// A box of the weights: x within a block of 64 bytes (0), row, gate or up, block, expert.
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int row, int block, int expert) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::
+            "r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(row), "r"(block), "r"(expert)
+        : "memory");
+}
+
 // Loads whose addresses are only good where the program order comes to them: volatile, so that none is made earlier.
 __device__ __forceinline__ uint32_t ld_u16(const void *p) {
     uint16_t r;
@@ -252,15 +235,20 @@ __device__ __forceinline__ void add_scaled(float (&c)[4], const float (&part)[4]
     c[3] = fmaf(part[3], sb, c[3]);
 }
 
-// A step's products: the fragment rows' blocks at pa (rows g) and pb (rows g + 8) with the inputs of o.
+__device__ __forceinline__ uint4 ld_l2_v4(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// A step's products: the blocks at pa (rows g; rows g + 8 are 512 bytes on) with the inputs of o.
 template <int WT>
-__device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o, const uint8_t *pa, const uint8_t *pb,
-                                         int blocks) {
+__device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o, const uint8_t *pa, int blocks) {
     if constexpr (WT == kBf16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= blocks) break;
-            const uint4 va = *reinterpret_cast<const uint4 *>(pa + 64 * i), vb = *reinterpret_cast<const uint4 *>(pb + 64 * i);
+            const uint4 va = *reinterpret_cast<const uint4 *>(pa + 1024 * i), vb = *reinterpret_cast<const uint4 *>(pa + 1024 * i + 512);
             mma16816<false>(c, va.x, vb.x, va.y, vb.y, o.x[i].x, o.x[i].y);
             mma16816<false>(c, va.z, vb.z, va.w, vb.w, o.x[i].z, o.x[i].w);
         }
@@ -268,7 +256,7 @@ __device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o,
         float part[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint4 va = *reinterpret_cast<const uint4 *>(pa + 64 * i), vb = *reinterpret_cast<const uint4 *>(pb + 64 * i);
+            const uint4 va = *reinterpret_cast<const uint4 *>(pa + 1024 * i), vb = *reinterpret_cast<const uint4 *>(pa + 1024 * i + 512);
             const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -281,7 +269,7 @@ __device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o,
         }
         add_scaled(c, part, __uint_as_float(o.sa.x), __uint_as_float(o.sb.x));
     } else {
-        const uint4 va = *reinterpret_cast<const uint4 *>(pa), vb = *reinterpret_cast<const uint4 *>(pb);
+        const uint4 va = *reinterpret_cast<const uint4 *>(pa), vb = *reinterpret_cast<const uint4 *>(pa + 512);
         const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
         constexpr int kPer = kFewGroup<WT> / 32;                       // blocks of 32 inputs to a group
         float part[4];
@@ -304,17 +292,16 @@ __device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o,
 
 template <int WT, bool DOWN>
 __global__ void __launch_bounds__(kFewThreads, 2)
-few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const void *__restrict__ logits,
-           const float *__restrict__ bias, const uint8_t *__restrict__ w, const void *__restrict__ w_scale, uint16_t *h,
-           int32_t *__restrict__ topk_idx, float *__restrict__ topk_w, uint16_t *__restrict__ out, unsigned *status) {
+few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const FewLists *made, const uint16_t *x,
+           const void *__restrict__ w_scale, uint16_t *h, uint16_t *__restrict__ out, unsigned *status) {
     extern __shared__ __align__(128) uint8_t few_smem[];
     __shared__ __align__(8) uint64_t full[kFewWarps][kFewSlots];
     __shared__ FewLists lists;
     __shared__ float4 red[DOWN ? 1 : kFewWarps][32];
     // down: each warp's share of its unit's outputs, [warp][token][16]
     float *acc_out = reinterpret_cast<float *>(few_smem + kFewRing);
-    constexpr int kBlockIn = kFewBlockInputs<WT>, kPieceIn = kBlockIn * (kFewPiece / 64);
-    constexpr int kGroup = kFewGroup<WT>, kStep = kFewStepBlocks<WT>, kSteps = kFewPiece / 64 / kStep;
+    constexpr int kBlockIn = kFewBlockInputs<WT>, kPieceIn = kBlockIn * kFewBlocks;
+    constexpr int kGroup = kFewGroup<WT>, kStep = kFewStepBlocks<WT>, kSteps = kFewBlocks / kStep;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int K = DOWN ? a.I : a.H, M = DOWN ? a.H : 2 * a.I;
     if (lane < kFewSlots) {
@@ -325,9 +312,10 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
         pdl_wait();
         pdl_launch_dependents();
     }
-    // The up kernel lets this one start once it has itself waited for all before it: the inputs of the call are there.
-    few_lists(a, logits, bias, lists, *reinterpret_cast<FewScratch *>(few_smem),
-              DOWN || blockIdx.x != 0 ? nullptr : topk_idx, DOWN || blockIdx.x != 0 ? nullptr : topk_w);
+    // the up kernel lets the down kernel start once the choice is made
+    for (int i = tid; i < (int)(sizeof(FewLists) / 16); i += kFewThreads)
+        reinterpret_cast<uint4 *>(&lists)[i] = ld_l2_v4(reinterpret_cast<const uint4 *>(made) + i);
+    __syncthreads();
 
     FewPlan plan;
     plan.lists = lists.n;
@@ -338,21 +326,22 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
     plan.team = team;
     plan.first = warp & (team - 1);
     plan.stride = gridDim.x * (kFewWarps / team);
-    const unsigned row_bytes = (unsigned)(K / kBlockIn) * 64u, scale_row = (unsigned)(K / kGroup) * 2u;
+    const unsigned scale_row = (unsigned)(K / kGroup) * 2u;
     // from the unit's row 0 to its row 8
     const unsigned row8 = DOWN ? 8u : (unsigned)a.I;
 
-    // Fetching: lane r < 16 the unit's row r; with 4-bit weights lane 16 + r that row's scales, as far as L2.
+    // Fetching: lane 0 asks for the box; with 4-bit weights lane r < 16 for row r's scales, as far as L2.
     FewWalk<DOWN> fw;
     fw.unit = blockIdx.x + gridDim.x * (warp / team);
-    const uint8_t *from = w;
-    const auto aim = [&]() {                       // `from` for the walk's list and place
+    int expert = 0, row0 = 0;
+    const uint8_t *from = static_cast<const uint8_t *>(w_scale);
+    const auto aim = [&]() {                       // for the walk's list and place
         if (fw.unit >= plan.units || fw.q >= plan.all) return;
-        const size_t row = (size_t)lists.expert[fw.d] * M + fw.row(plan) * (DOWN ? 16 : 8) + (lane & 7) + (lane & 8 ? row8 : 0u);
-        if (kIsW4<WT> && lane >= 16)
-            from = static_cast<const uint8_t *>(w_scale) + row * scale_row + (size_t)fw.c * (kPieceIn * 2 / kGroup);
-        else
-            from = w + row * row_bytes + (size_t)fw.c * kFewPiece;
+        expert = lists.expert[fw.d];
+        row0 = fw.row(plan) * (DOWN ? 16 : 8);
+        if (kIsW4<WT>)
+            from = static_cast<const uint8_t *>(w_scale) +
+                   ((size_t)expert * M + row0 + (lane & 7) + (lane & 8 ? row8 : 0u)) * scale_row + (size_t)fw.c * (kPieceIn * 2 / kGroup);
     };
     fw.start(plan);
     aim();
@@ -360,13 +349,11 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
     const auto fetch = [&]() {
         if (fw.unit >= plan.units || fw.q >= plan.all) return;
         const unsigned s = fetched % kFewSlots;
-        const unsigned bytes = min((unsigned)kFewPiece, row_bytes - (unsigned)fw.c * kFewPiece);
-        if (lane == 0) mbar_expect_tx(&full[warp][s], kFewRows * bytes);
-        __syncwarp();
-        if (lane < 16)
-            bulk_g2s(few_smem + (warp * kFewSlots + s) * kFewSlot + lane * kFewPitch, from, bytes, &full[warp][s]);
-        else if (kIsW4<WT>)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
+        if (lane == 0) {
+            mbar_expect_tx(&full[warp][s], kFewSlot);              // blocks past the row's end count, as zeros
+            tma_load_5d(few_smem + (warp * kFewSlots + s) * kFewSlot, &map, &full[warp][s], row0, fw.c * kFewBlocks, expert);
+        }
+        if (kIsW4<WT> && lane < 16) asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
         ++fetched;
         fw.q += plan.team;
         fw.c += plan.team;
@@ -377,7 +364,7 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
         } else if (DOWN && fw.wrap(plan)) {
             aim();
         } else {
-            from += plan.team * (kIsW4<WT> && lane >= 16 ? kPieceIn * 2 / kGroup : kFewPiece);
+            from += plan.team * (kPieceIn * 2 / kGroup);
         }
     };
 #pragma unroll
@@ -469,7 +456,7 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
                     to.sb = ld_v2(psb + 8 * step);
                 }
             };
-            const int blocks = min(kFewPiece / 64, (K - k0) / kBlockIn);
+            const int blocks = min(kFewBlocks, (K - k0) / kBlockIn);
             FewOperand<WT> o;
             load(o, px, 0, false);
             const unsigned s = n % kFewSlots;
@@ -478,13 +465,13 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
                 lost = n;
                 if (lane == 0) atomicOr(status, kStatusWaitGaveUp);
             }
-            const uint8_t *pa = few_smem + (warp * kFewSlots + s) * kFewSlot + g * kFewPitch + 16 * t, *pb = pa + 8 * kFewPitch;
-            if (rows <= 8 && blocks == kFewPiece / 64) {               // most pieces: steps and offsets known
+            const uint8_t *pa = few_smem + (warp * kFewSlots + s) * kFewSlot + 16 * lane;          // row g, 16 t bytes in
+            if (rows <= 8 && blocks == kFewBlocks) {               // most pieces: steps and offsets known
 #pragma unroll
                 for (int step = 0; step < kSteps; ++step) {
                     FewOperand<WT> next;
                     if (step + 1 < kSteps) load(next, px, step + 1, true);
-                    few_step<WT>(acc[0], o, pa + 64 * kStep * step, pb + 64 * kStep * step, kStep);
+                    few_step<WT>(acc[0], o, pa + 1024 * kStep * step, kStep);
                     if (step + 1 < kSteps) o = next;
                 }
             } else {
@@ -494,7 +481,7 @@ few_kernel(const __grid_constant__ FewArgs a, int team, const uint16_t *x, const
                     if (8 * nt >= rows) break;     // warp-uniform
 #pragma unroll 1
                     for (int step = 0; step * kStep < blocks; ++step) {
-                        few_step<WT>(acc[nt], o, pa + 64 * kStep * step, pb + 64 * kStep * step, blocks - step * kStep);
+                        few_step<WT>(acc[nt], o, pa + 1024 * kStep * step, blocks - step * kStep);
                         if ((step + 1) * kStep < blocks) {
                             load(o, p, step + 1, false);
                         } else if (8 * (nt + 1) < rows) {
@@ -596,32 +583,63 @@ int few_team(long long units) {
     while (team < kFewWarps && units * team * 2 <= 2LL * 152 * kFewWarps) team *= 2;
     return team;
 }
-int few_grid(long long units, int max_blocks) {
-    const long long blocks = (units * few_team(units) + kFewWarps - 1) / kFewWarps;
-    return persistent_grid(std::min(blocks, units), 2 * sm_count(), max_blocks);
+int few_grid(long long units, int max_blocks) { return persistent_grid(units, 2 * sm_count(), max_blocks); }
+
+// Matrices [S][parts][rows][row_bytes] in boxes of `box_rows` rows of each part x kFewBlocks blocks of 64 bytes.
+bool encode_few(CUtensorMap *map, const void *base, uint64_t rows, uint64_t parts, uint64_t row_bytes, uint64_t S,
+                uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[5] = {64, rows, parts, row_bytes / 64, S};
+    const cuuint64_t strides[4] = {row_bytes, rows * row_bytes, 64, parts * rows * row_bytes};
+    const cuuint32_t box[5] = {64, box_rows, (cuuint32_t)parts, kFewBlocks, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int V>
+int launch_choice(const FewArgs &a, cudaStream_t st, const void *logits, const float *bias, int32_t *idx, float *w,
+                  FewLists *lists) {
+    const int most = V <= 16 ? 32 : 8;             // warps; at least 4 for the clearing and the rows
+    const int warps = std::min(most, std::max(a.T, 4));
+    return launch_pdl(few_choice_kernel<T, V>, 1, warps * 32, st, a, static_cast<const T *>(logits), bias, idx, w, lists) ==
+                   cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+template <typename T, typename... A>
+int launch_choice_v(const FewArgs &a, A... args) {
+    if (a.gate.v <= 2) return launch_choice<T, 2>(a, args...);
+    if (a.gate.v <= 4) return launch_choice<T, 4>(a, args...);
+    if (a.gate.v <= 8) return launch_choice<T, 8>(a, args...);
+    if (a.gate.v <= 16) return launch_choice<T, 16>(a, args...);
+    if (a.gate.v <= 32) return launch_choice<T, 32>(a, args...);
+    return launch_choice<T, 64>(a, args...);
 }
 
 template <int WT>
-int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, const void *logits, const float *bias,
-               const void *w_up, const void *up_scale, const void *w_down, const void *down_scale, int32_t *idx, float *w,
-               void *out, void *h, unsigned *status) {
+int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, const void *w_up, const void *up_scale,
+               const void *w_down, const void *down_scale, void *out, const FewLists *lists, void *h, unsigned *status) {
     static PerContext<int> up_done, down_done;
-    const size_t ring = kFewRing, most = ring + kFewWarps * kFewTokens * 16 * sizeof(float);
-    if (!set_smem_once(up_done, few_kernel<WT, false>, (int)ring) || !set_smem_once(down_done, few_kernel<WT, true>, (int)most))
+    const size_t most = kFewRing + kFewWarps * kFewTokens * 16 * sizeof(float);
+    if (!set_smem_once(up_done, few_kernel<WT, false>, kFewRing) || !set_smem_once(down_done, few_kernel<WT, true>, (int)most))
         return MOE_ERR_CUDA;
-    const long long lists = std::min<long long>((long long)d.T * d.k, d.E) + a.shared;
-    long long units = lists * (a.I / 8);
-    int grid = few_grid(units, d.max_blocks), team = few_team(units);
-    if (launch_pdl_smem(few_kernel<WT, false>, grid, kFewThreads, ring, st, a, team, static_cast<const uint16_t *>(x), logits,
-                        bias, static_cast<const uint8_t *>(w_up), up_scale, static_cast<uint16_t *>(h), idx, w,
+    CUtensorMap up, down;
+    const uint64_t S = a.E + a.shared, block = kFewBlockInputs<WT>;
+    if (!encode_few(&up, w_up, a.I, 2, a.H / block * 64, S, 8) || !encode_few(&down, w_down, a.H, 1, a.I / block * 64, S, 16))
+        return MOE_ERR_CUDA;
+    long long units = (std::min<long long>((long long)d.T * d.k, d.E) + a.shared) * (a.I / 8);
+    if (launch_pdl_smem(few_kernel<WT, false>, few_grid(units, d.max_blocks), kFewThreads, kFewRing, st, up, a, few_team(units),
+                        lists, static_cast<const uint16_t *>(x), up_scale, static_cast<uint16_t *>(h),
                         static_cast<uint16_t *>(out), status) != cudaSuccess)
         return MOE_ERR_CUDA;
     units = d.H / 16;
-    grid = few_grid(units, d.max_blocks);
-    team = few_team(units);
-    if (launch_pdl_smem(few_kernel<WT, true>, grid, kFewThreads, ring + (size_t)kFewWarps * d.T * 16 * sizeof(float), st, a,
-                        team, static_cast<const uint16_t *>(x), logits, bias, static_cast<const uint8_t *>(w_down), down_scale,
-                        static_cast<uint16_t *>(h), idx, w, static_cast<uint16_t *>(out), status) != cudaSuccess)
+    if (launch_pdl_smem(few_kernel<WT, true>, few_grid(units, d.max_blocks), kFewThreads,
+                        kFewRing + (size_t)kFewWarps * d.T * 16 * sizeof(float), st, down, a, few_team(units), lists,
+                        static_cast<const uint16_t *>(x), down_scale, static_cast<uint16_t *>(h),
+                        static_cast<uint16_t *>(out), status) != cudaSuccess)
         return MOE_ERR_CUDA;
     return MOE_OK;
 }
@@ -633,8 +651,8 @@ extern "C" size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_
     using namespace moe;
     Dims d;
     if (check_problem(p, &d) != MOE_OK || check_mlp(mlp) != MOE_OK || check_few(d, mlp) != MOE_OK) return 0;
-    const size_t n = (size_t)d.T * (d.k + mlp->shared) * mlp->inner * 2;
-    return n < 256 ? 256 : (n + 255) & ~(size_t)255;
+    const size_t n = kFewListsBytes + (size_t)d.T * (d.k + mlp->shared) * mlp->inner * 2;
+    return (n + 255) & ~(size_t)255;
 }
 
 extern "C" int moe_layer_few(const moe_problem *p, const moe_gate *gate, const moe_mlp *mlp, const void *x,
@@ -665,13 +683,16 @@ extern "C" int moe_layer_few(const moe_problem *p, const moe_gate *gate, const m
     a.T = d.T;
     a.k = d.k;
     a.shared = mlp->shared;
-    a.logits_bf16 = gate->logits_type == MOE_LOGITS_BF16;
     unsigned *status = device_status_word();
     if (status == nullptr) return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
+    FewLists *lists = static_cast<FewLists *>(workspace);
+    void *h = static_cast<uint8_t *>(workspace) + kFewListsBytes;
+    rc = gate->logits_type == MOE_LOGITS_BF16 ? launch_choice_v<__nv_bfloat16>(a, st, logits, bias, topk_idx, topk_w, lists)
+                                              : launch_choice_v<float>(a, st, logits, bias, topk_idx, topk_w, lists);
+    if (rc != MOE_OK) return rc;
     const auto go = [&](auto kind) {
-        return launch_few<decltype(kind)::value>(d, a, st, x, logits, bias, w_up, up_scale, w_down, down_scale, topk_idx, topk_w,
-                                                 out, workspace, status);
+        return launch_few<decltype(kind)::value>(d, a, st, x, w_up, up_scale, w_down, down_scale, out, lists, h, status);
     };
     if (mlp->weights == MOE_WEIGHTS_BF16) return go(std::integral_constant<int, kBf16>{});
     if (mlp->weights == MOE_WEIGHTS_FP8_B128) return go(std::integral_constant<int, kFp8>{});
