@@ -13,7 +13,14 @@
 //   - every warp fetches its own weights, a 5-d TMA box of 16 rows x 256 bytes at a time, laid out
 //     so that a fragment's 64 bytes of each row are contiguous, into a ring of its own: no barrier
 //     between warps but where several share a tile of rows;
-//   - the down kernel's blocks start as the up kernel's end and fill their rings before h is there.
+//   - the down kernel's blocks start as the up kernel's end and fill their rings before h is there;
+//   - weights of 8 and 4 bits are made fp16 operands, which costs least: an e4m3 pair one conversion (a bf16
+//     pair takes five instructions), a 4-bit pair one logic operation, which leaves 1024 + q, or 1024 + 16 q where
+//     the code stands 4 bits higher. The inputs of such weights are fp16 too, each row behind a power of two that
+//     brings its largest value to 2^14 .. 2^15: a bf16 x keeps all its bits there but for values below 2^-25 of
+//     the row's largest, which keep an error of 2^-36 of it; h, kept in fp32 meanwhile, is rounded to its 11 bits.
+//     4-bit weights: inputs whose code stands higher are divided by 16, and what 1024 (or 64) and the codes' middle,
+//     8, add to a group's sum is taken off it in fp32: sum x (1024 + q) - 1032 sum x.
 #include <algorithm>
 #include <type_traits>
 
@@ -46,6 +53,8 @@ template <int WT>
 constexpr bool kIsW4 = WT >= kW4G32;
 template <int WT>
 constexpr int kFewGroup = WT == kW4G32 ? 32 : WT == kW4G64 ? 64 : 128;
+template <int WT>
+constexpr bool kFewHalf = WT != kBf16;             // inputs as fp16
 
 // A block of a row: the 64 bytes that the four lanes of a fragment's row read at once.
 template <int WT>
@@ -63,14 +72,122 @@ struct alignas(16) FewLists {
     float weight[kFewMaxPairs];
     int n;
 };
-constexpr size_t kFewListsBytes = (sizeof(FewLists) + 255) / 256 * 256;
 
-// The choice of all tokens, a warp to a token, and the lists: one block. The other kernels' blocks read the lists; the
+// Loads whose addresses are only good where the program order comes to them: volatile, so that none is made earlier.
+__device__ __forceinline__ uint32_t ld_u16(const void *p) {
+    uint16_t r;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_u32(const void *p) {
+    uint32_t r;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint2 ld_v2(const void *p) {
+    uint2 r;
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint4 ld_v4(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+__device__ __forceinline__ uint4 ld_l2_v4(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// Inputs as fp16: the rows, their scales, and with 4-bit weights what each group's sum starts from.
+struct FewInputs {
+    uint16_t *x;
+    float *scale, *less;
+};
+
+// Eight values of a row.
+__device__ __forceinline__ void load8(const uint16_t *p, float (&f)[8]) {
+    const uint4 v = ld_v4(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
+    const uint4 u = ld_v4(p), v = ld_v4(p + 4);
+    const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+}
+// A row of n (a multiple of 128) values as fp16 behind a power of two that brings its largest to 2^14 .. 2^15, and that
+// power's inverse; group 32, 64 or 128: as the inputs of 4-bit weights. By a block, all of whose threads come here; rows of up
+// to eight values a thread are read once.
+template <typename T>
+__device__ __forceinline__ void row_to_half(const T *row, int n, int group, const FewInputs &to, size_t at) {
+    __shared__ float most[32];
+    const int nt = 8 * blockDim.x, first = 8 * threadIdx.x;
+    float f[8], m = 0.0f;
+    for (int i = first; i < n; i += nt) {
+        load8(row + i, f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = fmaxf(m, fabsf(f[q]));         // NaN stays out
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int i = 0; i < (int)blockDim.x >> 5; ++i) m = fmaxf(m, most[i]);
+    // the power of two from the exponent's bits; a row with infinities stays as it is
+    const int e = (int)(__float_as_uint(m) >> 23) - 127;
+    const int s = m == 0.0f || e == 128 ? 0 : max(e - 14, -112);
+    const float by = __uint_as_float((uint32_t)(127 - s) << 23);
+    for (int i0 = 0; i0 < n; i0 += nt) {
+        const int i = i0 + first;
+        float less = 0.0f;
+        if (i < n) {
+            if (n > nt) load8(row + i, f);
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float b = group != 0 && (q & 1) ? by * 0.0625f : by;
+                const __half2 v = __floats2half2_rn(__fmul_rn(f[2 * q], b), __fmul_rn(f[2 * q + 1], b));
+                w[q] = *reinterpret_cast<const uint32_t *>(&v);
+                // codes behind 1024 + q (1032 at the middle), or 1024 + 16 q (1152)
+                const float2 r = __half22float2(v);
+                less -= (q & 1 ? 1152.0f : 1032.0f) * (r.x + r.y);
+            }
+            st_v4(to.x + at * n + i, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+        if (group != 0) {                          // 4, 8 or 16 lanes to a group, all of them on the same side of n
+            for (int o = 1; o < group / 8; o <<= 1) less += __shfl_xor_sync(kFull, less, o);
+            if (i < n && i % group == 0) to.less[at * (n / group) + i / group] = less;
+        }
+    }
+    if (threadIdx.x == 0) to.scale[at] = __uint_as_float((uint32_t)(127 + s) << 23);
+}
+
+// h as fp16, a block to a pair. Lets the down kernel start at once.
+__global__ void __launch_bounds__(256)
+few_half_kernel(const FewLists *__restrict__ l, const float *h, int I, int group, FewInputs to) {
+    pdl_launch_dependents();
+    pdl_wait();
+    if ((int)blockIdx.x >= l->off[l->n]) return;
+    const int pair = l->pair[blockIdx.x];
+    row_to_half(h + (size_t)pair * I, I, group, to, pair);
+}
+
+// The choice of all tokens, a warp to a token, and the lists: block 0. With weights of 8 or 4 bits the other blocks, one
+// to a token, make its x fp16. The other kernels' blocks read the lists; the
 // down kernel's may do so before the up kernel has ended, which lets them start only once this one has.
 template <typename T, int V>
 __global__ void __launch_bounds__(V <= 16 ? 1024 : 256)
 few_choice_kernel(const __grid_constant__ FewArgs a, const T *__restrict__ logits, const float *__restrict__ bias,
-                  int32_t *__restrict__ topk_idx, float *__restrict__ topk_w, FewLists *__restrict__ l) {
+                  int32_t *__restrict__ topk_idx, float *__restrict__ topk_w, FewLists *__restrict__ l,
+                  unsigned *__restrict__ there, const uint16_t *x, int group, FewInputs half) {
     __shared__ uint32_t mask[kMaxExperts];         // an expert's tokens
     __shared__ uint16_t off_of[kMaxExperts];       // its first row
     __shared__ int16_t chosen[kFewTokens * kMaxTopK];                  // expert of a pair, -1: no pair
@@ -79,6 +196,12 @@ few_choice_kernel(const __grid_constant__ FewArgs a, const T *__restrict__ logit
     for (int e = tid; e < a.E; e += blockDim.x) mask[e] = 0u;
     __syncthreads();
     pdl_enter();
+    if (blockIdx.x > 0) {
+        const int t = blockIdx.x - 1;
+        row_to_half(x + (size_t)t * a.H, a.H, group, half, t);
+        return;
+    }
+    for (int i = tid; i < a.H / 16; i += blockDim.x) there[i] = 0u;
     for (int t = warp; t < a.T; t += blockDim.x >> 5) {
         int e;
         float w;
@@ -149,15 +272,15 @@ few_choice_kernel(const __grid_constant__ FewArgs a, const T *__restrict__ logit
 
 // The pieces of one warp's work, in order. A unit is 16 matrix rows: up, 8 of the gate's and 8 of the up's of a list's
 // expert; down, 16 of each list's expert in turn. A unit belongs to a team of `team` warps, which take its pieces in
-// turn.
+// turn; down, where the units are few, to 2^split teams of different blocks, and counts as so many units.
 struct FewPlan {
-    int units, lists, pieces, per, all, first, team, stride;
+    int units, lists, pieces, per, all, first, team, step, split, stride;
 };
 template <bool DOWN>
 struct FewWalk {
     int unit, q, d, c;                             // q: piece of the unit; d: its list, c: its place in the rows
     __device__ __forceinline__ void start(const FewPlan &p) {
-        q = c = p.first;
+        q = c = p.first + (DOWN ? p.team * (unit & ((1 << p.split) - 1)) : 0);
         d = DOWN ? 0 : unit / p.per;
         if (DOWN) wrap(p);
     }
@@ -169,25 +292,16 @@ struct FewWalk {
         } while (c >= p.pieces);
         return true;
     }
-    __device__ __forceinline__ int row(const FewPlan &p) const { return DOWN ? unit : unit - d * p.per; }
+    __device__ __forceinline__ int row(const FewPlan &p) const { return DOWN ? unit >> p.split : unit - d * p.per; }
 };
 
-// Two bytes of e4m3 at a time -> two bf16: a code's exponent and mantissa bits under a bf16's are its value times
-// 2^-120, exactly, subnormals among them.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w, uint32_t pick) {
-    const uint32_t b = __byte_perm(w, 0u, pick);   // each code in the upper byte of its half
-    const uint32_t v = (b & 0x80008000u) | (b >> 4 & 0x07F007F0u);
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7B807B80u));
-    return r;
-}
-
-// What a step needs from global memory besides the weights: 8 columns' inputs, and the scales of the fragment's rows g
-// and g + 8.
+// What a step needs from global memory besides the weights: 8 columns' inputs, the scales of the fragment's rows g
+// and g + 8, and with 4-bit weights what each group's sum starts from in the lane's columns 2 t and 2 t + 1.
 template <int WT>
 struct FewOperand {
     uint4 x[4];
     uint2 sa, sb;
+    float less[kIsW4<WT> ? 128 / kFewGroup<WT> : 1][2];
 };
 
 // A box of the weights: x within a block of 64 bytes (0), row, gate or up, block, expert.
@@ -199,34 +313,13 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
-// Loads whose addresses are only good where the program order comes to them: volatile, so that none is made earlier.
-__device__ __forceinline__ uint32_t ld_u16(const void *p) {
-    uint16_t r;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint32_t ld_u32(const void *p) {
-    uint32_t r;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint2 ld_v2(const void *p) {
-    uint2 r;
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint4 ld_v4(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-    return r;
-}
-
-// The first product of a sum: d = A B.
-__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                               uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+// A packed word's 8 codes as four pairs of fp16, pair (2i, 2i + 1) to r[i]: 1024 + q, and for odd i 1024 + 16 q.
+__device__ __forceinline__ void w4_raw_pairs(uint32_t word, uint32_t (&r)[4]) {
+    const uint32_t up = word >> 8;
+    r[0] = (word & 0x000F000Fu) | 0x64006400u;
+    r[1] = (word & 0x00F000F0u) | 0x64006400u;
+    r[2] = (up & 0x000F000Fu) | 0x64006400u;
+    r[3] = (up & 0x00F000F0u) | 0x64006400u;
 }
 __device__ __forceinline__ void add_scaled(float (&c)[4], const float (&part)[4], float sa, float sb) {
     c[0] = fmaf(part[0], sa, c[0]);
@@ -235,73 +328,94 @@ __device__ __forceinline__ void add_scaled(float (&c)[4], const float (&part)[4]
     c[3] = fmaf(part[3], sb, c[3]);
 }
 
-__device__ __forceinline__ uint4 ld_l2_v4(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-    return r;
-}
-
-// A step's products: the blocks at pa (rows g; rows g + 8 are 512 bytes on) with the inputs of o.
-template <int WT>
-__device__ __forceinline__ void few_step(float (&c)[4], const FewOperand<WT> &o, const uint8_t *pa, int blocks) {
+// A step's products: the blocks at pa (rows g; rows g + 8 are 512 bytes on) with the inputs of NT times 8 columns, the
+// weights made operands once for all.
+template <int WT, int NT>
+__device__ __forceinline__ void few_step(float (*c)[4], const FewOperand<WT> (&o)[NT], const uint8_t *pa, int blocks) {
     if constexpr (WT == kBf16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i >= blocks) break;
             const uint4 va = *reinterpret_cast<const uint4 *>(pa + 1024 * i), vb = *reinterpret_cast<const uint4 *>(pa + 1024 * i + 512);
-            mma16816<false>(c, va.x, vb.x, va.y, vb.y, o.x[i].x, o.x[i].y);
-            mma16816<false>(c, va.z, vb.z, va.w, vb.w, o.x[i].z, o.x[i].w);
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+                mma16816<false>(c[m], va.x, vb.x, va.y, vb.y, o[m].x[i].x, o[m].x[i].y);
+                mma16816<false>(c[m], va.z, vb.z, va.w, vb.w, o[m].x[i].z, o[m].x[i].w);
+            }
         }
     } else if constexpr (WT == kFp8) {
-        float part[4];
+        float part[NT][4];
+#pragma unroll
+        for (int m = 0; m < NT; ++m) part[m][0] = part[m][1] = part[m][2] = part[m][3] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint4 va = *reinterpret_cast<const uint4 *>(pa + 1024 * i), vb = *reinterpret_cast<const uint4 *>(pa + 1024 * i + 512);
             const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 b = o.x[2 * i + q / 2];
-                const uint32_t a0 = e4m3x2_to_bf16x2(wa[q], 0x1404), a1 = e4m3x2_to_bf16x2(wb[q], 0x1404);
-                const uint32_t a2 = e4m3x2_to_bf16x2(wa[q], 0x3424), a3 = e4m3x2_to_bf16x2(wb[q], 0x3424);
-                if (i == 0 && q == 0) mma16816_first(part, a0, a1, a2, a3, b.x, b.y);
-                else mma16816<false>(part, a0, a1, a2, a3, q % 2 ? b.z : b.x, q % 2 ? b.w : b.y);
+                const uint32_t a0 = e4m3x2_to_f16x2(wa[q]), a1 = e4m3x2_to_f16x2(wb[q]);
+                const uint32_t a2 = e4m3x2_to_f16x2(wa[q] >> 16), a3 = e4m3x2_to_f16x2(wb[q] >> 16);
+#pragma unroll
+                for (int m = 0; m < NT; ++m) {
+                    const uint4 b = o[m].x[2 * i + q / 2];
+                    mma16816<true>(part[m], a0, a1, a2, a3, q % 2 ? b.z : b.x, q % 2 ? b.w : b.y);
+                }
             }
         }
-        add_scaled(c, part, __uint_as_float(o.sa.x), __uint_as_float(o.sb.x));
+#pragma unroll
+        for (int m = 0; m < NT; ++m) add_scaled(c[m], part[m], __uint_as_float(o[0].sa.x), __uint_as_float(o[0].sb.x));
     } else {
         const uint4 va = *reinterpret_cast<const uint4 *>(pa), vb = *reinterpret_cast<const uint4 *>(pa + 512);
         const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
         constexpr int kPer = kFewGroup<WT> / 32;                       // blocks of 32 inputs to a group
-        float part[4];
+        float part[NT][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t ra[4], rb[4];
-            w4_pairs<false>(wa[j], ra);
-            w4_pairs<false>(wb[j], rb);
-            if (j % kPer == 0) mma16816_first(part, ra[0], rb[0], ra[1], rb[1], o.x[j].x, o.x[j].y);
-            else mma16816<false>(part, ra[0], rb[0], ra[1], rb[1], o.x[j].x, o.x[j].y);
-            mma16816<false>(part, ra[2], rb[2], ra[3], rb[3], o.x[j].z, o.x[j].w);
-            if (j % kPer == kPer - 1) {
-                const uint32_t sa = j / kPer < 2 ? o.sa.x : o.sa.y, sb = j / kPer < 2 ? o.sb.x : o.sb.y;
-                if (j / kPer % 2 == 0) add_scaled(c, part, bf16_lo(sa), bf16_lo(sb));
-                else add_scaled(c, part, bf16_hi(sa), bf16_hi(sb));
+            w4_raw_pairs(wa[j], ra);
+            w4_raw_pairs(wb[j], rb);
+            const uint32_t sa = j / kPer < 2 ? o[0].sa.x : o[0].sa.y, sb = j / kPer < 2 ? o[0].sb.x : o[0].sb.y;
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+                if (j % kPer == 0) {               // from what the group's sum is too large by
+                    part[m][0] = part[m][2] = o[m].less[j / kPer][0];
+                    part[m][1] = part[m][3] = o[m].less[j / kPer][1];
+                }
+                mma16816<true>(part[m], ra[0], rb[0], ra[1], rb[1], o[m].x[j].x, o[m].x[j].y);
+                mma16816<true>(part[m], ra[2], rb[2], ra[3], rb[3], o[m].x[j].z, o[m].x[j].w);
+                if (j % kPer == kPer - 1) {
+                    if (j / kPer % 2 == 0) add_scaled(c[m], part[m], bf16_lo(sa), bf16_lo(sb));
+                    else add_scaled(c[m], part[m], bf16_hi(sa), bf16_hi(sb));
+                }
             }
         }
     }
 }
 
+// down, a unit split between several blocks: their sums [unit][2^split][T][16], and how many of them are there.
+struct FewParts {
+    float *sums;
+    unsigned *there;
+};
+
+// x: up, the tokens' inputs; down, the pairs' h; where they are fp16 with their rows' scales. h: what the up kernel writes,
+// fp32 where it is made fp16 after, else bf16.
 template <int WT, bool DOWN>
 __global__ void __launch_bounds__(kFewThreads, 2)
-few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const FewLists *made, const uint16_t *x,
-           const void *__restrict__ w_scale, uint16_t *h, uint16_t *__restrict__ out, unsigned *status) {
+few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int split, const FewLists *made, FewInputs in,
+           const void *__restrict__ w_scale, void *h, uint16_t *__restrict__ out, FewParts parts, unsigned *status) {
     extern __shared__ __align__(128) uint8_t few_smem[];
     __shared__ __align__(8) uint64_t full[kFewWarps][kFewSlots];
     __shared__ FewLists lists;
     __shared__ float4 red[DOWN ? 1 : kFewWarps][32];
+    __shared__ float token_scale[kFewTokens];
+    __shared__ bool last_here;
     // down: each warp's share of its unit's outputs, [warp][token][16]
     float *acc_out = reinterpret_cast<float *>(few_smem + kFewRing);
     constexpr int kBlockIn = kFewBlockInputs<WT>, kPieceIn = kBlockIn * kFewBlocks;
     constexpr int kGroup = kFewGroup<WT>, kStep = kFewStepBlocks<WT>, kSteps = kFewBlocks / kStep;
+    // bytes of a row's scales in a piece
+    constexpr int kScaleBytes = WT == kFp8 ? kPieceIn / 128 * 4 : kPieceIn / kGroup * 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int K = DOWN ? a.I : a.H, M = DOWN ? a.H : 2 * a.I;
     if (lane < kFewSlots) {
@@ -311,6 +425,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const F
     if constexpr (!DOWN) {
         pdl_wait();
         pdl_launch_dependents();
+        if (kFewHalf<WT> && tid < a.T) token_scale[tid] = in.scale[tid];
     }
     // the up kernel lets the down kernel start once the choice is made
     for (int i = tid; i < (int)(sizeof(FewLists) / 16); i += kFewThreads)
@@ -321,11 +436,14 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const F
     plan.lists = lists.n;
     plan.pieces = (K + kPieceIn - 1) / kPieceIn;
     plan.per = DOWN ? a.H / 16 : a.I / 8;
-    plan.units = DOWN ? (plan.lists > 0 ? plan.per : 0) : plan.per * plan.lists;
+    plan.units = DOWN ? (plan.lists > 0 ? plan.per << split : 0) : plan.per * plan.lists;
     plan.all = DOWN ? plan.lists * plan.pieces : plan.pieces;
     plan.team = team;
     plan.first = warp & (team - 1);
+    plan.split = split;
+    plan.step = team << split;
     plan.stride = gridDim.x * (kFewWarps / team);
+    const int tail = (K - (plan.pieces - 1) * kPieceIn) / kBlockIn;    // blocks of a row's last piece
     const unsigned scale_row = (unsigned)(K / kGroup) * 2u;
     // from the unit's row 0 to its row 8
     const unsigned row8 = DOWN ? 8u : (unsigned)a.I;
@@ -335,54 +453,56 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const F
     fw.unit = blockIdx.x + gridDim.x * (warp / team);
     int expert = 0, row0 = 0;
     const uint8_t *from = static_cast<const uint8_t *>(w_scale);
-    const auto aim = [&]() {                       // for the walk's list and place
-        if (fw.unit >= plan.units || fw.q >= plan.all) return;
+    const auto aim = [&]() {                       // for the walk's list and place, or the next unit's that has one for us
+        while (fw.q >= plan.all && fw.unit < plan.units) {
+            fw.unit += plan.stride;
+            fw.start(plan);
+        }
+        if (fw.unit >= plan.units) return;
         expert = lists.expert[fw.d];
         row0 = fw.row(plan) * (DOWN ? 16 : 8);
         if (kIsW4<WT>)
             from = static_cast<const uint8_t *>(w_scale) +
-                   ((size_t)expert * M + row0 + (lane & 7) + (lane & 8 ? row8 : 0u)) * scale_row + (size_t)fw.c * (kPieceIn * 2 / kGroup);
+                   ((size_t)expert * M + row0 + (lane & 7) + (lane & 8 ? row8 : 0u)) * scale_row + (size_t)fw.c * kScaleBytes;
     };
     fw.start(plan);
     aim();
     unsigned fetched = 0;
-    const auto fetch = [&]() {
-        if (fw.unit >= plan.units || fw.q >= plan.all) return;
-        const unsigned s = fetched % kFewSlots;
+    const auto fetch = [&](unsigned s) {
+        if (fw.unit >= plan.units) return;
         if (lane == 0) {
             mbar_expect_tx(&full[warp][s], kFewSlot);              // blocks past the row's end count, as zeros
             tma_load_5d(few_smem + (warp * kFewSlots + s) * kFewSlot, &map, &full[warp][s], row0, fw.c * kFewBlocks, expert);
         }
         if (kIsW4<WT> && lane < 16) asm volatile("prefetch.global.L2 [%0];" ::"l"(from));
         ++fetched;
-        fw.q += plan.team;
-        fw.c += plan.team;
-        if (fw.q >= plan.all) {
-            fw.unit += plan.stride;
-            fw.start(plan);
+        fw.q += plan.step;
+        fw.c += plan.step;
+        if (fw.q >= plan.all || (DOWN && fw.wrap(plan))) {
             aim();
-        } else if (DOWN && fw.wrap(plan)) {
-            aim();
-        } else {
-            from += plan.team * (kPieceIn * 2 / kGroup);
+        } else if (kIsW4<WT>) {
+            from += plan.step * kScaleBytes;
         }
     };
 #pragma unroll
-    for (int i = 0; i < kFewSlots; ++i) fetch();
+    for (int i = 0; i < kFewSlots; ++i) fetch(i);
 
     if constexpr (DOWN) {
         for (int i = lane; i < a.T * 16; i += 32) acc_out[warp * a.T * 16 + i] = 0.0f;
         pdl_wait();                                // h is there
         pdl_launch_dependents();
+        if (kFewHalf<WT>) {
+            for (int i = tid; i < lists.off[lists.n]; i += kFewThreads) lists.weight[i] *= in.scale[lists.pair[i]];
+            __syncthreads();
+        }
         __syncwarp();
     }
-    constexpr float kUnit = kIsW4<WT> ? kW4Unit<false> : 1.0f;
     const int first_warp = warp & ~(team - 1);
     const auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + first_warp), "r"(team * 32) : "memory"); };
     float acc[kFewTokens / 8][4];
 #pragma unroll
     for (int i = 0; i < kFewTokens / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-    unsigned n = 0, lost = 0;
+    unsigned n = 0, lost = 0, slot = 0, parity = 0;
     bool alive = true;
     int first = 0, rows = 0;
     // down: the list's rows into this warp's sums of their tokens
@@ -395,7 +515,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const F
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 if (r + q < rows) {
-                    const float by = lists.weight[first + r + q] * kUnit;
+                    const float by = lists.weight[first + r + q];
                     float *to = mine + lists.token[first + r + q] * 16 + g;
                     to[0] = fmaf(acc[nt][q], by, to[0]);
                     to[8] = fmaf(acc[nt][2 + q], by, to[8]);
@@ -404,20 +524,27 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const F
             acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
         }
     };
+    // A row of the inputs, that of row r of the list; rows past the list's last are the last one again: their columns are
+    // not stored.
+    const auto input_row = [&](int r) {
+        r = first + min(r, rows - 1);
+        return DOWN ? (int)lists.pair[r] : (int)lists.token[r];
+    };
 
     FewWalk<DOWN> walk;
     for (walk.unit = blockIdx.x + gridDim.x * (warp / team); walk.unit < plan.units; walk.unit += plan.stride) {
         walk.start(plan);
         bool fresh = true;                         // the list is new
-        // at the piece: a lane's inputs of its column of the first eight, and its rows' scales. Columns past the rows read
-        // the last row, and are not stored.
-        const uint16_t *px = x;
+        // at the piece: a lane's inputs of its column of the first eight, its columns' sums' starts, and its rows' scales
+        const uint16_t *px = in.x;
+        const float *pl0 = in.less, *pl1 = in.less;
         const uint8_t *psa = static_cast<const uint8_t *>(w_scale), *psb = psa;
-        for (; walk.q < plan.all;) {
-            const int k0 = walk.c * kPieceIn;
+        while (walk.q < plan.all) {
             const auto column = [&](int nt) {
-                const int r = first + min(8 * nt + g, rows - 1);
-                return (DOWN ? h + (size_t)lists.pair[r] * K : x + (size_t)lists.token[r] * K) + k0 + (WT == kFp8 ? 16 : 8) * t;
+                return in.x + (size_t)input_row(8 * nt + g) * K + walk.c * kPieceIn + (WT == kFp8 ? 16 : 8) * t;
+            };
+            const auto starts = [&](int col) {
+                return in.less + (size_t)input_row(col) * (K / kGroup) + walk.c * (kPieceIn / kGroup);
             };
             if (fresh) {
                 first = lists.off[walk.d];
@@ -425,85 +552,105 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const F
                 const size_t e = lists.expert[walk.d];
                 if constexpr (WT == kFp8) {
                     const int ma = walk.row(plan) * (DOWN ? 16 : 8), mb = DOWN ? ma : a.I + ma;
-                    const uint8_t *sc = static_cast<const uint8_t *>(w_scale) + 4 * (e * (M / 128) * (K / 128) + k0 / 128);
+                    const uint8_t *sc = static_cast<const uint8_t *>(w_scale) + 4 * (e * (M / 128) * (K / 128)) + walk.c * kScaleBytes;
                     psa = sc + 4 * (size_t)((ma / 128) * (K / 128));
                     psb = sc + 4 * (size_t)((mb / 128) * (K / 128));
                 }
                 if constexpr (kIsW4<WT>) {
                     psa = static_cast<const uint8_t *>(w_scale) + (e * M + walk.row(plan) * (DOWN ? 16 : 8) + g) * scale_row +
-                          k0 / kGroup * 2;
+                          walk.c * kScaleBytes;
                     psb = psa + (size_t)row8 * scale_row;
+                    pl0 = starts(2 * t);
+                    pl1 = starts(2 * t + 1);
                 }
                 px = column(0);
                 fresh = false;
             }
-            const auto load = [&](FewOperand<WT> &to, const uint16_t *p, int step, bool whole) {
+            const int blocks = walk.c == plan.pieces - 1 ? tail : kFewBlocks;
+            const auto load = [&](FewOperand<WT> &to, const uint16_t *p, const float *l0, const float *l1, int step, bool whole,
+                                  bool scales) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (WT != kBf16 || whole || k0 + (step * kStep + i) * kBlockIn < K)
+                    if (WT != kBf16 || whole || step * kStep + i < blocks)
                         to.x[i] = ld_v4(p + step * kStep * kBlockIn + (WT == kFp8 ? 64 * (i / 2) + 8 * (i % 2) : 32 * i));
-                if constexpr (WT == kFp8) {
+                if constexpr (kIsW4<WT>) {
+#pragma unroll
+                    for (int i = 0; i < 128 / kGroup; ++i) {
+                        to.less[i][0] = __uint_as_float(ld_u32(l0 + step * (128 / kGroup) + i));
+                        to.less[i][1] = __uint_as_float(ld_u32(l1 + step * (128 / kGroup) + i));
+                    }
+                }
+                if (!scales) return;
+                if constexpr (WT == kFp8 || WT == kW4G64) {
                     to.sa.x = ld_u32(psa + 4 * step);
                     to.sb.x = ld_u32(psb + 4 * step);
                 } else if constexpr (WT == kW4G128) {
                     to.sa.x = ld_u16(psa + 2 * step);
                     to.sb.x = ld_u16(psb + 2 * step);
-                } else if constexpr (WT == kW4G64) {
-                    to.sa.x = ld_u32(psa + 4 * step);
-                    to.sb.x = ld_u32(psb + 4 * step);
                 } else if constexpr (WT == kW4G32) {
                     to.sa = ld_v2(psa + 8 * step);
                     to.sb = ld_v2(psb + 8 * step);
                 }
             };
-            const int blocks = min(kFewBlocks, (K - k0) / kBlockIn);
-            FewOperand<WT> o;
-            load(o, px, 0, false);
-            const unsigned s = n % kFewSlots;
-            if (alive && !__all_sync(kFull, mbar_wait_bounded(&full[warp][s], (n / kFewSlots) & 1u))) {
+            FewOperand<WT> o[1];
+            load(o[0], px, pl0, pl1, 0, false, true);
+            if (alive && !__all_sync(kFull, mbar_try_wait(smem_u32(&full[warp][slot]), parity)) &&
+                !__all_sync(kFull, mbar_wait_bounded(&full[warp][slot], parity))) {
                 alive = false;                     // outputs stay wrong; the barriers below still meet
                 lost = n;
                 if (lane == 0) atomicOr(status, kStatusWaitGaveUp);
             }
-            const uint8_t *pa = few_smem + (warp * kFewSlots + s) * kFewSlot + 16 * lane;          // row g, 16 t bytes in
-            if (rows <= 8 && blocks == kFewBlocks) {               // most pieces: steps and offsets known
+            const uint8_t *pa = few_smem + (warp * kFewSlots + slot) * kFewSlot + 16 * lane;       // row g, 16 t bytes in
+            if (rows <= 8 && blocks == kFewBlocks) {                   // most pieces: steps and offsets known
 #pragma unroll
                 for (int step = 0; step < kSteps; ++step) {
                     FewOperand<WT> next;
-                    if (step + 1 < kSteps) load(next, px, step + 1, true);
-                    few_step<WT>(acc[0], o, pa + 1024 * kStep * step, kStep);
-                    if (step + 1 < kSteps) o = next;
+                    if (step + 1 < kSteps) load(next, px, pl0, pl1, step + 1, true, true);
+                    few_step<WT, 1>(acc, o, pa + 1024 * kStep * step, kStep);
+                    if (step + 1 < kSteps) o[0] = next;
+                }
+            } else if (rows <= 8) {
+#pragma unroll 1
+                for (int step = 0; step * kStep < blocks; ++step) {
+                    few_step<WT, 1>(acc, o, pa + 1024 * kStep * step, blocks - step * kStep);
+                    if ((step + 1) * kStep < blocks) load(o[0], px, pl0, pl1, step + 1, false, true);
                 }
             } else {
-                const uint16_t *p = px;
+                // 16 rows of the list at a time, for which the weights are made operands once
 #pragma unroll
-                for (int nt = 0; nt < kFewTokens / 8; ++nt) {
+                for (int nt = 0; nt < kFewTokens / 8; nt += 2) {
                     if (8 * nt >= rows) break;     // warp-uniform
+                    const uint16_t *p0 = column(nt), *p1 = column(nt + 1);
+                    const float *l[4] = {};
+                    if (kIsW4<WT>)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) l[i] = starts(8 * nt + 8 * (i / 2) + 2 * t + i % 2);
 #pragma unroll 1
                     for (int step = 0; step * kStep < blocks; ++step) {
-                        few_step<WT>(acc[nt], o, pa + 1024 * kStep * step, blocks - step * kStep);
-                        if ((step + 1) * kStep < blocks) {
-                            load(o, p, step + 1, false);
-                        } else if (8 * (nt + 1) < rows) {
-                            p = column(nt + 1);
-                            load(o, p, 0, false);
-                        }
+                        FewOperand<WT> two[2];
+                        load(two[0], p0, l[0], l[1], step, false, true);
+                        load(two[1], p1, l[2], l[3], step, false, false);
+                        few_step<WT, 2>(acc + nt, two, pa + 1024 * kStep * step, blocks - step * kStep);
                     }
                 }
             }
             ++n;
             __syncwarp();                          // every lane has read the slot
-            if (alive) fetch();
-            walk.q += plan.team;
-            walk.c += plan.team;
-            px += plan.team * kPieceIn;
-            if (WT == kFp8) {
-                psa += plan.team * (kPieceIn / 128) * 4;
-                psb += plan.team * (kPieceIn / 128) * 4;
+            if (alive) fetch(slot);
+            if (++slot == kFewSlots) {
+                slot = 0;
+                parity ^= 1u;
+            }
+            walk.q += plan.step;
+            walk.c += plan.step;
+            px += plan.step * kPieceIn;
+            if (WT != kBf16) {
+                psa += plan.step * kScaleBytes;
+                psb += plan.step * kScaleBytes;
             }
             if (kIsW4<WT>) {
-                psa += plan.team * (kPieceIn * 2 / kGroup);
-                psb += plan.team * (kPieceIn * 2 / kGroup);
+                pl0 += plan.step * (kPieceIn / kGroup);
+                pl1 += plan.step * (kPieceIn / kGroup);
             }
             if (DOWN && walk.wrap(plan)) {
                 fold();
@@ -535,18 +682,45 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, const F
                     team_sync();
                     if (warp != first_warp) continue;
                 }
-                const int r = 8 * nt + 2 * t, o = walk.row(plan) * 8 + g;
-                if (r < rows) put_bf16(h + (size_t)lists.pair[first + r] * a.I + o, silu(v.x * kUnit) * (v.z * kUnit));
-                if (r + 1 < rows) put_bf16(h + (size_t)lists.pair[first + r + 1] * a.I + o, silu(v.y * kUnit) * (v.w * kUnit));
+                const int r = first + 8 * nt + 2 * t, o = walk.row(plan) * 8 + g;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (r + q >= first + rows) break;
+                    const float by = kFewHalf<WT> ? token_scale[lists.token[r + q]] : 1.0f;
+                    const float u = silu((q ? v.y : v.x) * by) * ((q ? v.w : v.z) * by);
+                    const size_t to = (size_t)lists.pair[r + q] * a.I + o;
+                    if (kFewHalf<WT>) static_cast<float *>(h)[to] = u;
+                    else put_bf16(static_cast<uint16_t *>(h) + to, u);
+                }
             }
         } else {
             if (!fresh) fold();
             team_sync();
             const float *sums = acc_out + first_warp * a.T * 16;
-            for (int i = (warp - first_warp) * 32 + lane; i < a.T * 16; i += team * 32) {
+            const int in_team = (warp - first_warp) * 32 + lane;
+            const auto put = [&](int i, float v) { put_bf16(out + (size_t)(i >> 4) * a.H + walk.row(plan) * 16 + (i & 15), v); };
+            float *part = parts.sums + (size_t)walk.unit * a.T * 16;
+            for (int i = in_team; i < a.T * 16; i += team * 32) {
                 float v = 0.0f;
                 for (int j = 0; j < team; ++j) v += sums[j * a.T * 16 + i];
-                put_bf16(out + (size_t)(i >> 4) * a.H + walk.row(plan) * 16 + (i & 15), v);
+                if (split == 0) put(i, v);
+                else part[i] = v;
+            }
+            if (split > 0) {                       // the team is the block; the last one of the unit joins the sums, in order
+                __threadfence();
+                team_sync();
+                const int unit = walk.unit >> split;
+                if (tid == 0) last_here = atomicAdd(parts.there + unit, 1u) == (1u << split) - 1u;
+                team_sync();
+                if (last_here) {
+                    __threadfence();
+                    part = parts.sums + ((size_t)unit << split) * a.T * 16;
+                    for (int i = in_team; i < a.T * 16; i += team * 32) {
+                        float v = 0.0f;
+                        for (int j = 0; j < 1 << split; ++j) v += __ldcg(part + j * a.T * 16 + i);
+                        put(i, v);
+                    }
+                }
             }
             team_sync();
             for (int i = lane; i < a.T * 16; i += 32) acc_out[warp * a.T * 16 + i] = 0.0f;
@@ -599,13 +773,58 @@ bool encode_few(CUtensorMap *map, const void *base, uint64_t rows, uint64_t part
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What the workspace holds.
+struct FewSpace {
+    FewLists *lists;
+    FewParts parts;
+    void *h;                                       // [T (k + shared)][I]: bf16, or fp32 where h_half follows
+    FewInputs x_half, h_half;
+    size_t bytes;
+};
+// The binary logarithm of how many blocks share a down unit: where the units are too few for the SMs' warps (2048 outputs
+// are 128 units).
+int few_split(int H) {
+    int split = 0;
+    while (split < 3 && ((long long)(H / 16) * kFewWarps << (split + 1)) <= 2LL * 152 * kFewWarps) ++split;
+    return split;
+}
+FewSpace few_space(void *base, const Dims &d, const moe_mlp *m) {
+    FewSpace s = {};
+    uint8_t *at = static_cast<uint8_t *>(base);
+    const auto take = [&](size_t bytes) {
+        void *p = at + s.bytes;
+        s.bytes += (bytes + 255) & ~(size_t)255;
+        return p;
+    };
+    const size_t T = d.T, pairs = T * (d.k + m->shared), I = m->inner;
+    const int split = few_split(d.H);
+    const bool half = m->weights != MOE_WEIGHTS_BF16, w4 = m->weights == MOE_WEIGHTS_W4;
+    const auto inputs = [&](size_t rows, size_t n) {
+        FewInputs f;
+        f.x = static_cast<uint16_t *>(take(rows * n * 2));
+        f.scale = static_cast<float *>(take(rows * 4));
+        f.less = static_cast<float *>(take(w4 ? rows * (n / m->group) * 4 : 0));
+        return f;
+    };
+    s.lists = static_cast<FewLists *>(take(sizeof(FewLists)));
+    s.parts.there = static_cast<unsigned *>(take((size_t)d.H / 16 * sizeof(unsigned)));
+    s.parts.sums = static_cast<float *>(take(split > 0 ? ((size_t)d.H << split) * T * sizeof(float) : 0));
+    s.h = take(pairs * I * (half ? 4 : 2));
+    if (half) {
+        s.x_half = inputs(T, d.H);
+        s.h_half = inputs(pairs, I);
+    }
+    return s;
+}
+
 template <typename T, int V>
 int launch_choice(const FewArgs &a, cudaStream_t st, const void *logits, const float *bias, int32_t *idx, float *w,
-                  FewLists *lists) {
-    const int most = V <= 16 ? 32 : 8;             // warps; at least 4 for the clearing and the rows
-    const int warps = std::min(most, std::max(a.T, 4));
-    return launch_pdl(few_choice_kernel<T, V>, 1, warps * 32, st, a, static_cast<const T *>(logits), bias, idx, w, lists) ==
-                   cudaSuccess
+                  const void *x, int group, const FewSpace &s) {
+    const bool half = s.x_half.x != nullptr;
+    const int most = V <= 16 ? 32 : 8;             // warps; at least 8 for the clearing, and 8 values of x to a thread
+    const int warps = std::min(most, std::max(std::max(a.T, 8), half ? a.H / 256 : 0));
+    return launch_pdl(few_choice_kernel<T, V>, half ? 1 + a.T : 1, warps * 32, st, a, static_cast<const T *>(logits), bias, idx,
+                      w, s.lists, s.parts.there, static_cast<const uint16_t *>(x), group, s.x_half) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
@@ -621,7 +840,7 @@ int launch_choice_v(const FewArgs &a, A... args) {
 
 template <int WT>
 int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, const void *w_up, const void *up_scale,
-               const void *w_down, const void *down_scale, void *out, const FewLists *lists, void *h, unsigned *status) {
+               const void *w_down, const void *down_scale, void *out, const FewSpace &s, unsigned *status) {
     static PerContext<int> up_done, down_done;
     const size_t most = kFewRing + kFewWarps * kFewTokens * 16 * sizeof(float);
     if (!set_smem_once(up_done, few_kernel<WT, false>, kFewRing) || !set_smem_once(down_done, few_kernel<WT, true>, (int)most))
@@ -630,16 +849,26 @@ int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, 
     const uint64_t S = a.E + a.shared, block = kFewBlockInputs<WT>;
     if (!encode_few(&up, w_up, a.I, 2, a.H / block * 64, S, 8) || !encode_few(&down, w_down, a.H, 1, a.I / block * 64, S, 16))
         return MOE_ERR_CUDA;
+    uint16_t *o = static_cast<uint16_t *>(out);
+    constexpr bool half = kFewHalf<WT>;
+    constexpr int group = kIsW4<WT> ? kFewGroup<WT> : 0;
+    FewInputs up_x = s.x_half, down_x = s.h_half;
+    if (!half) {
+        up_x.x = static_cast<uint16_t *>(const_cast<void *>(x));
+        down_x.x = static_cast<uint16_t *>(s.h);
+    }
     long long units = (std::min<long long>((long long)d.T * d.k, d.E) + a.shared) * (a.I / 8);
-    if (launch_pdl_smem(few_kernel<WT, false>, few_grid(units, d.max_blocks), kFewThreads, kFewRing, st, up, a, few_team(units),
-                        lists, static_cast<const uint16_t *>(x), up_scale, static_cast<uint16_t *>(h),
-                        static_cast<uint16_t *>(out), status) != cudaSuccess)
+    if (launch_pdl_smem(few_kernel<WT, false>, few_grid(units, d.max_blocks), kFewThreads, kFewRing, st, up, a, few_team(units), 0,
+                        s.lists, up_x, up_scale, s.h, o, s.parts, status) != cudaSuccess)
         return MOE_ERR_CUDA;
-    units = d.H / 16;
+    if (half && launch_pdl(few_half_kernel, d.T * (d.k + a.shared), 256, st, s.lists, static_cast<const float *>(s.h), a.I, group,
+                           s.h_half) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    const int split = few_split(d.H);
+    units = (long long)(d.H / 16) << split;
     if (launch_pdl_smem(few_kernel<WT, true>, few_grid(units, d.max_blocks), kFewThreads,
-                        kFewRing + (size_t)kFewWarps * d.T * 16 * sizeof(float), st, down, a, few_team(units), lists,
-                        static_cast<const uint16_t *>(x), down_scale, static_cast<uint16_t *>(h),
-                        static_cast<uint16_t *>(out), status) != cudaSuccess)
+                        kFewRing + (size_t)kFewWarps * d.T * 16 * sizeof(float), st, down, a, few_team(units), split, s.lists,
+                        down_x, down_scale, s.h, o, s.parts, status) != cudaSuccess)
         return MOE_ERR_CUDA;
     return MOE_OK;
 }
@@ -651,8 +880,7 @@ extern "C" size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_
     using namespace moe;
     Dims d;
     if (check_problem(p, &d) != MOE_OK || check_mlp(mlp) != MOE_OK || check_few(d, mlp) != MOE_OK) return 0;
-    const size_t n = kFewListsBytes + (size_t)d.T * (d.k + mlp->shared) * mlp->inner * 2;
-    return (n + 255) & ~(size_t)255;
+    return few_space(nullptr, d, mlp).bytes;
 }
 
 extern "C" int moe_layer_few(const moe_problem *p, const moe_gate *gate, const moe_mlp *mlp, const void *x,
@@ -686,13 +914,13 @@ extern "C" int moe_layer_few(const moe_problem *p, const moe_gate *gate, const m
     unsigned *status = device_status_word();
     if (status == nullptr) return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
-    FewLists *lists = static_cast<FewLists *>(workspace);
-    void *h = static_cast<uint8_t *>(workspace) + kFewListsBytes;
-    rc = gate->logits_type == MOE_LOGITS_BF16 ? launch_choice_v<__nv_bfloat16>(a, st, logits, bias, topk_idx, topk_w, lists)
-                                              : launch_choice_v<float>(a, st, logits, bias, topk_idx, topk_w, lists);
+    const FewSpace s = few_space(workspace, d, mlp);
+    const int group = mlp->weights == MOE_WEIGHTS_W4 ? mlp->group : 0;
+    rc = gate->logits_type == MOE_LOGITS_BF16 ? launch_choice_v<__nv_bfloat16>(a, st, logits, bias, topk_idx, topk_w, x, group, s)
+                                              : launch_choice_v<float>(a, st, logits, bias, topk_idx, topk_w, x, group, s);
     if (rc != MOE_OK) return rc;
     const auto go = [&](auto kind) {
-        return launch_few<decltype(kind)::value>(d, a, st, x, w_up, up_scale, w_down, down_scale, out, lists, h, status);
+        return launch_few<decltype(kind)::value>(d, a, st, x, w_up, up_scale, w_down, down_scale, out, s, status);
     };
     if (mlp->weights == MOE_WEIGHTS_BF16) return go(std::integral_constant<int, kBf16>{});
     if (mlp->weights == MOE_WEIGHTS_FP8_B128) return go(std::integral_constant<int, kFp8>{});

@@ -552,13 +552,15 @@ typedef struct moe_mlp {
  * invalid. Contents need no initialisation. */
 size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
 
-/* A whole mixture-of-experts layer for up to 32 tokens, in two launches: the
+/* A whole mixture-of-experts layer for up to 32 tokens, in a few launches: the
  * choice as moe_route_gated makes it, then for every pair (t, j), e = topk_idx[t][j],
  *   u = x[t] Wup_e^T (2I values: the gate's I, then the up's)
- *   h[i] = bf16(silu(u[i]) u[I + i]),   silu(v) = v / (1 + exp(-v))
+ *   h[i] = round(silu(u[i]) u[I + i]),   silu(v) = v / (1 + exp(-v))
  *   out[t] = bf16(sum_j topk_w[t][j] h Wdown_e^T)
  * with the shared expert's term of weight 1 behind the pairs'. Products are exact,
- * sums fp32; h is rounded to bf16 (the products' operand type) and out once. There
+ * sums fp32; h is rounded to the products' operand type, which is bf16, or with e4m3
+ * weights fp16 behind a power of two for each row (x too: its values below 2^-29 of
+ * their row's largest then lose bits, 2^-39 of that largest at most); out once. There
  * is no capacity: no pair is dropped, and choices that are no pair take no part (a
  * token without pairs and without a shared expert has out 0). Each chosen expert's weights
  * are read once, the others' not at all.
@@ -568,8 +570,7 @@ size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
  * Matrices, output index major, of S = E + shared experts; M = 2I, K = H for w_up
  *   (the gate's I rows, then the up's) and M = H, K = I for w_down:
  *   MOE_WEIGHTS_BF16: bf16 [S][M][K], scales NULL;
- *   MOE_WEIGHTS_FP8_B128: e4m3 u8 [S][M][K], scale f32 [S][M/128][K/128] (the codes
- *     0x7f and 0xff, e4m3's NaN, count as +-480);
+ *   MOE_WEIGHTS_FP8_B128: e4m3 u8 [S][M][K], scale f32 [S][M/128][K/128];
  *   MOE_WEIGHTS_W4: codes u8 [S][M][K/2] packed as for moe_expert_w4 (w4_pack),
  *     scale bf16 [S][M][K/group].
  * T > 32, H or I no multiple of 64 (bf16) or 128 (fp8, 4-bit): MOE_ERR_UNSUPPORTED.

@@ -101,25 +101,39 @@ def bf16(a):
     return torch.from_numpy(np.ascontiguousarray(a)).float().to(torch.bfloat16).double().numpy()
 
 
-def mlp(x, up, down, inner):
+def mlp(x, up, down, inner, half=False, up_mag=None, down_mag=None):
     """One expert's MLP of rows x in float64, up [2 inner][H], down [H][inner], with h rounded to bf16 as the layer's
-    definition has it; and a bound on what the fp32 sums may move the result by.
+    definition has it; and a bound on what the fp32 sums may move the result by. half (weights of 8 and 4 bits): the inputs
+    of both products are fp16 behind a power of two for each row, h not rounded before: every h may be off by 2^-11 of it
+    (half a step of fp16), and every input by 2^-35 of its row's largest (half of fp16's lowest step, 2^-25, where the
+    largest is 2^14 or more, and 16 times that where inputs are divided by 16).
 
     A product of K inputs: an MMA step of 16 rounds its sum and its add into the accumulator (2), at most K/16 steps; a
-    group's sum is scaled and added (2 for each of K/32 groups at most); 8 partial sums are joined: (K/8 + K/16 + 16) u
-    of the sum of magnitudes =: B. silu moves by at most 1.1 of its argument's error and is formed in 4 roundings more,
-    2^-21 in all. Where that reach crosses a rounding border of bf16, h may be the neighbour: its reach is the difference
-    of the rounded ends. Down, h's reach goes through the magnitudes, and the product's own B is added."""
-    def product(v, w):
+    group's sum is scaled and added (2 for each of K/32 groups at most); 8 partial sums are joined, and at most 8 blocks':
+    (K/8 + K/16 + 24) u of the sum of magnitudes =: B. up_mag, down_mag (4-bit weights): the group's scale times 1040, the
+    largest operand that stands for a code; within a group of at most 128 inputs the sum is of these, from a start that is a
+    rounded sum itself: 16 roundings of 8 MMA steps and 36 of the start, 52 u of their magnitudes more. silu moves by at most
+    1.1 of its argument's error and is formed in 4 roundings more, 2^-21 in all. Where that reach crosses a rounding border
+    of bf16, h may be the neighbour: its reach is the difference of the rounded ends. Down, h's reach goes through the
+    magnitudes, and the product's own B is added."""
+    def product(v, w, mag):
         K = w.shape[1]
-        return v @ w.T, (K / 8 + K / 16 + 16) * U * (np.abs(v) @ np.abs(w).T)
-    r, B = product(x, up)
+        B = (K / 8 + K / 16 + 24) * U * (np.abs(v) @ np.abs(w).T)
+        if half:
+            B = B + 2.0 ** -35 * np.abs(v).max(1, keepdims=True) * np.abs(w).sum(1)
+        if mag is not None:
+            B = B + 52 * U * (np.abs(v) @ mag.T)
+        return v @ w.T, B
+    r, B = product(x, up, up_mag)
     g, u, Bg, Bu = r[:, :inner], r[:, inner:], B[:, :inner], B[:, inner:]
     with np.errstate(over="ignore"):
         s = g / (1.0 + np.exp(-g))
     h = s * u
     reach = 1.1 * Bg * np.abs(u) + np.abs(s) * Bu + Bg * Bu + 2.0 ** -21 * np.abs(h)
-    hr = bf16(h)
-    reach = np.maximum(np.abs(bf16(h + reach) - hr), np.abs(bf16(h - reach) - hr))
-    out, Bo = product(hr, down)
+    if half:
+        reach, hr = reach + 2.0 ** -11 * np.abs(h), h
+    else:
+        hr = bf16(h)
+        reach = np.maximum(np.abs(bf16(h + reach) - hr), np.abs(bf16(h - reach) - hr))
+    out, Bo = product(hr, down, down_mag)
     return out, Bo + reach @ np.abs(down).T

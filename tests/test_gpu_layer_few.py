@@ -1,5 +1,5 @@
 """The whole layer for a few tokens on the GPU against a plain form in 64 bits: the choice as plain64.gate makes it, the
-experts' MLPs with h rounded to bf16 as the layer's definition has it.
+experts' MLPs with h rounded as the layer's definition has it.
 
 Tolerance: plain64_block.mlp's bound for each pair, weighted; the weighted sum's own roundings, 2 for each of at most 17
 terms and 3 for the warps' joining, 2^-19 of the sum of magnitudes with room; a routing weight's own error, 2^-20 of it
@@ -25,19 +25,20 @@ def M():
 
 
 def matrix(M, n, rows, cols, kind, group, g):
-    """(weights, scales, their values [n][rows][cols] in float64)"""
+    """(weights, scales, their values [n][rows][cols] in float64, for 4-bit ones their operands' magnitudes)"""
     if kind == "bf16":
         w = (torch.randn((n, rows, cols), device=DEV, generator=g) / cols ** 0.5).to(torch.bfloat16)
-        return w, None, w.double().cpu().numpy()
+        return w, None, w.double().cpu().numpy(), None
     if kind == "fp8":
         q = torch.randint(0, 256, (n, rows, cols), dtype=torch.uint8, device=DEV, generator=g)
         q = torch.where((q & 0x7F) == 0x7F, q - 1, q)        # every code but the NaNs
         s = (1 + torch.rand((n, rows // 128, cols // 128), device=DEV, generator=g)) * 0.01 / cols ** 0.5
         v = q.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(128, 1).repeat_interleave(128, 2)
-        return q, s, v.cpu().numpy()
+        return q, s, v.cpu().numpy(), None
     q = torch.randint(0, 16, (n, rows, cols), dtype=torch.uint8, device=DEV, generator=g)
     s = ((1 + torch.rand((n, rows, cols // group), device=DEV, generator=g)) * 0.15 / cols ** 0.5).to(torch.bfloat16)
-    return M.w4_pack(q), s, ((q.double() - 8) * s.double().repeat_interleave(group, 2)).cpu().numpy()
+    full = s.double().repeat_interleave(group, 2)
+    return M.w4_pack(q), s, ((q.double() - 8) * full).cpu().numpy(), (1040 * full).cpu().numpy()
 
 
 def make(M, T, E, k, H, I, kind, group=128, shared=0, seed=0, sigmoid=True, logits_bf16=False):
@@ -86,7 +87,8 @@ def check(s, idx, w, out):
         t, j = np.nonzero((ri == e) & ok) if e < E else (np.arange(T), None)
         if len(t) == 0:
             continue
-        v, B = PB.mlp(x[t], s["up"][2][e], s["down"][2][e], I)
+        v, B = PB.mlp(x[t], s["up"][2][e], s["down"][2][e], I, s["kind"] != "bf16",
+                      *(m[3][e] if m[3] is not None else None for m in (s["up"], s["down"])))
         by = rw[t, j][:, None] if j is not None else 1.0
         ref[t] += by * v
         bound[t] += np.abs(by) * B
@@ -96,6 +98,8 @@ def check(s, idx, w, out):
     err = np.abs(o - ref)
     assert np.isfinite(o).all()
     assert (err <= bar).all(), (err / bar).max()
+    # the bounds add worst cases up; what is left in earnest is the output's rounding, at most 2^-8 of each value
+    assert np.linalg.norm(err) <= (2.0 ** -8 + 2.0 ** -12) * np.linalg.norm(ref)
 
 
 def steps(kind):
