@@ -37,7 +37,7 @@ constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewRows = 16;                       // matrix rows of a unit
 constexpr int kFewBlocks = 4;                      // blocks (64 bytes of each row) in a slot of a warp's ring
 constexpr int kFewSlot = kFewBlocks * kFewRows * 64;
-constexpr int kFewSlots = 3;                       // for each warp
+constexpr int kFewSlots = 2;                       // for each warp
 constexpr int kFewRing = kFewWarps * kFewSlots * kFewSlot;
 constexpr int kFewMaxPairs = kFewTokens * kMaxTopK + kFewTokens;       // with the shared expert's
 constexpr int kFewMaxLists = kFewTokens * kMaxTopK + 1;                // experts with rows
@@ -74,27 +74,45 @@ struct alignas(16) FewLists {
 };
 
 // Loads whose addresses are only good where the program order comes to them: volatile, so that none is made earlier.
+// OFF: bytes on from the address, within the instruction.
+template <int OFF>
 __device__ __forceinline__ uint32_t ld_u16(const void *p) {
     uint16_t r;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+    asm volatile("ld.global.nc.u16 %0, [%1+%2];" : "=h"(r) : "l"(p), "n"(OFF));
     return r;
 }
+template <int OFF>
 __device__ __forceinline__ uint32_t ld_u32(const void *p) {
     uint32_t r;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(r) : "l"(p));
+    asm volatile("ld.global.nc.u32 %0, [%1+%2];" : "=r"(r) : "l"(p), "n"(OFF));
     return r;
 }
+template <int OFF>
 __device__ __forceinline__ uint2 ld_v2(const void *p) {
     uint2 r;
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2+%3];" : "=r"(r.x), "=r"(r.y) : "l"(p), "n"(OFF));
     return r;
 }
+template <int OFF>
+__device__ __forceinline__ float ld_f32(const void *p) {
+    float r;
+    asm volatile("ld.global.f32 %0, [%1+%2];" : "=f"(r) : "l"(p), "n"(OFF));
+    return r;
+}
+template <int OFF = 0>
 __device__ __forceinline__ uint4 ld_v4(const void *p) {
     uint4 r;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4+%5];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p), "n"(OFF));
     return r;
 }
-
+// f of the numbers 0 .. N - 1 as types.
+template <int I, int N, typename F>
+__device__ __forceinline__ void each(F f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each<I + 1, N>(f);
+    }
+}
 __device__ __forceinline__ uint4 ld_l2_v4(const void *p) {
     uint4 r;
     asm volatile("ld.global.cg.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
@@ -172,11 +190,13 @@ __device__ __forceinline__ void row_to_half(const T *row, int n, int group, cons
 
 // h as fp16, a block to a pair. Lets the down kernel start at once.
 __global__ void __launch_bounds__(256)
-few_half_kernel(const FewLists *__restrict__ l, const float *h, int I, int group, FewInputs to) {
+few_half_kernel(const FewLists *l, const float *h, int I, int group, FewInputs to) {
     pdl_launch_dependents();
-    pdl_wait();
-    if ((int)blockIdx.x >= l->off[l->n]) return;
+    // the lists are there: the up kernel, which let this one start, waited for them
+    const bool live = (int)blockIdx.x < l->off[l->n];
     const int pair = l->pair[blockIdx.x];
+    pdl_wait();
+    if (!live) return;
     row_to_half(h + (size_t)pair * I, I, group, to, pair);
 }
 
@@ -400,7 +420,8 @@ struct FewParts {
 
 // x: up, the tokens' inputs; down, the pairs' h; where they are fp16 with their rows' scales. h: what the up kernel writes,
 // fp32 where it is made fp16 after, else bf16.
-template <int WT, bool DOWN>
+// NTM times 8 columns at most.
+template <int WT, bool DOWN, int NTM>
 __global__ void __launch_bounds__(kFewThreads, 2)
 few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int split, const FewLists *made, FewInputs in,
            const void *__restrict__ w_scale, void *h, uint16_t *__restrict__ out, FewParts parts, unsigned *status) {
@@ -499,9 +520,9 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int spl
     }
     const int first_warp = warp & ~(team - 1);
     const auto team_sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + first_warp), "r"(team * 32) : "memory"); };
-    float acc[kFewTokens / 8][4];
+    float acc[NTM][4];
 #pragma unroll
-    for (int i = 0; i < kFewTokens / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+    for (int i = 0; i < NTM; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
     unsigned n = 0, lost = 0, slot = 0, parity = 0;
     bool alive = true;
     int first = 0, rows = 0;
@@ -509,7 +530,7 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int spl
     const auto fold = [&]() {
         float *mine = acc_out + warp * a.T * 16;
 #pragma unroll
-        for (int nt = 0; nt < kFewTokens / 8; ++nt) {
+        for (int nt = 0; nt < NTM; ++nt) {
             if (8 * nt >= rows) break;
             const int r = 8 * nt + 2 * t;
 #pragma unroll
@@ -531,69 +552,88 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int spl
         return DOWN ? (int)lists.pair[r] : (int)lists.token[r];
     };
 
+    // Where a lane reads at a piece: its inputs of its column of the list's first eight, the starts of its two columns' sums,
+    // its rows' scales.
+    struct Place {
+        const uint16_t *x;
+        const float *l0, *l1;
+        const uint8_t *sa, *sb;
+    };
     FewWalk<DOWN> walk;
     for (walk.unit = blockIdx.x + gridDim.x * (warp / team); walk.unit < plan.units; walk.unit += plan.stride) {
         walk.start(plan);
-        bool fresh = true;                         // the list is new
-        // at the piece: a lane's inputs of its column of the first eight, its columns' sums' starts, and its rows' scales
-        const uint16_t *px = in.x;
-        const float *pl0 = in.less, *pl1 = in.less;
-        const uint8_t *psa = static_cast<const uint8_t *>(w_scale), *psb = psa;
-        while (walk.q < plan.all) {
-            const auto column = [&](int nt) {
-                return in.x + (size_t)input_row(8 * nt + g) * K + walk.c * kPieceIn + (WT == kFp8 ? 16 : 8) * t;
-            };
-            const auto starts = [&](int col) {
-                return in.less + (size_t)input_row(col) * (K / kGroup) + walk.c * (kPieceIn / kGroup);
-            };
-            if (fresh) {
-                first = lists.off[walk.d];
-                rows = lists.off[walk.d + 1] - first;
-                const size_t e = lists.expert[walk.d];
-                if constexpr (WT == kFp8) {
-                    const int ma = walk.row(plan) * (DOWN ? 16 : 8), mb = DOWN ? ma : a.I + ma;
-                    const uint8_t *sc = static_cast<const uint8_t *>(w_scale) + 4 * (e * (M / 128) * (K / 128)) + walk.c * kScaleBytes;
-                    psa = sc + 4 * (size_t)((ma / 128) * (K / 128));
-                    psb = sc + 4 * (size_t)((mb / 128) * (K / 128));
-                }
-                if constexpr (kIsW4<WT>) {
-                    psa = static_cast<const uint8_t *>(w_scale) + (e * M + walk.row(plan) * (DOWN ? 16 : 8) + g) * scale_row +
-                          walk.c * kScaleBytes;
-                    psb = psa + (size_t)row8 * scale_row;
-                    pl0 = starts(2 * t);
-                    pl1 = starts(2 * t + 1);
-                }
-                px = column(0);
-                fresh = false;
+        const auto place = [&](Place &p) {         // for the walk's list and piece
+            first = lists.off[walk.d];
+            rows = lists.off[walk.d + 1] - first;
+            const size_t e = lists.expert[walk.d];
+            if constexpr (WT == kFp8) {
+                const int ma = walk.row(plan) * (DOWN ? 16 : 8), mb = DOWN ? ma : a.I + ma;
+                const uint8_t *sc = static_cast<const uint8_t *>(w_scale) + 4 * (e * (M / 128) * (K / 128)) + walk.c * kScaleBytes;
+                p.sa = sc + 4 * (size_t)((ma / 128) * (K / 128));
+                p.sb = sc + 4 * (size_t)((mb / 128) * (K / 128));
             }
-            const int blocks = walk.c == plan.pieces - 1 ? tail : kFewBlocks;
-            const auto load = [&](FewOperand<WT> &to, const uint16_t *p, const float *l0, const float *l1, int step, bool whole,
-                                  bool scales) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (WT != kBf16 || whole || step * kStep + i < blocks)
-                        to.x[i] = ld_v4(p + step * kStep * kBlockIn + (WT == kFp8 ? 64 * (i / 2) + 8 * (i % 2) : 32 * i));
-                if constexpr (kIsW4<WT>) {
-#pragma unroll
-                    for (int i = 0; i < 128 / kGroup; ++i) {
-                        to.less[i][0] = __uint_as_float(ld_u32(l0 + step * (128 / kGroup) + i));
-                        to.less[i][1] = __uint_as_float(ld_u32(l1 + step * (128 / kGroup) + i));
-                    }
+            if constexpr (kIsW4<WT>) {
+                p.sa = static_cast<const uint8_t *>(w_scale) + (e * M + walk.row(plan) * (DOWN ? 16 : 8) + g) * scale_row +
+                       walk.c * kScaleBytes;
+                p.sb = p.sa + (size_t)row8 * scale_row;
+            }
+        };
+        const auto columns = [&](Place &p, int nt) {                   // and for the list's rows 8 nt and on
+            p.x = in.x + (size_t)input_row(8 * nt + g) * K + walk.c * kPieceIn + (WT == kFp8 ? 16 : 8) * t;
+            if constexpr (kIsW4<WT>) {
+                p.l0 = in.less + (size_t)input_row(8 * nt + 2 * t) * (K / kGroup) + walk.c * (kPieceIn / kGroup);
+                p.l1 = in.less + (size_t)input_row(8 * nt + 2 * t + 1) * (K / kGroup) + walk.c * (kPieceIn / kGroup);
+            }
+        };
+        // step `number` of a piece that has `blocks` blocks
+        const auto load = [&](FewOperand<WT> &to, const Place &p, auto number, int blocks, bool scales) {
+            constexpr int step = decltype(number)::value, at = step * kStep * kBlockIn * 2;
+            if constexpr (WT == kBf16) {
+                to.x[0] = ld_v4<at>(p.x);          // a row's length is a multiple of two blocks
+                to.x[1] = ld_v4<at + 64>(p.x);
+                if (blocks > 2) {
+                    to.x[2] = ld_v4<at + 128>(p.x);
+                    to.x[3] = ld_v4<at + 192>(p.x);
                 }
-                if (!scales) return;
-                if constexpr (WT == kFp8 || WT == kW4G64) {
-                    to.sa.x = ld_u32(psa + 4 * step);
-                    to.sb.x = ld_u32(psb + 4 * step);
-                } else if constexpr (WT == kW4G128) {
-                    to.sa.x = ld_u16(psa + 2 * step);
-                    to.sb.x = ld_u16(psb + 2 * step);
-                } else if constexpr (WT == kW4G32) {
-                    to.sa = ld_v2(psa + 8 * step);
-                    to.sb = ld_v2(psb + 8 * step);
-                }
-            };
-            FewOperand<WT> o[1];
-            load(o[0], px, pl0, pl1, 0, false, true);
+            } else if constexpr (WT == kFp8) {
+                to.x[0] = ld_v4<at>(p.x);
+                to.x[1] = ld_v4<at + 16>(p.x);
+                to.x[2] = ld_v4<at + 128>(p.x);
+                to.x[3] = ld_v4<at + 144>(p.x);
+            } else {
+                to.x[0] = ld_v4<at>(p.x);
+                to.x[1] = ld_v4<at + 64>(p.x);
+                to.x[2] = ld_v4<at + 128>(p.x);
+                to.x[3] = ld_v4<at + 192>(p.x);
+                each<0, 128 / kGroup>([&](auto i) {
+                    constexpr int off = 4 * (step * (128 / kGroup) + decltype(i)::value);
+                    to.less[decltype(i)::value][0] = ld_f32<off>(p.l0);
+                    to.less[decltype(i)::value][1] = ld_f32<off>(p.l1);
+                });
+            }
+            if (!scales) return;
+            if constexpr (WT == kFp8 || WT == kW4G64) {
+                to.sa.x = ld_u32<4 * step>(p.sa);
+                to.sb.x = ld_u32<4 * step>(p.sb);
+            } else if constexpr (WT == kW4G128) {
+                to.sa.x = ld_u16<2 * step>(p.sa);
+                to.sb.x = ld_u16<2 * step>(p.sb);
+            } else if constexpr (WT == kW4G32) {
+                to.sa = ld_v2<8 * step>(p.sa);
+                to.sb = ld_v2<8 * step>(p.sb);
+            }
+        };
+        constexpr std::integral_constant<int, 0> kFirst{};
+        Place at;
+        FewOperand<WT> o[1];
+        const auto blocks_of = [&](int c) { return c == plan.pieces - 1 ? tail : kFewBlocks; };
+        if (walk.q < plan.all) {
+            place(at);
+            columns(at, 0);
+            load(o[0], at, kFirst, blocks_of(walk.c), true);
+        }
+        while (walk.q < plan.all) {
+            const int blocks = blocks_of(walk.c);
             if (alive && !__all_sync(kFull, mbar_try_wait(smem_u32(&full[warp][slot]), parity)) &&
                 !__all_sync(kFull, mbar_wait_bounded(&full[warp][slot], parity))) {
                 alive = false;                     // outputs stay wrong; the barriers below still meet
@@ -601,38 +641,66 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int spl
                 if (lane == 0) atomicOr(status, kStatusWaitGaveUp);
             }
             const uint8_t *pa = few_smem + (warp * kFewSlots + slot) * kFewSlot + 16 * lane;       // row g, 16 t bytes in
-            if (rows <= 8 && blocks == kFewBlocks) {                   // most pieces: steps and offsets known
-#pragma unroll
-                for (int step = 0; step < kSteps; ++step) {
+            if ((NTM == 1 || rows <= 8) && blocks == kFewBlocks) {                   // most pieces: steps and offsets known
+                each<0, kSteps>([&](auto number) {
+                    constexpr int step = decltype(number)::value;
                     FewOperand<WT> next;
-                    if (step + 1 < kSteps) load(next, px, pl0, pl1, step + 1, true, true);
+                    if constexpr (step + 1 < kSteps) load(next, at, std::integral_constant<int, step + 1>{}, kFewBlocks, true);
                     few_step<WT, 1>(acc, o, pa + 1024 * kStep * step, kStep);
-                    if (step + 1 < kSteps) o[0] = next;
-                }
-            } else if (rows <= 8) {
-#pragma unroll 1
-                for (int step = 0; step * kStep < blocks; ++step) {
-                    few_step<WT, 1>(acc, o, pa + 1024 * kStep * step, blocks - step * kStep);
-                    if ((step + 1) * kStep < blocks) load(o[0], px, pl0, pl1, step + 1, false, true);
-                }
+                    if constexpr (step + 1 < kSteps) o[0] = next;
+                });
             } else {
-                // 16 rows of the list at a time, for which the weights are made operands once
+                // 16 rows of the list at a time, for which the weights are made operands once; the tails of few rows
 #pragma unroll
-                for (int nt = 0; nt < kFewTokens / 8; nt += 2) {
+                for (int nt = 0; nt < NTM; nt += 2) {
                     if (8 * nt >= rows) break;     // warp-uniform
-                    const uint16_t *p0 = column(nt), *p1 = column(nt + 1);
-                    const float *l[4] = {};
-                    if (kIsW4<WT>)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) l[i] = starts(8 * nt + 8 * (i / 2) + 2 * t + i % 2);
+                    const bool pair = NTM > 1 && rows > 8 * (nt + 1);
+                    Place p0 = at, p1 = at;
+                    columns(p0, nt);
+                    if (pair) columns(p1, nt + 1);
 #pragma unroll 1
-                    for (int step = 0; step * kStep < blocks; ++step) {
-                        FewOperand<WT> two[2];
-                        load(two[0], p0, l[0], l[1], step, false, true);
-                        load(two[1], p1, l[2], l[3], step, false, false);
-                        few_step<WT, 2>(acc + nt, two, pa + 1024 * kStep * step, blocks - step * kStep);
+                    for (int b = 0; b < blocks; b += kStep) {
+                        load(o[0], p0, kFirst, blocks - b, true);
+                        if (NTM > 1 && pair) {
+                            FewOperand<WT> two[2];
+                            two[0] = o[0];
+                            load(two[1], p1, kFirst, blocks - b, false);
+                            few_step<WT, 2>(acc + nt, two, pa + 1024 * b, blocks - b);
+                        } else {
+                            few_step<WT, 1>(acc + nt, o, pa + 1024 * b, blocks - b);
+                        }
+                        p0.x += kStep * kBlockIn;
+                        p1.x += kStep * kBlockIn;
+                        p0.sa += kScaleBytes / kSteps;
+                        p0.sb += kScaleBytes / kSteps;
+                        if (kIsW4<WT>) {
+                            p0.l0 += 128 / kGroup;
+                            p0.l1 += 128 / kGroup;
+                            p1.l0 += 128 / kGroup;
+                            p1.l1 += 128 / kGroup;
+                        }
                     }
                 }
+            }
+            // on to the next piece, whose first step's operands come while this warp frees the slot and waits
+            walk.q += plan.step;
+            walk.c += plan.step;
+            const bool other = DOWN && walk.wrap(plan);
+            if (DOWN && (other || walk.q >= plan.all)) fold();
+            if (walk.q < plan.all) {
+                if (other) {
+                    place(at);
+                    columns(at, 0);
+                } else {
+                    at.x += plan.step * kPieceIn;
+                    at.sa += plan.step * kScaleBytes;
+                    at.sb += plan.step * kScaleBytes;
+                    if (kIsW4<WT>) {
+                        at.l0 += plan.step * (kPieceIn / kGroup);
+                        at.l1 += plan.step * (kPieceIn / kGroup);
+                    }
+                }
+                load(o[0], at, kFirst, blocks_of(walk.c), true);
             }
             ++n;
             __syncwarp();                          // every lane has read the slot
@@ -641,29 +709,15 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int spl
                 slot = 0;
                 parity ^= 1u;
             }
-            walk.q += plan.step;
-            walk.c += plan.step;
-            px += plan.step * kPieceIn;
-            if (WT != kBf16) {
-                psa += plan.step * kScaleBytes;
-                psb += plan.step * kScaleBytes;
-            }
-            if (kIsW4<WT>) {
-                pl0 += plan.step * (kPieceIn / kGroup);
-                pl1 += plan.step * (kPieceIn / kGroup);
-            }
-            if (DOWN && walk.wrap(plan)) {
-                fold();
-                fresh = true;
-            }
         }
 
         if constexpr (!DOWN) {
             // h from the sums of the unit's list, joined over the team's warps
+            walk.start(plan);
             first = lists.off[walk.d];
             rows = lists.off[walk.d + 1] - first;
 #pragma unroll
-            for (int nt = 0; nt < kFewTokens / 8; ++nt) {
+            for (int nt = 0; nt < NTM; ++nt) {
                 if (8 * nt >= rows) break;
                 float4 v = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
                 acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
@@ -694,7 +748,6 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int spl
                 }
             }
         } else {
-            if (!fresh) fold();
             team_sync();
             const float *sums = acc_out + first_warp * a.T * 16;
             const int in_team = (warp - first_warp) * 32 + lane;
@@ -838,12 +891,12 @@ int launch_choice_v(const FewArgs &a, A... args) {
     return launch_choice<T, 64>(a, args...);
 }
 
-template <int WT>
+template <int WT, int NTM>
 int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, const void *w_up, const void *up_scale,
                const void *w_down, const void *down_scale, void *out, const FewSpace &s, unsigned *status) {
     static PerContext<int> up_done, down_done;
     const size_t most = kFewRing + kFewWarps * kFewTokens * 16 * sizeof(float);
-    if (!set_smem_once(up_done, few_kernel<WT, false>, kFewRing) || !set_smem_once(down_done, few_kernel<WT, true>, (int)most))
+    if (!set_smem_once(up_done, few_kernel<WT, false, NTM>, kFewRing) || !set_smem_once(down_done, few_kernel<WT, true, NTM>, (int)most))
         return MOE_ERR_CUDA;
     CUtensorMap up, down;
     const uint64_t S = a.E + a.shared, block = kFewBlockInputs<WT>;
@@ -858,7 +911,7 @@ int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, 
         down_x.x = static_cast<uint16_t *>(s.h);
     }
     long long units = (std::min<long long>((long long)d.T * d.k, d.E) + a.shared) * (a.I / 8);
-    if (launch_pdl_smem(few_kernel<WT, false>, few_grid(units, d.max_blocks), kFewThreads, kFewRing, st, up, a, few_team(units), 0,
+    if (launch_pdl_smem(few_kernel<WT, false, NTM>, few_grid(units, d.max_blocks), kFewThreads, kFewRing, st, up, a, few_team(units), 0,
                         s.lists, up_x, up_scale, s.h, o, s.parts, status) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (half && launch_pdl(few_half_kernel, d.T * (d.k + a.shared), 256, st, s.lists, static_cast<const float *>(s.h), a.I, group,
@@ -866,7 +919,7 @@ int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, 
         return MOE_ERR_CUDA;
     const int split = few_split(d.H);
     units = (long long)(d.H / 16) << split;
-    if (launch_pdl_smem(few_kernel<WT, true>, few_grid(units, d.max_blocks), kFewThreads,
+    if (launch_pdl_smem(few_kernel<WT, true, NTM>, few_grid(units, d.max_blocks), kFewThreads,
                         kFewRing + (size_t)kFewWarps * d.T * 16 * sizeof(float), st, down, a, few_team(units), split, s.lists,
                         down_x, down_scale, s.h, o, s.parts, status) != cudaSuccess)
         return MOE_ERR_CUDA;
@@ -920,7 +973,8 @@ extern "C" int moe_layer_few(const moe_problem *p, const moe_gate *gate, const m
                                               : launch_choice_v<float>(a, st, logits, bias, topk_idx, topk_w, x, group, s);
     if (rc != MOE_OK) return rc;
     const auto go = [&](auto kind) {
-        return launch_few<decltype(kind)::value>(d, a, st, x, w_up, up_scale, w_down, down_scale, out, s, status);
+        if (d.T <= 8) return launch_few<decltype(kind)::value, 1>(d, a, st, x, w_up, up_scale, w_down, down_scale, out, s, status);
+        return launch_few<decltype(kind)::value, 4>(d, a, st, x, w_up, up_scale, w_down, down_scale, out, s, status);
     };
     if (mlp->weights == MOE_WEIGHTS_BF16) return go(std::integral_constant<int, kBf16>{});
     if (mlp->weights == MOE_WEIGHTS_FP8_B128) return go(std::integral_constant<int, kFp8>{});
