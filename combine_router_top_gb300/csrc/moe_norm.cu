@@ -24,6 +24,8 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxHidden = 16384;
+constexpr int kNormMaxDepth = 4;                   // rows on their way or at hand in a ring
+constexpr int kNormThreadsPerSM = 1024;
 
 struct NormArgs {
     int T, H8, k, C;                   // H8 chunks of 8 elements to a row
@@ -127,6 +129,36 @@ __device__ __forceinline__ void block_sum(BlockSum<N> &s, float (&v)[N], unsigne
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
     }
+}
+
+// Sums of four values over the block: over the warp by halves, two values to a lane after one exchange, one after two,
+// which takes 6 shuffles instead of 20; then over the warps, a lane to a value of a warp.
+struct BlockSum4 {
+    float part[2][32][4];
+};
+__device__ __forceinline__ void block_sum4(BlockSum4 &s, float (&v)[4], unsigned &turn) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const bool odd = lane & 1, upper = lane & 2;
+    // lanes with bit 1 go on with values 2 and 3, the others with 0 and 1; then bit 0 chooses between two
+    float a0 = upper ? v[2] : v[0], a1 = upper ? v[3] : v[1];
+    a0 += __shfl_xor_sync(kFull, upper ? v[0] : v[2], 2);
+    a1 += __shfl_xor_sync(kFull, upper ? v[1] : v[3], 2);
+    float x = odd ? a1 : a0;
+    x += __shfl_xor_sync(kFull, odd ? a0 : a1, 1);
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+    if (warps > 1) {
+        const unsigned b = turn & 1u;
+        ++turn;
+        if (lane < 4) s.part[b][warp][lane] = x;
+        __syncthreads();
+        x = 0.0f;
+        for (int i = lane >> 2; i < warps; i += 8) x += s.part[b][i][lane & 3];
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(kFull, x, i);
 }
 
 __device__ __forceinline__ float inv_rms(float sum_sq, const NormArgs &a) {
@@ -294,6 +326,129 @@ norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__restrict__ 
     }
 }
 
+// moe_block_norm for many rows. A block of threads takes a row at a time, NC chunks of 8 elements to a thread; the rows of
+// y and of the residual come by bulk copies into a ring, `depth` rows deep, so that loads run on while a row's sums meet.
+template <bool RES32, bool PAR32, int NC>
+__global__ void __launch_bounds__(512, NC == 4 ? 1 : 2)
+norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__restrict__ w_post,
+                 const void *__restrict__ w_pre, const void *__restrict__ gate, void *r_out, void *n_out, int depth,
+                 unsigned *status) {
+    extern __shared__ __align__(128) char norm_ring[];
+    __shared__ __align__(8) uint64_t full[kNormMaxDepth];
+    __shared__ BlockSum<1> sums;
+    const int tid = threadIdx.x;
+    const unsigned bf_row = (unsigned)a.H8 * 16u, res_row = RES32 ? 2u * bf_row : bf_row, stage = bf_row + res_row;
+    if (tid < depth) {
+        mbar_init(&full[tid], 1u);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_enter();
+    bool alive = true;
+    unsigned fetched = 0;
+    const auto fetch = [&](unsigned s) {             // thread 0
+        const long long row = blockIdx.x + (long long)fetched * gridDim.x;
+        if (row >= a.T || !alive) return;
+        char *to = norm_ring + (size_t)s * stage;
+        mbar_expect_tx(&full[s], stage);
+        bulk_g2s(to, static_cast<const char *>(y) + (size_t)row * bf_row, bf_row, &full[s]);
+        bulk_g2s(to + bf_row, static_cast<const char *>(residual) + (size_t)row * res_row, res_row, &full[s]);
+        ++fetched;
+    };
+    if (tid == 0)
+        for (int i = 0; i < depth; ++i) fetch(i);
+    unsigned turn = 0, n_row = 0, lost = 0, s = 0, parity = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, ++n_row) {
+        if (alive && !mbar_wait_bounded(&full[s], parity)) {
+            alive = false;                           // outputs stay wrong; the barriers below still meet
+            lost = n_row;
+            atomicOr(status, kStatusWaitGaveUp);
+        }
+        const char *in = norm_ring + (size_t)s * stage;
+        Raw8<false> yy[NC];
+        Raw8<RES32> res[NC];
+        float f[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = i * (int)blockDim.x + tid;
+            if (c < a.H8) {
+                yy[i] = *reinterpret_cast<const Raw8<false> *>(in + (size_t)c * 16);
+                res[i] = *reinterpret_cast<const Raw8<RES32> *>(in + bf_row + (size_t)c * sizeof(Raw8<RES32>));
+                float v[8];
+                to_floats(yy[i], v);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) f[0] = __fmaf_rn(v[q], v[q], f[0]);
+            }
+        }
+        float g = a.scale;
+        if (a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
+        if (w_post) {
+            block_sum(sums, f, turn);
+            g = __fmul_rn(g, inv_rms(f[0], a));
+        } else {
+            __syncthreads();
+        }
+        if (blockDim.x == 32) __syncwarp();
+        if (tid == 0) fetch(s);                      // all have read the row's place in the ring
+        if (++s == (unsigned)depth) {
+            s = 0;
+            parity ^= 1u;
+        }
+        float v[NC][8];
+        f[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = i * (int)blockDim.x + tid;
+            if (c < a.H8) {
+                float x[8];
+                to_floats(yy[i], v[i]);
+                to_floats(res[i], x);
+                if (w_post) {
+                    Raw8<PAR32> w;
+                    float p[8];
+                    load_param8(w_post, c, w);
+                    to_floats(w, p);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], p[q]);
+                }
+                if (a.channel) {
+                    Raw8<PAR32> w;
+                    float p[8];
+                    load_param8(gate, c, w);
+                    to_floats(w, p);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], p[q]);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    v[i][q] = __fmaf_rn(v[i][q], g, x[q]);
+                    f[0] = __fmaf_rn(v[i][q], v[i][q], f[0]);
+                }
+                if (r_out) store8<RES32>(static_cast<char *>(r_out) + (size_t)t * res_row, c, v[i]);
+            }
+        }
+        if (w_pre) {
+            block_sum(sums, f, turn);
+            const float by = inv_rms(f[0], a);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = i * (int)blockDim.x + tid;
+                if (c < a.H8) {
+                    Raw8<PAR32> w;
+                    float p[8];
+                    load_param8(w_pre, c, w);
+                    to_floats(w, p);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) p[q] = __fmul_rn(__fmul_rn(v[i][q], by), p[q]);
+                    store8<false>(static_cast<char *>(n_out) + (size_t)t * bf_row, c, p);
+                }
+            }
+        }
+    }
+    if (tid == 0 && !alive)                          // no copy outlives the block
+        for (; lost < fetched; ++lost) mbar_wait_bounded(&full[lost % (unsigned)depth], (lost / (unsigned)depth) & 1u);
+}
+
 struct NormPtrs {
     const void *y;
     const int32_t *idx;
@@ -331,6 +486,39 @@ int launch_norm_types(const Dims &d, const moe_norm *n, const NormArgs &a, cudaS
     return par ? launch_norm_nc<SRC, false, true>(d, a, st, p) : launch_norm_nc<SRC, false, false>(d, a, st, p);
 }
 
+// Rows from which the ring pays, for a block's output of its own.
+bool norm_many_rows(const Dims &d) { return d.T >= 8 * 152; }
+
+template <bool RES32, bool PAR32, int NC>
+int launch_norm_rows(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    const auto kernel = norm_rows_kernel<RES32, PAR32, NC>;
+    constexpr int kMaxSmem = 200 * 1024;
+    const int threads = ((a.H8 + NC - 1) / NC + 31) / 32 * 32, row = d.H * (RES32 ? 6 : 4);
+    int per_sm = std::max(1, std::min(16, kNormThreadsPerSM / threads));
+    while (per_sm > 1 && kMaxSmem / per_sm / row < 2) --per_sm;
+    const int depth = std::max(1, std::min(kNormMaxDepth, kMaxSmem / per_sm / row));
+    static PerContext<int> smem_done;
+    if (!set_smem_once(smem_done, kernel, kMaxSmem)) return MOE_ERR_CUDA;
+    unsigned *status = device_status_word();
+    if (status == nullptr) return MOE_ERR_CUDA;
+    const int grid = persistent_grid(d.T, sm_count() * per_sm, d.max_blocks);
+    return launch_pdl_smem(kernel, grid, threads, (size_t)depth * row, st, a, p.y, p.residual, p.w_post, p.w_pre, p.gate, p.r,
+                           p.n, depth, status) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+template <bool RES32, bool PAR32>
+int launch_norm_rows_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    if (a.H8 <= 256) return launch_norm_rows<RES32, PAR32, 1>(d, a, st, p);
+    if (a.H8 <= 1024) return launch_norm_rows<RES32, PAR32, 2>(d, a, st, p);
+    return launch_norm_rows<RES32, PAR32, 4>(d, a, st, p);
+}
+int launch_norm_rows_types(const Dims &d, const moe_norm *n, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    const bool res = n->residual_type == MOE_VALUE_F32, par = n->param_type == MOE_VALUE_F32;
+    if (res) return par ? launch_norm_rows_nc<true, true>(d, a, st, p) : launch_norm_rows_nc<true, false>(d, a, st, p);
+    return par ? launch_norm_rows_nc<false, true>(d, a, st, p) : launch_norm_rows_nc<false, false>(d, a, st, p);
+}
+
 int check_norm(const Dims &d, const moe_norm *n, NormArgs *a) {
     if (n == nullptr) return MOE_ERR_INVALID_ARG;
     if (n->branch_gate < MOE_BRANCH_PLAIN || n->branch_gate > MOE_BRANCH_TOKEN) return MOE_ERR_INVALID_ARG;
@@ -365,8 +553,6 @@ int check_forward(const moe_norm *n, bool has_y, const NormPtrs &p) {
 
 // ---- gradient -----------------------------------------------------------------
 
-constexpr int kBwdMaxDepth = 4;                    // rows on their way or at hand
-
 struct NormBwdPtrs {
     const void *y, *r, *d_r, *d_n, *w_post, *w_pre, *gate;
     void *d_y, *d_residual;
@@ -376,13 +562,14 @@ struct NormBwdPtrs {
 
 // A block takes the rows of one part (rows p, p + parts, ...) at a time and keeps that part's column
 // sums in registers: NC chunks of 8 columns to a thread. The rows of y, r, d_r and d_n come by
-// bulk copies into a ring, `depth` rows deep, so that loads run on while a row's two sums meet.
+// bulk copies into a ring, `depth` rows deep, so that loads run on while a row's two sums meet; they are
+// read there again for each of the three passes over a row, which leaves registers for twice the threads.
 template <bool RES32, bool PAR32, int NC>
-__global__ void __launch_bounds__(NC == 1 ? 1024 : 512)
+__global__ void __launch_bounds__(NC == 1 ? 256 : 512)
 norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
     extern __shared__ __align__(128) char bwd_ring[];
-    __shared__ __align__(8) uint64_t full[kBwdMaxDepth];
-    __shared__ BlockSum<3> sums3;
+    __shared__ __align__(8) uint64_t full[kNormMaxDepth];
+    __shared__ BlockSum4 sums4;
     __shared__ BlockSum<1> sums1;
     const int tid = threadIdx.x;
     const unsigned bf_row = (unsigned)a.H8 * 16u, res_row = RES32 ? 2u * bf_row : bf_row;
@@ -400,9 +587,8 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
     int f_part = blockIdx.x, f_row = blockIdx.x;
     unsigned fetched = 0;
     bool alive = true;
-    const auto fetch = [&]() {                       // thread 0
+    const auto fetch = [&](unsigned s) {             // thread 0
         if (f_part >= parts || !alive) return;
-        const unsigned s = fetched % (unsigned)depth;
         char *to = bwd_ring + (size_t)s * stage;
         mbar_expect_tx(&full[s], stage);
         if (y_bytes) bulk_g2s(to, static_cast<const char *>(p.y) + (size_t)f_row * bf_row, y_bytes, &full[s]);
@@ -417,9 +603,23 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
         }
     };
     if (tid == 0)
-        for (int i = 0; i < depth; ++i) fetch();
+        for (int i = 0; i < depth; ++i) fetch(i);
 
-    unsigned turn3 = 0, turn1 = 0, n_row = 0, n_lost = 0;
+    // the vectors that every row uses, where registers hold them
+    constexpr bool kHold = !PAR32 && NC <= 2;
+    Raw8<PAR32> hold[kHold ? 3 : 1][kHold ? NC : 1];
+    if constexpr (kHold) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = i * (int)blockDim.x + tid;
+            if (c < a.H8) {
+                if (p.w_pre) load_param8(p.w_pre, c, hold[0][i]);
+                if (p.w_post) load_param8(p.w_post, c, hold[1][i]);
+                if (a.channel) load_param8(p.gate, c, hold[2][i]);
+            }
+        }
+    }
+    unsigned turn3 = 0, turn1 = 0, n_row = 0, lost = 0, s = 0, parity = 0;
     for (int part = blockIdx.x; part < parts; part += gridDim.x) {
         float sum_pre[NC][8], sum_post[NC][8];
 #pragma unroll
@@ -427,67 +627,76 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) sum_pre[i][q] = sum_post[i][q] = 0.0f;
         for (int t = part; t < a.T; t += parts, ++n_row) {
-            const unsigned s = n_row % (unsigned)depth;
-            if (alive && !mbar_wait_bounded(&full[s], (n_row / (unsigned)depth) & 1u)) {
+            if (alive && !mbar_wait_bounded(&full[s], parity)) {
                 alive = false;                       // outputs stay wrong; the barriers below still meet
-                n_lost = n_row;
+                lost = n_row;
                 atomicOr(p.status, kStatusWaitGaveUp);
             }
             const char *in = bwd_ring + (size_t)s * stage;
-            Raw8<false> y[NC], dn[NC];
-            Raw8<RES32> r[NC], dr[NC];
-            float v[NC][8], f[3] = {0.0f, 0.0f, 0.0f};
+            const auto y_of = [&](int c, float (&f)[8]) {
+                to_floats(*reinterpret_cast<const Raw8<false> *>(in + (size_t)c * 16), f);
+            };
+            const auto r_of = [&](int c, float (&f)[8]) {
+                to_floats(*reinterpret_cast<const Raw8<RES32> *>(in + at_r + (size_t)c * sizeof(Raw8<RES32>)), f);
+            };
+            const auto dn_of = [&](int c, float (&f)[8]) {
+                to_floats(*reinterpret_cast<const Raw8<false> *>(in + at_dn + (size_t)c * 16), f);
+            };
+            const auto times = [&](const void *w, int which, int i, int c, float (&f)[8]) {
+                Raw8<PAR32> raw;
+                float wf[8];
+                if constexpr (kHold) raw = hold[which][i];
+                else load_param8(w, c, raw);
+                to_floats(raw, wf);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) f[q] = __fmul_rn(f[q], wf[q]);
+            };
+            float v[NC][8], f[4] = {0.0f, 0.0f, 0.0f, 0.0f};                         // v: w_pre d_n, then w_post g D
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = i * (int)blockDim.x + tid;
                 if (c < a.H8) {
                     float x[8];
-                    if (y_bytes) {
-                        y[i] = *reinterpret_cast<const Raw8<false> *>(in + (size_t)c * 16);
-                        to_floats(y[i], x);
+                    if (p.w_post) {
+                        y_of(c, x);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) f[2] = __fmaf_rn(x[q], x[q], f[2]);
                     }
-                    if (dr_bytes) dr[i] = *reinterpret_cast<const Raw8<RES32> *>(in + at_dr + (size_t)c * sizeof(Raw8<RES32>));
                     if (r_bytes) {
-                        r[i] = *reinterpret_cast<const Raw8<RES32> *>(in + at_r + (size_t)c * sizeof(Raw8<RES32>));
-                        dn[i] = *reinterpret_cast<const Raw8<false> *>(in + at_dn + (size_t)c * 16);
-                        Raw8<PAR32> w;
-                        load_param8(p.w_pre, c, w);
-                        float wf[8];
-                        to_floats(w, wf);
-                        to_floats(dn[i], v[i]);
-                        to_floats(r[i], x);
+                        dn_of(c, v[i]);
+                        times(p.w_pre, 0, i, c, v[i]);
+                        r_of(c, x);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            v[i][q] = __fmul_rn(v[i][q], wf[q]);
                             f[0] = __fmaf_rn(x[q], x[q], f[0]);
                             f[1] = __fmaf_rn(x[q], v[i][q], f[1]);
                         }
                     }
                 }
             }
-            block_sum(sums3, f, turn3);
+            block_sum4(sums4, f, turn3);
             if (blockDim.x == 32) __syncwarp();
-            if (tid == 0) fetch();                   // all have read the row's place in the ring
+            // all are done with the row before this one
+            if (tid == 0 && n_row > 0 && depth > 1) fetch(s == 0 ? depth - 1 : s - 1);
 
             const float rs = inv_rms(f[0], a), ys = p.w_post ? inv_rms(f[2], a) : 1.0f;
             const float mean = __fmul_rn(__fmul_rn(f[1], rs), a.inv_h);         // of r^ w_pre d_n
-            const float g = a.token ? __ldg(static_cast<const float *>(p.gate) + t) : 1.0f;
+            const float g = a.token ? __ldg(static_cast<const float *>(p.gate) + t) : 1.0f, gy = __fmul_rn(g, ys);
             float e[1] = {0.0f};
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = i * (int)blockDim.x + tid;
                 if (c < a.H8) {
                     float D[8], x[8];
-                    if (dr_bytes) to_floats(dr[i], D);
+                    if (dr_bytes)
+                        to_floats(*reinterpret_cast<const Raw8<RES32> *>(in + at_dr + (size_t)c * sizeof(Raw8<RES32>)), D);
                     else
 #pragma unroll
                         for (int q = 0; q < 8; ++q) D[q] = 0.0f;
                     if (r_bytes) {
                         float n[8];
-                        to_floats(r[i], x);
-                        to_floats(dn[i], n);
+                        r_of(c, x);
+                        dn_of(c, n);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             const float rh = __fmul_rn(x[q], rs);
@@ -497,26 +706,11 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
                     }
                     store8<RES32>(static_cast<char *>(p.d_residual) + (size_t)t * res_row, c, D);
                     if (y_bytes) {
-                        to_floats(y[i], x);
+                        y_of(c, x);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            sum_post[i][q] = __fmaf_rn(__fmul_rn(D[q], g), __fmul_rn(x[q], ys), sum_post[i][q]);
-                        if (a.channel) {
-                            Raw8<PAR32> w;
-                            float wf[8];
-                            load_param8(p.gate, c, w);
-                            to_floats(w, wf);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) D[q] = __fmul_rn(D[q], wf[q]);
-                        }
-                        if (p.w_post) {
-                            Raw8<PAR32> w;
-                            float wf[8];
-                            load_param8(p.w_post, c, w);
-                            to_floats(w, wf);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) D[q] = __fmul_rn(D[q], wf[q]);
-                        }
+                        for (int q = 0; q < 8; ++q) sum_post[i][q] = __fmaf_rn(D[q], __fmul_rn(x[q], gy), sum_post[i][q]);
+                        if (a.channel) times(p.gate, 2, i, c, D);
+                        if (p.w_post) times(p.w_post, 1, i, c, D);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             v[i][q] = D[q];
@@ -530,20 +724,26 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
                 const float by = __fmul_rn(a.scale, g);
                 if (p.d_gate_token && tid == 0) p.d_gate_token[t] = __fmul_rn(__fmul_rn(a.scale, ys), e[0]);
                 const float m = __fmul_rn(__fmul_rn(e[0], ys), a.inv_h);        // of y^ w_post D
+                const float by_y = __fmul_rn(by, ys), less = p.w_post ? __fmul_rn(ys, m) : 0.0f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) {
                     const int c = i * (int)blockDim.x + tid;
                     if (c < a.H8) {
                         float x[8];
-                        to_floats(y[i], x);
+                        y_of(c, x);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float u = p.w_post ? __fmul_rn(ys, __fmaf_rn(-__fmul_rn(x[q], ys), m, v[i][q])) : v[i][q];
-                            x[q] = __fmul_rn(u, by);
-                        }
+                        for (int q = 0; q < 8; ++q) x[q] = __fmul_rn(__fmaf_rn(-x[q], less, v[i][q]), by_y);
                         store8<false>(static_cast<char *>(p.d_y) + (size_t)t * bf_row, c, x);
                     }
                 }
+            }
+            if (depth == 1) {                        // a row of its own at a time
+                __syncthreads();
+                if (tid == 0) fetch(0);
+            }
+            if (++s == (unsigned)depth) {
+                s = 0;
+                parity ^= 1u;
             }
         }
         float *to = p.part + (size_t)part * 16 * a.H8;                          // [part][pre, post][H]
@@ -557,43 +757,50 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
         }
     }
     if (tid == 0 && !alive)                          // no copy outlives the block
-        for (unsigned i = n_lost; i < fetched; ++i) mbar_wait_bounded(&full[i % (unsigned)depth], (i / (unsigned)depth) & 1u);
+        for (; lost < fetched; ++lost) mbar_wait_bounded(&full[lost % (unsigned)depth], (lost / (unsigned)depth) & 1u);
 }
 
-// The parts' column sums into the gradients of the norms' weights and of a gate for each channel.
-// A block takes 32 columns of one of the two sums, 32 warps the parts in turn, joined in order.
+// The parts' column sums into the gradients of the norms' weights and of a gate for each channel. A block
+// takes 128 columns of one of the two sums, four to a lane, 32 warps the parts in turn, joined in order.
 template <bool PAR32>
 __global__ void __launch_bounds__(1024)
-norm_columns_kernel(NormArgs a, const float *__restrict__ part, int parts, const void *__restrict__ w_post,
+norm_columns_kernel(NormArgs a, const float *part, int parts, const void *__restrict__ w_post,
                     const void *__restrict__ gate, float *__restrict__ d_w_post, float *__restrict__ d_w_pre,
                     float *__restrict__ d_gate) {
-    __shared__ float sums[32][33];
+    __shared__ float4 sums[32][32];
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H = a.H8 * 8;
     const bool post = blockIdx.y != 0;
     if (post ? !d_w_post && !d_gate : !d_w_pre) return;
-    const int h = blockIdx.x * 32 + lane;
-    float s = 0.0f;
-    if (h < H) {
-        const float *from = part + (post ? H : 0) + h;
+    const int h4 = blockIdx.x * 128 + 4 * lane;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (h4 < H) {
+        const float *from = part + (post ? H : 0) + h4;
 #pragma unroll 8
-        for (int i = warp; i < parts; i += 32) s += from[(size_t)i * 2 * H];
+        for (int i = warp; i < parts; i += 32) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + (size_t)i * 2 * H));
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
     }
     sums[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && h < H) {
-        s = 0.0f;
+    const int h = blockIdx.x * 128 + (int)threadIdx.x;
+    if (threadIdx.x < 128 && h < H) {
+        float v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s += sums[i][lane];
+        for (int i = 0; i < 32; ++i) v += reinterpret_cast<const float *>(&sums[i][0])[threadIdx.x];
         if (!post) {
-            d_w_pre[h] = s;
+            d_w_pre[h] = v;
         } else {
             const auto at = [&](const void *p) {
                 return PAR32 ? static_cast<const float *>(p)[h] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[h]);
             };
-            s = __fmul_rn(s, a.scale);
-            if (d_w_post) d_w_post[h] = a.channel ? __fmul_rn(s, at(gate)) : s;
-            if (d_gate) d_gate[h] = w_post ? __fmul_rn(s, at(w_post)) : s;
+            v = __fmul_rn(v, a.scale);
+            if (d_w_post) d_w_post[h] = a.channel ? __fmul_rn(v, at(gate)) : v;
+            if (d_gate) d_gate[h] = w_post ? __fmul_rn(v, at(w_post)) : v;
         }
     }
 }
@@ -610,7 +817,7 @@ int launch_columns(const Dims &d, const NormArgs &a, cudaStream_t st, const floa
                    const void *gate, float *d_w_post, float *d_w_pre, float *d_gate) {
     if (!d_w_post && !d_w_pre && !d_gate) return MOE_OK;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((d.H + 31) / 32), 2);
+    cfg.gridDim = dim3((unsigned)((d.H + 127) / 128), 2);
     cfg.blockDim = dim3(1024);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -633,7 +840,7 @@ int launch_backward_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const 
     const int parts = norm_parts(d.T, d.H);
     constexpr int kMaxSmem = 200 * 1024;
     const int blocks_per_sm = std::max(1, std::min(8, 8192 / d.H));
-    const int depth = std::max(1, std::min(kBwdMaxDepth, kMaxSmem / blocks_per_sm / row));
+    const int depth = std::max(1, std::min(kNormMaxDepth, kMaxSmem / blocks_per_sm / row));
     static PerContext<int> smem_done;
     if (!set_smem_once(smem_done, kernel, kMaxSmem)) return MOE_ERR_CUDA;
     const size_t smem = (size_t)depth * row;
@@ -665,6 +872,7 @@ extern "C" int moe_block_norm(const moe_problem *p, const moe_norm *norm, const 
     rc = check_forward(norm, y != nullptr, ptrs);
     if (rc != MOE_OK) return rc;
     if (y == nullptr) return launch_norm_types<kNoBlock>(d, norm, a, as_stream(stream), ptrs);
+    if (norm_many_rows(d)) return launch_norm_rows_types(d, norm, a, as_stream(stream), ptrs);
     return launch_norm_types<kRows>(d, norm, a, as_stream(stream), ptrs);
 }
 
