@@ -17,6 +17,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_internal.cuh"
 
@@ -26,6 +27,7 @@ namespace {
 constexpr int kNormMaxHidden = 16384;
 constexpr int kNormMaxDepth = 4;                   // rows on their way or at hand in a ring
 constexpr int kNormThreadsPerSM = 1024;
+constexpr int kCombineSlots = 16, kCombineSmem = 160 * 1024;       // experts' rows in a ring
 
 struct NormArgs {
     int T, H8, k, C;                   // H8 chunks of 8 elements to a row
@@ -61,10 +63,6 @@ __device__ __forceinline__ void to_floats(const Raw8<true> &v, float (&f)[8]) {
 __device__ __forceinline__ void load_row8(const void *row, int c, Raw8<false> &v) {
     v.a = ld_stream_v4(static_cast<const uint4 *>(row) + c);
 }
-__device__ __forceinline__ void load_row8(const void *row, int c, Raw8<true> &v) {
-    v.a = ld_stream_v4(static_cast<const uint4 *>(row) + 2 * c);
-    v.b = ld_stream_v4(static_cast<const uint4 *>(row) + 2 * c + 1);
-}
 // The residual's: the same memory may be written as r, by the thread that read it.
 __device__ __forceinline__ uint4 ld_once_v4(const uint4 *p) {
     uint4 r;
@@ -89,6 +87,19 @@ __device__ __forceinline__ void load_param8(const void *p, int c, Raw8<true> &v)
     v.a = __ldg(static_cast<const uint4 *>(p) + 2 * c);
     v.b = __ldg(static_cast<const uint4 *>(p) + 2 * c + 1);
 }
+// The same where it is not to stay in registers from row to row: volatile.
+__device__ __forceinline__ uint4 ld_again_v4(const uint4 *p) {
+    uint4 r;
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ void load_param8_again(const void *p, int c, Raw8<false> &v) {
+    v.a = ld_again_v4(static_cast<const uint4 *>(p) + c);
+}
+__device__ __forceinline__ void load_param8_again(const void *p, int c, Raw8<true> &v) {
+    v.a = ld_again_v4(static_cast<const uint4 *>(p) + 2 * c);
+    v.b = ld_again_v4(static_cast<const uint4 *>(p) + 2 * c + 1);
+}
 template <bool F32>
 __device__ __forceinline__ void store8(void *row, int c, const float (&f)[8]) {
     if constexpr (F32) {
@@ -108,9 +119,10 @@ template <int N>
 struct BlockSum {
     float part[2][N][32];
 };
+// `threads`: the block's first ones, whole warps, which alone come here.
 template <int N>
-__device__ __forceinline__ void block_sum(BlockSum<N> &s, float (&v)[N], unsigned &turn) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__device__ __forceinline__ void block_sum(BlockSum<N> &s, float (&v)[N], unsigned &turn, int threads) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = threads >> 5;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -122,7 +134,7 @@ __device__ __forceinline__ void block_sum(BlockSum<N> &s, float (&v)[N], unsigne
 #pragma unroll
         for (int i = 0; i < N; ++i) s.part[b][i][warp] = v[i];
     }
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         v[i] = lane < warps ? s.part[b][i][lane] : 0.0f;
@@ -165,164 +177,337 @@ __device__ __forceinline__ float inv_rms(float sum_sq, const NormArgs &a) {
     return __frsqrt_rn(__fmaf_rn(sum_sq, a.inv_h, a.eps));
 }
 
-// Where the block's output comes from: no block at all, its rows, or KMAX gathers at a time
-// of the experts' rows.
-constexpr int kNoBlock = 0, kRows = -1;
+// From the block's output v, of which a thread has NC chunks of 8 elements in registers, and the residual to r and n. g: the
+// scale and a token's gate. param(k, c): chunk c of w_post (k = 0), of the gate for each channel (1) or of w_pre (2).
+template <bool HAS_Y, bool RES32, int NC, typename Param>
+__device__ __forceinline__ void finish_row(const NormArgs &a, int t, float g, float (&v)[NC][8], const Raw8<RES32> (&res)[NC],
+                                           bool w_post, bool w_pre, Param param, void *r_out, void *n_out, BlockSum<1> &sums,
+                                           unsigned &turn, int threads) {
+    const size_t res_row = (size_t)a.H8 * (RES32 ? 32 : 16), bf_row = (size_t)a.H8 * 16;
+    const auto times = [&](int k, int c, float (&f)[8]) {
+        float p[8];
+        to_floats(param(k, c), p);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] = __fmul_rn(f[q], p[q]);
+    };
+    float f[1] = {0.0f};
+    if (HAS_Y && w_post) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            if (i * threads + (int)threadIdx.x < a.H8)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) f[0] = __fmaf_rn(v[i][q], v[i][q], f[0]);
+        block_sum(sums, f, turn, threads);
+        g = __fmul_rn(g, inv_rms(f[0], a));
+    }
+    f[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = i * threads + (int)threadIdx.x;
+        if (c < a.H8) {
+            float x[8];
+            to_floats(res[i], x);
+            if constexpr (HAS_Y) {
+                if (w_post) times(0, c, v[i]);
+                if (a.channel) times(1, c, v[i]);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(v[i][q], g, x[q]);
+            }
+            if (r_out) store8<RES32>(static_cast<char *>(r_out) + t * res_row, c, x);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                f[0] = __fmaf_rn(x[q], x[q], f[0]);
+                v[i][q] = x[q];
+            }
+        }
+    }
+    if (!w_pre) return;
+    block_sum(sums, f, turn, threads);
+    const float s = inv_rms(f[0], a);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        const int c = i * threads + (int)threadIdx.x;
+        if (c < a.H8) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], s);
+            times(2, c, v[i]);
+            store8<false>(static_cast<char *>(n_out) + t * bf_row, c, v[i]);
+        }
+    }
+}
 
-// A block of at most MAXT threads takes a row at a time, NC chunks of 8 elements to a thread.
-template <int SRC, bool RES32, bool PAR32, int NC, int MAXT>
-__global__ void __launch_bounds__(MAXT)
-norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__restrict__ topk_idx,
-            const float *__restrict__ topk_w, const int32_t *__restrict__ slot, const void *residual,
-            const void *__restrict__ w_post, const void *__restrict__ w_pre, const void *__restrict__ gate, void *out,
-            void *r_out, void *n_out) {
+// moe_block_norm for few rows: a block takes a row at a time, NC chunks of 8 elements to a thread, straight into
+// registers; has_y: there is a block before the norm.
+template <bool HAS_Y, bool RES32, bool PAR32, int NC>
+__global__ void __launch_bounds__(1024)
+norm_kernel(NormArgs a, const void *__restrict__ y, const void *residual, const void *__restrict__ w_post,
+            const void *__restrict__ w_pre, const void *__restrict__ gate, void *r_out, void *n_out) {
+    // one chunk to a thread: the vectors come along with the first row, and stay
+    constexpr bool kHold = NC == 1;
     __shared__ BlockSum<1> sums;
     pdl_enter();
-    const int lane = threadIdx.x & 31;
     unsigned turn = 0;
     const size_t res_row = (size_t)a.H8 * (RES32 ? 32 : 16), bf_row = (size_t)a.H8 * 16;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
         int c[NC];
         Raw8<RES32> res[NC];
         Raw8<false> yy[NC];
+        Raw8<PAR32> p_post, p_pre, p_gate;
         float v[NC][8];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             c[i] = i * (int)blockDim.x + (int)threadIdx.x;
-            if (c[i] < a.H8) load_residual8(static_cast<const char *>(residual) + t * res_row, c[i], res[i]);
-        }
-        if constexpr (SRC == kRows) {
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (c[i] < a.H8) load_row8(static_cast<const char *>(y) + t * bf_row, c[i], yy[i]);
-        }
-        // one row at a time is latency: the vectors come along with it
-        Raw8<PAR32> p_post[NC], p_pre[NC], p_gate[NC];
-        const auto params = [&](bool early) {
-            if (early != (NC == 1)) return;
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                if (c[i] < a.H8) {
-                    if (SRC != kNoBlock && w_post) load_param8(w_post, c[i], p_post[i]);
-                    if (SRC != kNoBlock && a.channel) load_param8(gate, c[i], p_gate[i]);
-                    if (w_pre) load_param8(w_pre, c[i], p_pre[i]);
-                }
+            if (c[i] < a.H8) {
+                load_residual8(static_cast<const char *>(residual) + t * res_row, c[i], res[i]);
+                if (HAS_Y) load_row8(static_cast<const char *>(y) + t * bf_row, c[i], yy[i]);
             }
-        };
-        params(true);
+        }
+        if constexpr (kHold) {
+            if (c[0] < a.H8) {
+                if (HAS_Y && w_post) load_param8(w_post, c[0], p_post);
+                if (HAS_Y && a.channel) load_param8(gate, c[0], p_gate);
+                if (w_pre) load_param8(w_pre, c[0], p_pre);
+            }
+        }
         float g = a.scale;
-        if (SRC != kNoBlock && a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
-
-        if constexpr (SRC > 0) {
-            float w = 0.0f;
-            int row = -1;
-            if (lane < a.k) {
-                const int s = __ldg(slot + (size_t)t * a.k + lane);
-                const int e = __ldg(topk_idx + (size_t)t * a.k + lane);
-                w = __ldg(topk_w + (size_t)t * a.k + lane);
-                if (s >= 0) row = e * a.C + s;
-            }
-            unsigned rem = __ballot_sync(kFull, row >= 0);
-            int left = __popc(rem);
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
-            while (left > 0) {                                         // once, or twice past 8 choices
-                Raw8<false> in[SRC][NC];
-                float wj[SRC];
-#pragma unroll
-                for (int j = 0; j < SRC; ++j) {
-                    if (j < left) {                                    // warp-uniform
-                        const int src = __ffs(rem) - 1;
-                        rem &= rem - 1;
-                        const size_t at = (size_t)__shfl_sync(kFull, row, src) * bf_row;
-                        wj[j] = __shfl_sync(kFull, w, src);
-#pragma unroll
-                        for (int i = 0; i < NC; ++i)
-                            if (c[i] < a.H8) load_row8(static_cast<const char *>(y) + at, c[i], in[j][i]);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < SRC; ++j) {
-                    if (j < left) {
-#pragma unroll
-                        for (int i = 0; i < NC; ++i) {
-                            float f[8];
-                            to_floats(in[j][i], f);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) v[i][q] = __fmaf_rn(wj[j], f[q], v[i][q]);
-                        }
-                    }
-                }
-                left -= SRC;
-            }
-            if (out != nullptr) {
-#pragma unroll
-                for (int i = 0; i < NC; ++i)
-                    if (c[i] < a.H8) store8<false>(static_cast<char *>(out) + t * bf_row, c[i], v[i]);
-            }
-        } else if constexpr (SRC == kRows) {
+        if (HAS_Y && a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
+        if constexpr (HAS_Y) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) to_floats(yy[i], v[i]);
         }
+        const auto param = [&](int k, int ch) {
+            if constexpr (kHold) {
+                return k == 0 ? p_post : k == 1 ? p_gate : p_pre;
+            } else {
+                Raw8<PAR32> raw;
+                load_param8_again(k == 0 ? w_post : k == 1 ? gate : w_pre, ch, raw);
+                return raw;
+            }
+        };
+        finish_row<HAS_Y, RES32, NC>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, (int)blockDim.x);
+    }
+}
 
-        float f[1];
-        if (SRC != kNoBlock && w_post) {
-            f[0] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (c[i] < a.H8)
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) f[0] = __fmaf_rn(v[i][q], v[i][q], f[0]);
-            block_sum(sums, f, turn);
-            g = __fmul_rn(g, inv_rms(f[0], a));
-        }
-        params(false);
-        f[0] = 0.0f;
+// The kept choices of a token, in order.
+struct Choices {
+    int n;
+    float w[kMaxTopK];
+    size_t at[kMaxTopK];                             // bytes from y to the row
+};
+// Lane j < k of one warp: choice j of a token; none past the last token.
+struct Choice {
+    int s, e;
+    float w;
+};
+__device__ __forceinline__ Choice load_choice(const NormArgs &a, const int32_t *topk_idx, const float *topk_w, const int32_t *slot,
+                                              long long t) {
+    const int lane = threadIdx.x & 31;
+    Choice c = {-1, 0, 0.0f};
+    if (lane < a.k && t < a.T) {
+        c.s = __ldg(slot + t * a.k + lane);
+        c.e = __ldg(topk_idx + t * a.k + lane);
+        c.w = __ldg(topk_w + t * a.k + lane);
+    }
+    return c;
+}
+__device__ __forceinline__ void put_choices(const NormArgs &a, const Choice &c, Choices &to) {
+    const int lane = threadIdx.x & 31;
+    const unsigned kept = __ballot_sync(kFull, c.s >= 0);
+    if (c.s >= 0) {
+        const int j = __popc(kept & ((1u << lane) - 1u));
+        to.w[j] = c.w;
+        to.at[j] = (size_t)(c.e * a.C + c.s) * ((size_t)a.H8 * 16);
+    }
+    if (lane == 0) to.n = __popc(kept);
+}
+
+// moe_combine_norm: the same behind the weighted sum of SRC experts' rows at a time, a token after the other.
+template <int SRC, bool RES32, bool PAR32, int NC, int MAXT>
+__global__ void __launch_bounds__(MAXT)
+combine_norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__restrict__ topk_idx,
+                    const float *__restrict__ topk_w, const int32_t *__restrict__ slot, const void *residual,
+                    const void *__restrict__ w_post, const void *__restrict__ w_pre, const void *__restrict__ gate, void *out,
+                    void *r_out, void *n_out) {
+    __shared__ Choices choices[2];
+    __shared__ BlockSum<1> sums;
+    const size_t res_row = (size_t)a.H8 * (RES32 ? 32 : 16), bf_row = (size_t)a.H8 * 16;
+    pdl_enter();
+    if (threadIdx.x < 32) put_choices(a, load_choice(a, topk_idx, topk_w, slot, blockIdx.x), choices[0]);
+    __syncthreads();
+    unsigned turn = 0, at = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, at ^= 1u) {
+        const Choices &now = choices[at];
+        Raw8<RES32> res[NC];
+        float v[NC][8];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            if (c[i] < a.H8) {
-                float x[8];
-                to_floats(res[i], x);
-                if constexpr (SRC != kNoBlock) {
-                    if (w_post) {
-                        float p[8];
-                        to_floats(p_post[i], p);
+            const int c = i * (int)blockDim.x + (int)threadIdx.x;
+            if (c < a.H8) load_residual8(static_cast<const char *>(residual) + t * res_row, c, res[i]);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], p[q]);
+            for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+        }
+        for (int j0 = 0; j0 < now.n; j0 += SRC) {                      // once, or more past SRC choices
+            Raw8<false> in[SRC][NC];
+#pragma unroll
+            for (int j = 0; j < SRC; ++j)
+                if (j0 + j < now.n)
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        const int c = i * (int)blockDim.x + (int)threadIdx.x;
+                        if (c < a.H8) load_row8(static_cast<const char *>(y) + now.at[j0 + j], c, in[j][i]);
                     }
-                    if (a.channel) {
-                        float p[8];
-                        to_floats(p_gate[i], p);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], p[q]);
+            for (int j = 0; j < SRC; ++j) {
+                if (j0 + j < now.n) {
+                    const float w = now.w[j0 + j];
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        float f[8];
+                        to_floats(in[j][i], f);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[i][q] = __fmaf_rn(w, f[q], v[i][q]);
                     }
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(v[i][q], g, x[q]);
-                }
-                if (r_out) store8<RES32>(static_cast<char *>(r_out) + t * res_row, c[i], x);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    f[0] = __fmaf_rn(x[q], x[q], f[0]);
-                    v[i][q] = x[q];
                 }
             }
         }
-        if (w_pre) {
-            block_sum(sums, f, turn);
-            const float s = inv_rms(f[0], a);
+        // the other buffer was last read before the barriers of the token before
+        if (threadIdx.x < 32) put_choices(a, load_choice(a, topk_idx, topk_w, slot, (long long)t + gridDim.x), choices[at ^ 1u]);
+        float g = a.scale;
+        if (a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
+        if (out != nullptr) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                if (c[i] < a.H8) {
-                    float p[8];
-                    to_floats(p_pre[i], p);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) p[q] = __fmul_rn(__fmul_rn(v[i][q], s), p[q]);
-                    store8<false>(static_cast<char *>(n_out) + t * bf_row, c[i], p);
+                const int c = i * (int)blockDim.x + (int)threadIdx.x;
+                if (c < a.H8) store8<false>(static_cast<char *>(out) + t * bf_row, c, v[i]);
+            }
+        }
+        const auto param = [&](int k, int ch) {
+            Raw8<PAR32> raw;
+            load_param8_again(k == 0 ? w_post : k == 1 ? gate : w_pre, ch, raw);
+            return raw;
+        };
+        finish_row<true, RES32, NC>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, (int)blockDim.x);
+        if ((!w_post && !w_pre) || blockDim.x == 32) __syncthreads();  // the choices' buffers turn behind a barrier
+    }
+}
+
+// The same for many tokens. The block's last warp sees to the tokens' choices and to the experts' rows, which come by bulk
+// copies into a ring of `slots` rows, tokens ahead; the others add each row as it arrives. (Loads to registers a token ahead
+// would fill the SM's load queue, behind which the sums' shared memory accesses then wait.)
+template <bool RES32, bool PAR32, int NC>
+__global__ void __launch_bounds__(544, NC == 4 ? 1 : 2)
+combine_norm_rows_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__restrict__ topk_idx,
+                         const float *__restrict__ topk_w, const int32_t *__restrict__ slot, const void *residual,
+                         const void *__restrict__ w_post, const void *__restrict__ w_pre, const void *__restrict__ gate,
+                         void *out, void *r_out, void *n_out, int slots, unsigned *status) {
+    constexpr int kAhead = 4;                                          // tokens whose choices are at hand
+    extern __shared__ __align__(128) char norm_ring[];
+    __shared__ __align__(8) uint64_t full[kCombineSlots], empty[kCombineSlots], known[kAhead], done[kAhead];
+    __shared__ Choices choices[kAhead];
+    __shared__ BlockSum<1> sums;
+    const int tid = threadIdx.x, threads = (int)blockDim.x - 32, lane = tid & 31;
+    const unsigned bf_row = (unsigned)a.H8 * 16u;
+    const size_t res_row = (size_t)a.H8 * (RES32 ? 32 : 16);
+    if (tid < slots) {
+        mbar_init(&full[tid], 1u);
+        mbar_init(&empty[tid], threads >> 5);
+        fence_mbar_init();
+    }
+    if (tid < kAhead) {
+        mbar_init(&known[tid], 1u);
+        mbar_init(&done[tid], threads >> 5);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_enter();
+    bool alive = true;
+    const auto wait = [&](uint64_t *bar, unsigned use) {               // one warp, all lanes
+        if (alive && !__all_sync(kFull, mbar_wait_bounded(bar, use & 1u))) {
+            alive = false;                           // outputs stay wrong; the barriers below still meet
+            if (lane == 0) atomicOr(status, kStatusWaitGaveUp);
+        }
+    };
+    if (tid >= threads) {
+        unsigned n_token = 0, n_row = 0, s = 0, use = 0;
+        Choice next = load_choice(a, topk_idx, topk_w, slot, blockIdx.x);
+        for (long long t = blockIdx.x; t < a.T; t += gridDim.x, ++n_token) {
+            const unsigned at = n_token % kAhead;
+            if (n_token >= kAhead) wait(&done[at], n_token / kAhead - 1u);
+            const Choice now = next;
+            next = load_choice(a, topk_idx, topk_w, slot, t + gridDim.x);
+            put_choices(a, now, choices[at]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&known[at]);
+            const int n = choices[at].n;
+            for (int j = 0; j < n && alive; ++j, ++n_row) {
+                if (n_row >= (unsigned)slots) wait(&empty[s], use - 1u);
+                if (alive && lane == 0) {
+                    mbar_expect_tx(&full[s], bf_row);
+                    bulk_g2s(norm_ring + (size_t)s * bf_row, static_cast<const char *>(y) + choices[at].at[j], bf_row, &full[s]);
+                }
+                if (++s == (unsigned)slots) {
+                    s = 0;
+                    ++use;
                 }
             }
         }
+        // no copy outlives the block
+        for (unsigned i = n_row > (unsigned)slots ? n_row - slots : 0u; i < n_row; ++i)
+            mbar_wait_bounded(&full[i % (unsigned)slots], (i / (unsigned)slots) & 1u);
+        return;
+    }
+    unsigned turn = 0, s = 0, use = 0, n_token = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, ++n_token) {
+        const unsigned at = n_token % kAhead;
+        Raw8<RES32> res[NC];
+        float v[NC][8];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = i * threads + tid;
+            if (c < a.H8) load_residual8(static_cast<const char *>(residual) + t * res_row, c, res[i]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+        }
+        wait(&known[at], n_token / kAhead);
+        const int n = alive ? choices[at].n : 0;
+        for (int j = 0; j < n; ++j) {
+            const float w = choices[at].w[j];
+            wait(&full[s], use);
+            const char *in = norm_ring + (size_t)s * bf_row;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = i * threads + tid;
+                if (c < a.H8) {
+                    float f[8];
+                    to_floats(*reinterpret_cast<const Raw8<false> *>(in + (size_t)c * 16), f);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[i][q] = __fmaf_rn(w, f[q], v[i][q]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == (unsigned)slots) {
+                s = 0;
+                ++use;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&done[at]);
+        float g = a.scale;
+        if (a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
+        if (out != nullptr) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = i * threads + tid;
+                if (c < a.H8) store8<false>(static_cast<char *>(out) + (size_t)t * bf_row, c, v[i]);
+            }
+        }
+        const auto param = [&](int k, int ch) {
+            Raw8<PAR32> raw;
+            load_param8_again(k == 0 ? w_post : k == 1 ? gate : w_pre, ch, raw);
+            return raw;
+        };
+        finish_row<true, RES32, NC>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, threads);
     }
 }
 
@@ -383,7 +568,7 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
         float g = a.scale;
         if (a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
         if (w_post) {
-            block_sum(sums, f, turn);
+            block_sum(sums, f, turn, (int)blockDim.x);
             g = __fmul_rn(g, inv_rms(f[0], a));
         } else {
             __syncthreads();
@@ -428,7 +613,7 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
             }
         }
         if (w_pre) {
-            block_sum(sums, f, turn);
+            block_sum(sums, f, turn, (int)blockDim.x);
             const float by = inv_rms(f[0], a);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
@@ -458,32 +643,63 @@ struct NormPtrs {
     void *out, *r, *n;
 };
 
-template <int SRC, bool RES32, bool PAR32, int NC, int MAXT>
+template <bool HAS_Y, bool RES32, bool PAR32, int NC>
 int launch_norm(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
     const int threads = ((a.H8 + NC - 1) / NC + 31) / 32 * 32;
     // blocks do not wait on one another: a few more than an SM holds even out its end
     const int grid = persistent_grid(d.T, sm_count() * std::min(32, 2048 / threads), d.max_blocks);
-    return launch_pdl(norm_kernel<SRC, RES32, PAR32, NC, MAXT>, grid, threads, st, a, p.y, p.idx, p.w, p.slot,
-                      p.residual, p.w_post, p.w_pre, p.gate, p.out, p.r, p.n) == cudaSuccess
+    return launch_pdl(norm_kernel<HAS_Y, RES32, PAR32, NC>, grid, threads, st, a, p.y, p.residual, p.w_post, p.w_pre, p.gate,
+                      p.r, p.n) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+template <bool HAS_Y, bool RES32, bool PAR32>
+int launch_norm_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    if (a.H8 <= 1024) return launch_norm<HAS_Y, RES32, PAR32, 1>(d, a, st, p);
+    return launch_norm<HAS_Y, RES32, PAR32, 2>(d, a, st, p);
+}
+template <int SRC, bool RES32, bool PAR32, int NC, int MAXT>
+int launch_combine_norm(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    const int threads = ((a.H8 + NC - 1) / NC + 31) / 32 * 32;
+    const int grid = persistent_grid(d.T, sm_count() * std::min(32, 2048 / threads), d.max_blocks);
+    return launch_pdl(combine_norm_kernel<SRC, RES32, PAR32, NC, MAXT>, grid, threads, st, a, p.y, p.idx, p.w, p.slot, p.residual,
+                      p.w_post, p.w_pre, p.gate, p.out, p.r, p.n) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
 template <int SRC, bool RES32, bool PAR32>
-int launch_norm_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
-    if constexpr (SRC <= 0) {
-        if (a.H8 <= 1024) return launch_norm<SRC, RES32, PAR32, 1, 1024>(d, a, st, p);
-        return launch_norm<SRC, RES32, PAR32, 2, 1024>(d, a, st, p);
-    } else {
-        if (a.H8 <= 256) return launch_norm<SRC, RES32, PAR32, 1, 256>(d, a, st, p);
-        if (a.H8 <= 1024) return launch_norm<SRC, RES32, PAR32, 2, 512>(d, a, st, p);
-        return launch_norm<(SRC < 4 ? SRC : 4), RES32, PAR32, 4, 512>(d, a, st, p);
-    }
+int launch_combine_norm_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    if (a.H8 <= 512) return launch_combine_norm<SRC, RES32, PAR32, 1, 512>(d, a, st, p);
+    if (a.H8 <= 1024) return launch_combine_norm<SRC, RES32, PAR32, 1, 1024>(d, a, st, p);
+    return launch_combine_norm<(SRC < 4 ? SRC : 4), RES32, PAR32, 4, 512>(d, a, st, p);
 }
-template <int SRC>
-int launch_norm_types(const Dims &d, const moe_norm *n, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
-    const bool res = n->residual_type == MOE_VALUE_F32, par = n->param_type == MOE_VALUE_F32;
-    if (res) return par ? launch_norm_nc<SRC, true, true>(d, a, st, p) : launch_norm_nc<SRC, true, false>(d, a, st, p);
-    return par ? launch_norm_nc<SRC, false, true>(d, a, st, p) : launch_norm_nc<SRC, false, false>(d, a, st, p);
+template <bool RES32, bool PAR32, int NC>
+int launch_combine_norm_rows(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    const auto kernel = combine_norm_rows_kernel<RES32, PAR32, NC>;
+    const int threads = ((a.H8 + NC - 1) / NC + 31) / 32 * 32 + 32, row = d.H * 2;
+    int per_sm = std::max(1, std::min(16, 1088 / threads));
+    while (per_sm > 1 && kCombineSmem / per_sm / row < 4) --per_sm;
+    const int slots = std::min(kCombineSlots, kCombineSmem / per_sm / row);
+    static PerContext<int> smem_done;
+    if (!set_smem_once(smem_done, kernel, kCombineSmem)) return MOE_ERR_CUDA;
+    unsigned *status = device_status_word();
+    if (status == nullptr) return MOE_ERR_CUDA;
+    const int grid = persistent_grid(d.T, sm_count() * per_sm, d.max_blocks);
+    return launch_pdl_smem(kernel, grid, threads, (size_t)slots * row, st, a, p.y, p.idx, p.w, p.slot, p.residual, p.w_post,
+                           p.w_pre, p.gate, p.out, p.r, p.n, slots, status) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+template <bool RES32, bool PAR32>
+int launch_combine_norm_k(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+    if (d.T >= 2 * 152) {                            // several tokens to a block
+        if (a.H8 <= 256) return launch_combine_norm_rows<RES32, PAR32, 1>(d, a, st, p);
+        if (a.H8 <= 1024) return launch_combine_norm_rows<RES32, PAR32, 2>(d, a, st, p);
+        return launch_combine_norm_rows<RES32, PAR32, 4>(d, a, st, p);
+    }
+    if (d.k <= 2) return launch_combine_norm_nc<2, RES32, PAR32>(d, a, st, p);
+    if (d.k <= 4) return launch_combine_norm_nc<4, RES32, PAR32>(d, a, st, p);
+    return launch_combine_norm_nc<8, RES32, PAR32>(d, a, st, p);
 }
 
 // Rows from which the ring pays, for a block's output of its own.
@@ -513,10 +729,14 @@ int launch_norm_rows_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const
     if (a.H8 <= 1024) return launch_norm_rows<RES32, PAR32, 2>(d, a, st, p);
     return launch_norm_rows<RES32, PAR32, 4>(d, a, st, p);
 }
-int launch_norm_rows_types(const Dims &d, const moe_norm *n, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
+// By the types that the call names: f(residual fp32, parameters fp32).
+template <typename F>
+int by_types(const moe_norm *n, F f) {
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
     const bool res = n->residual_type == MOE_VALUE_F32, par = n->param_type == MOE_VALUE_F32;
-    if (res) return par ? launch_norm_rows_nc<true, true>(d, a, st, p) : launch_norm_rows_nc<true, false>(d, a, st, p);
-    return par ? launch_norm_rows_nc<false, true>(d, a, st, p) : launch_norm_rows_nc<false, false>(d, a, st, p);
+    if (res) return par ? f(yes, yes) : f(yes, no);
+    return par ? f(no, yes) : f(no, no);
 }
 
 int check_norm(const Dims &d, const moe_norm *n, NormArgs *a) {
@@ -720,7 +940,7 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
                 }
             }
             if (y_bytes) {
-                if (p.w_post || p.d_gate_token) block_sum(sums1, e, turn1);
+                if (p.w_post || p.d_gate_token) block_sum(sums1, e, turn1, (int)blockDim.x);
                 const float by = __fmul_rn(a.scale, g);
                 if (p.d_gate_token && tid == 0) p.d_gate_token[t] = __fmul_rn(__fmul_rn(a.scale, ys), e[0]);
                 const float m = __fmul_rn(__fmul_rn(e[0], ys), a.inv_h);        // of y^ w_post D
@@ -871,9 +1091,13 @@ extern "C" int moe_block_norm(const moe_problem *p, const moe_norm *norm, const 
     const NormPtrs ptrs = {y, nullptr, nullptr, nullptr, residual, w_post, w_pre, gate, nullptr, r, n};
     rc = check_forward(norm, y != nullptr, ptrs);
     if (rc != MOE_OK) return rc;
-    if (y == nullptr) return launch_norm_types<kNoBlock>(d, norm, a, as_stream(stream), ptrs);
-    if (norm_many_rows(d)) return launch_norm_rows_types(d, norm, a, as_stream(stream), ptrs);
-    return launch_norm_types<kRows>(d, norm, a, as_stream(stream), ptrs);
+    cudaStream_t st = as_stream(stream);
+    return by_types(norm, [&](auto res, auto par) {
+        constexpr bool kRes = decltype(res)::value, kPar = decltype(par)::value;
+        if (y == nullptr) return launch_norm_nc<false, kRes, kPar>(d, a, st, ptrs);
+        if (norm_many_rows(d)) return launch_norm_rows_nc<kRes, kPar>(d, a, st, ptrs);
+        return launch_norm_nc<true, kRes, kPar>(d, a, st, ptrs);
+    });
 }
 
 extern "C" int moe_combine_norm(const moe_problem *p, const moe_norm *norm, const void *y, const int32_t *topk_idx,
@@ -892,9 +1116,9 @@ extern "C" int moe_combine_norm(const moe_problem *p, const moe_norm *norm, cons
     rc = check_forward(norm, true, ptrs);
     if (rc != MOE_OK) return rc;
     cudaStream_t st = as_stream(stream);
-    if (d.k <= 2) return launch_norm_types<2>(d, norm, a, st, ptrs);
-    if (d.k <= 4) return launch_norm_types<4>(d, norm, a, st, ptrs);
-    return launch_norm_types<8>(d, norm, a, st, ptrs);
+    return by_types(norm, [&](auto res, auto par) {
+        return launch_combine_norm_k<decltype(res)::value, decltype(par)::value>(d, a, st, ptrs);
+    });
 }
 
 extern "C" size_t moe_block_norm_backward_workspace_bytes(const moe_problem *p, const moe_norm *norm) {
@@ -936,9 +1160,7 @@ extern "C" int moe_block_norm_backward(const moe_problem *p, const moe_norm *nor
     if (b.status == nullptr) return MOE_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
     if (a.token) d_gate = nullptr;                                     // a token's comes from its row
-    const bool res = norm->residual_type == MOE_VALUE_F32, par = norm->param_type == MOE_VALUE_F32;
-    if (res) return par ? launch_norm_backward<true, true>(d, a, st, b, d_w_post, d_w_pre, d_gate)
-                        : launch_norm_backward<true, false>(d, a, st, b, d_w_post, d_w_pre, d_gate);
-    return par ? launch_norm_backward<false, true>(d, a, st, b, d_w_post, d_w_pre, d_gate)
-               : launch_norm_backward<false, false>(d, a, st, b, d_w_post, d_w_pre, d_gate);
+    return by_types(norm, [&](auto res, auto par) {
+        return launch_norm_backward<decltype(res)::value, decltype(par)::value>(d, a, st, b, d_w_post, d_w_pre, d_gate);
+    });
 }
