@@ -546,32 +546,28 @@ def run_path(p: moe_problem, x, logits, s, bufs: dict, out, stream=None, fused=F
     moe_combine(p, bufs["y"], bufs["topk_idx"], bufs["topk_w"], bufs["slot"], out, stream)
 
 
-def _w4_workspace(bufs: dict, n: int, device, stream: int):
-    """bufs["w4_workspace"] of at least n bytes for work on the stream with this handle: made once, kept with the
+def _w4_workspace(bufs: dict, n: int, device, stream: int, name="w4_workspace"):
+    """bufs[name] of at least n bytes for work on the stream with this handle: made once, kept with the
     problem's buffers. Its memory belongs to the stream that it was made for, so that a dropped one is only handed on
     behind that stream's work; use on another stream is recorded with the allocator."""
     import torch
 
     def torch_stream():                                  # ExternalStream takes no default stream
         return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
-    ws = bufs.get("w4_workspace")
+    ws = bufs.get(name)
     if ws is None or ws.numel() < n:
         with torch.cuda.stream(torch_stream()):
-            bufs["w4_workspace"] = torch.empty(n, dtype=torch.uint8, device=device)
-        bufs["w4_workspace_stream"] = stream
-    elif bufs.get("w4_workspace_stream") != stream:
+            bufs[name] = torch.empty(n, dtype=torch.uint8, device=device)
+        bufs[name + "_stream"] = stream
+    elif bufs.get(name + "_stream") != stream:
         ws.record_stream(torch_stream())
 
 
-def run_w4_path(p: moe_problem, gate: moe_gate, x, logits, bias, gate_up, down, bufs: dict, h, out, stream=None):
-    """moe_route_gated -> moe_dispatch -> experts with 4-bit weights (gate and up through SiLU, then down) ->
-    moe_combine for one batch, on one stream. gate_up and down: (w4 shape, w_q, w_scale) of H -> I with
-    MOE_ACT_SILU_GATE and of I -> H; bufs as alloc_buffers(p) makes them, to which the path adds the experts' workspace
-    (which grows with the problem that needs more); h bf16 [E][C][I], the MLP's inner rows."""
-    b, T, H, E = bufs, p.num_tokens, p.hidden, p.num_experts
+def _w4_experts(p, gate, x, logits, bias, gate_up, down, b: dict, h, stream):
+    """The steps of run_w4_path up to the experts' rows b["y"]."""
+    T, H, E = p.num_tokens, p.hidden, p.num_experts
     pd = problem(T, H, E, p.top_k, p.num_ranks, p.capacity, MOE_DTYPE_BF16, p.max_blocks)     # h is bf16
     n = max(moe_expert_w4_workspace_bytes(p, gate_up[0]), moe_expert_w4_workspace_bytes(pd, down[0]))
-    stream = _stream(stream)
     _w4_workspace(b, n, h.device, stream)
     moe_route_gated(p, gate, logits, bias, b["topk_idx"], b["topk_w"], b["counts"], b["offsets"], b["slot"],
                     b["rank_counts"], b["dropped"], b["workspace"], stream)
@@ -579,7 +575,42 @@ def run_w4_path(p: moe_problem, gate: moe_gate, x, logits, bias, gate_up, down, 
     moe_expert_w4(p, gate_up[0], b["recv"], b.get("recv_scale"), b["counts"], gate_up[1], gate_up[2], h,
                   b["w4_workspace"], stream)
     moe_expert_w4(pd, down[0], h, None, b["counts"], down[1], down[2], b["y"], b["w4_workspace"], stream)
+
+
+def run_w4_path(p: moe_problem, gate: moe_gate, x, logits, bias, gate_up, down, bufs: dict, h, out, stream=None):
+    """moe_route_gated -> moe_dispatch -> experts with 4-bit weights (gate and up through SiLU, then down) ->
+    moe_combine for one batch, on one stream. gate_up and down: (w4 shape, w_q, w_scale) of H -> I with
+    MOE_ACT_SILU_GATE and of I -> H; bufs as alloc_buffers(p) makes them, to which the path adds the experts' workspace
+    (which grows with the problem that needs more); h bf16 [E][C][I], the MLP's inner rows."""
+    b, stream = bufs, _stream(stream)
+    _w4_experts(p, gate, x, logits, bias, gate_up, down, b, h, stream)
     moe_combine(p, b["y"], b["topk_idx"], b["topk_w"], b["slot"], out, stream)
+
+
+def run_w4_block(p: moe_problem, gate: moe_gate, norm: moe_norm, x, logits, bias, gate_up, down, bufs: dict, h, residual,
+                 w_post, w_pre, branch_gate, out, r, n, stream=None):
+    """run_w4_path with its combine joined to the residual stream: r = residual + scale * branch_gate * N(y; w_post) and
+    n = N(r; w_pre), the next block's input (moe_combine_norm). x is this block's input, the norm before it. out [T][H]
+    bf16 keeps y for the way back (run_block_backward), or is None."""
+    b, stream = bufs, _stream(stream)
+    _w4_experts(p, gate, x, logits, bias, gate_up, down, b, h, stream)
+    moe_combine_norm(p, norm, b["y"], b["topk_idx"], b["topk_w"], b["slot"], residual, w_post, w_pre, branch_gate, out, r, n,
+                     stream)
+
+
+def run_few_block(p: moe_problem, gate: moe_gate, mlp: moe_mlp, norm: moe_norm, x, logits, bias, w_up, up_scale, w_down,
+                  down_scale, residual, w_post, w_pre, branch_gate, bufs: dict, out, r, n, stream=None):
+    """A block of a decode step, for up to 32 tokens: moe_layer_few of x, this block's normed input, into out, then
+    moe_block_norm of it with the residual stream into r and n, the next block's input. bufs: a dict of the caller's (empty
+    at first) that keeps the layer's workspace, which grows with the problem that needs more."""
+    stream = _stream(stream)
+    need = moe_layer_few_workspace_bytes(p, mlp)
+    if need == 0:
+        raise MoeError("moe_layer_few_workspace_bytes", MOE_ERR_INVALID_ARG)
+    _w4_workspace(bufs, need, x.device, stream, "few_workspace")
+    moe_layer_few(p, gate, mlp, x, logits, bias, w_up, up_scale, w_down, down_scale, bufs.get("topk_idx"), bufs.get("topk_w"),
+                  out, bufs["few_workspace"], stream)
+    moe_block_norm(p, norm, out, residual, w_post, w_pre, branch_gate, r, n, stream)
 
 
 def run_gate_backward(p: moe_problem, gate: moe_gate, logits, d_out, bufs: dict, d_y, d_topk_w, d_logits, stream=None):
@@ -588,6 +619,17 @@ def run_gate_backward(p: moe_problem, gate: moe_gate, logits, d_out, bufs: dict,
     b = bufs
     moe_combine_backward(p, b["y"], d_out, b["topk_idx"], b["topk_w"], b["slot"], d_y, d_topk_w, stream)
     moe_route_gated_backward(p, gate, logits, b["topk_idx"], b["topk_w"], d_topk_w, d_logits, stream)
+
+
+def run_block_backward(p: moe_problem, gate: moe_gate, norm: moe_norm, logits, out, r, d_r, d_n, w_post, w_pre, branch_gate,
+                       bufs: dict, d_out, d_residual, d_w_post, d_w_pre, d_branch_gate, d_y, d_topk_w, d_logits, stream=None):
+    """The way back through run_w4_block's join, combine and router: moe_block_norm_backward from the forward pass's out and
+    r, then run_gate_backward of d_out, on the buffers that the forward pass left. Weights' gradients may be None."""
+    stream = _stream(stream)
+    _w4_workspace(bufs, moe_block_norm_backward_workspace_bytes(p, norm), d_out.device, stream, "norm_workspace")
+    moe_block_norm_backward(p, norm, out, r, d_r, d_n, w_post, w_pre, branch_gate, d_out, d_residual, d_w_post, d_w_pre,
+                            d_branch_gate, bufs["norm_workspace"], stream)
+    run_gate_backward(p, gate, logits, d_out, bufs, d_y, d_topk_w, d_logits, stream)
 
 
 def moe_layer_stand_in(x, out, a: float, busy_fmas: int = 0, stream=None):
