@@ -1,7 +1,8 @@
 // moe_few.cu -- a whole mixture-of-experts layer for up to 32 tokens: the choice by one block,
-// and two kernels for the products.
+// and two kernels for the products; with 8- and 4-bit weights blocks that make the tokens' x fp16
+// beside the choice, and a kernel that does so with h between the products.
 //
-//   up:    h[t][j] = bf16(silu(x Wg_e^T) (x Wu_e^T)) of every pair (t, j), e its expert
+//   up:    h[t][j] = round(silu(x Wg_e^T) (x Wu_e^T)) of every pair (t, j), e its expert
 //   down:  out[t] = bf16(sum_j w_j h[t][j] Wd_e^T)
 //
 // With few tokens every chosen expert's weights are read once for a handful of rows: the
@@ -21,6 +22,15 @@
 //     the row's largest, which keep an error of 2^-36 of it; h, kept in fp32 meanwhile, is rounded to its 11 bits.
 //     4-bit weights: inputs whose code stands higher are divided by 16, and what 1024 (or 64) and the codes' middle,
 //     8, add to a group's sum is taken off it in fp32: sum x (1024 + q) - 1032 sum x.
+//
+// us on GB300, with the floor of the chosen experts' bytes at the measured copy rate:
+//   1 token, 2 of 8 experts of 14336 x 4096, bf16             108    (floor 105)
+//   1 token, 8 of 256 of 2048 x 7168 and a shared one, 4-bit   60    (30.5)
+//   13 tokens, top-6 of 64 of 1408 x 2048 and shared, e4m3     94    (60.7; 46 experts live and the shared one)
+//   32 tokens, top-8 of 256 of 2048 x 7168, e4m3              797    (664; 101 live)
+// A call of next to no work takes 12.5 us: four launches one behind the other. What the slower ones spend: 4-bit
+// weights are bound by the instructions that make operands and scale their sums; lists of more than 8 rows by those
+// that load the inputs of each 16 of them.
 #include <algorithm>
 #include <type_traits>
 
@@ -37,7 +47,9 @@ constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewRows = 16;                       // matrix rows of a unit
 constexpr int kFewBlocks = 4;                      // blocks (64 bytes of each row) in a slot of a warp's ring
 constexpr int kFewSlot = kFewBlocks * kFewRows * 64;
-constexpr int kFewSlots = 2;                       // for each warp
+// For each warp. What the ring leaves of an SM's memory is L1 for the inputs and the scales: 32 tokens, top-6 of 64 experts
+// of 1408 x 2048, e4m3, take 116 us with two slots, 146 with three; one token 20.8 and 21.4.
+constexpr int kFewSlots = 2;
 constexpr int kFewRing = kFewWarps * kFewSlots * kFewSlot;
 constexpr int kFewMaxPairs = kFewTokens * kMaxTopK + kFewTokens;       // with the shared expert's
 constexpr int kFewMaxLists = kFewTokens * kMaxTopK + 1;                // experts with rows
@@ -420,7 +432,8 @@ struct FewParts {
 
 // x: up, the tokens' inputs; down, the pairs' h; where they are fp16 with their rows' scales. h: what the up kernel writes,
 // fp32 where it is made fp16 after, else bf16.
-// NTM times 8 columns at most.
+// NTM times 8 columns at most: one for up to 8 tokens, whose registers are few and whose code has no loop over columns. 8 tokens,
+// top-6 of 64 experts of 1408 x 2048, e4m3: 64.8 us, with four 67.8; 4-bit, 53.4 and 55.8.
 template <int WT, bool DOWN, int NTM>
 __global__ void __launch_bounds__(kFewThreads, 2)
 few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int split, const FewLists *made, FewInputs in,
@@ -832,13 +845,22 @@ struct FewSpace {
     FewParts parts;
     void *h;                                       // [T (k + shared)][I]: bf16, or fp32 where h_half follows
     FewInputs x_half, h_half;
+    int split;
     size_t bytes;
 };
 // The binary logarithm of how many blocks share a down unit: where the units are too few for the SMs' warps (2048 outputs
-// are 128 units).
-int few_split(int H) {
+// are 128 units) and leave each of those warps at least four pieces. us with one block to a unit and with two, 2048 outputs
+// of 1408 inputs, top-6 of 64 experts: 32 tokens, bf16, 212 and 182; e4m3, 152 and 116; one token, bf16 (8 pieces a warp with
+// one), 20.4 and 19.9; e4m3 (5), 20.5 and 20.8; 4-bit (2), 18.8 and 20.3.
+int few_split(const Dims &d, const moe_mlp *m) {
+    const int piece = kFewBlocks * (m->weights == MOE_WEIGHTS_BF16 ? kFewBlockInputs<kBf16>
+                                    : m->weights == MOE_WEIGHTS_W4 ? kFewBlockInputs<kW4G32>
+                                                                   : kFewBlockInputs<kFp8>);
+    const long long pieces = (std::min<long long>((long long)d.T * d.k, d.E) + m->shared) * ((m->inner + piece - 1) / piece);
     int split = 0;
-    while (split < 3 && ((long long)(H / 16) * kFewWarps << (split + 1)) <= 2LL * 152 * kFewWarps) ++split;
+    while (split < 3 && ((long long)(d.H / 16) * kFewWarps << (split + 1)) <= 2LL * 152 * kFewWarps &&
+           pieces >= 4LL * kFewWarps << (split + 1))
+        ++split;
     return split;
 }
 FewSpace few_space(void *base, const Dims &d, const moe_mlp *m) {
@@ -850,7 +872,7 @@ FewSpace few_space(void *base, const Dims &d, const moe_mlp *m) {
         return p;
     };
     const size_t T = d.T, pairs = T * (d.k + m->shared), I = m->inner;
-    const int split = few_split(d.H);
+    const int split = few_split(d, m);
     const bool half = m->weights != MOE_WEIGHTS_BF16, w4 = m->weights == MOE_WEIGHTS_W4;
     const auto inputs = [&](size_t rows, size_t n) {
         FewInputs f;
@@ -859,6 +881,7 @@ FewSpace few_space(void *base, const Dims &d, const moe_mlp *m) {
         f.less = static_cast<float *>(take(w4 ? rows * (n / m->group) * 4 : 0));
         return f;
     };
+    s.split = split;
     s.lists = static_cast<FewLists *>(take(sizeof(FewLists)));
     s.parts.there = static_cast<unsigned *>(take((size_t)d.H / 16 * sizeof(unsigned)));
     s.parts.sums = static_cast<float *>(take(split > 0 ? ((size_t)d.H << split) * T * sizeof(float) : 0));
@@ -917,7 +940,7 @@ int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, 
     if (half && launch_pdl(few_half_kernel, d.T * (d.k + a.shared), 256, st, s.lists, static_cast<const float *>(s.h), a.I, group,
                            s.h_half) != cudaSuccess)
         return MOE_ERR_CUDA;
-    const int split = few_split(d.H);
+    const int split = s.split;
     units = (long long)(d.H / 16) << split;
     if (launch_pdl_smem(few_kernel<WT, true, NTM>, few_grid(units, d.max_blocks), kFewThreads,
                         kFewRing + (size_t)kFewWarps * d.T * 16 * sizeof(float), st, down, a, few_team(units), split, s.lists,

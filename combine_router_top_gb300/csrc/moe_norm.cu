@@ -12,8 +12,16 @@
 //   D   = d_r + (w_pre d_n - r^ mean(r^ w_pre d_n)) / s_r                 = d_residual
 //   d_y = (w_post c - y^ mean(y^ w_post c)) / s_y,  c = a g D
 //   d_w_pre = sum_t d_n r^    d_w_post = sum_t c y^    d_gate = a sum D b  (over t, or over h)
-// Both norms' statistics come from the row itself again, which is in registers: the forward
+// Both norms' statistics come from the row itself again, which is in shared memory: the forward
 // pass keeps nothing but y and r.
+//
+// All of it is bound by HBM where there are many rows, and by a launch and two sums over a block
+// where there are few. One call a row's block, us on GB300 (floor: bytes at the measured copy rate):
+//   norm, 1 x 7168                           5.2  (launch, load, two sums, store)
+//   norm, 16384 x 7168, bf16               159    (floor 140; a copy and two sums a row)
+//   combine and norm, 1024 x 7168, top-8    34.8  (floor 24)
+//   gradient, 4096 x 7168, channel gate     90    (floor 53)
+//   gradient, 16381 x 4096                 148    (floor 120)
 #include <math.h>
 
 #include <algorithm>
@@ -26,6 +34,7 @@ namespace {
 
 constexpr int kNormMaxHidden = 16384;
 constexpr int kNormMaxDepth = 4;                   // rows on their way or at hand in a ring
+// Threads of the ring kernel on an SM: so many warps that one row's sums leave others to run.
 constexpr int kNormThreadsPerSM = 1024;
 constexpr int kCombineSlots = 16, kCombineSmem = 160 * 1024;       // experts' rows in a ring
 
@@ -236,8 +245,9 @@ __device__ __forceinline__ void finish_row(const NormArgs &a, int t, float g, fl
     }
 }
 
-// moe_block_norm for few rows: a block takes a row at a time, NC chunks of 8 elements to a thread, straight into
-// registers; has_y: there is a block before the norm.
+// moe_block_norm for few rows, or very long ones: a block takes a row at a time, NC chunks of 8 elements to a thread,
+// straight into registers, which has the shortest chain: no ring to set up, the vectors' loads beside the row's.
+// HAS_Y: there is a block before the norm.
 template <bool HAS_Y, bool RES32, bool PAR32, int NC>
 __global__ void __launch_bounds__(1024)
 norm_kernel(NormArgs a, const void *__restrict__ y, const void *residual, const void *__restrict__ w_post,
@@ -321,7 +331,9 @@ __device__ __forceinline__ void put_choices(const NormArgs &a, const Choice &c, 
     if (lane == 0) to.n = __popc(kept);
 }
 
-// moe_combine_norm: the same behind the weighted sum of SRC experts' rows at a time, a token after the other.
+// moe_combine_norm: the same behind the weighted sum of SRC experts' rows at a time, a token after the other, whose
+// choices are loaded a token ahead. Few tokens or short rows: all of a token's rows are asked for at once. 237 x 2056,
+// top-6: 6.7 us.
 template <int SRC, bool RES32, bool PAR32, int NC, int MAXT>
 __global__ void __launch_bounds__(MAXT)
 combine_norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__restrict__ topk_idx,
@@ -393,7 +405,8 @@ combine_norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__res
 
 // The same for many tokens. The block's last warp sees to the tokens' choices and to the experts' rows, which come by bulk
 // copies into a ring of `slots` rows, tokens ahead; the others add each row as it arrives. (Loads to registers a token ahead
-// would fill the SM's load queue, behind which the sums' shared memory accesses then wait.)
+// would fill the SM's load queue, behind which the sums' shared memory accesses then wait: 48 us for 1024 x 7168, top-8,
+// where this takes 35 and the kernel above 45.)
 template <bool RES32, bool PAR32, int NC>
 __global__ void __launch_bounds__(544, NC == 4 ? 1 : 2)
 combine_norm_rows_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__restrict__ topk_idx,
@@ -512,9 +525,10 @@ combine_norm_rows_kernel(NormArgs a, const void *__restrict__ y, const int32_t *
 }
 
 // moe_block_norm for many rows. A block of threads takes a row at a time, NC chunks of 8 elements to a thread; the rows of
-// y and of the residual come by bulk copies into a ring, `depth` rows deep, so that loads run on while a row's sums meet.
+// y and of the residual come by bulk copies into a ring, `depth` rows deep, so that loads run on while a row's sums meet:
+// 4864 x 7168 in 52 us, straight into registers 87.
 template <bool RES32, bool PAR32, int NC>
-__global__ void __launch_bounds__(512, NC == 4 ? 1 : 2)
+__global__ void __launch_bounds__(512, 2)
 norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__restrict__ w_post,
                  const void *__restrict__ w_pre, const void *__restrict__ gate, void *r_out, void *n_out, int depth,
                  unsigned *status) {
@@ -692,8 +706,10 @@ int launch_combine_norm_rows(const Dims &d, const NormArgs &a, cudaStream_t st, 
 }
 template <bool RES32, bool PAR32>
 int launch_combine_norm_k(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
-    if (d.T >= 2 * 152) {                            // several tokens to a block
-        if (a.H8 <= 256) return launch_combine_norm_rows<RES32, PAR32, 1>(d, a, st, p);
+    // the ring, where a block has several tokens and a row is long. us, direct and ring, with 2 choices a token: 304 tokens of
+    // 2048 channels, 3.7 and 3.9; 4096 of 2048, 21 and 28; 304 of 4096, 4.4 and 4.9; 4096 of 4096, 48 and 40; with 8: 4096 of
+    // 2048, 49 and 51; 304 of 4096, 8.0 and 6.8; 304 of 7168, 11.4 and 8.5; 4096 of 7168, 146 and 104; of 16384, 273 and 254.
+    if (d.T >= 2 * 152 && a.H8 > 256) {
         if (a.H8 <= 1024) return launch_combine_norm_rows<RES32, PAR32, 2>(d, a, st, p);
         return launch_combine_norm_rows<RES32, PAR32, 4>(d, a, st, p);
     }
@@ -702,8 +718,10 @@ int launch_combine_norm_k(const Dims &d, const NormArgs &a, cudaStream_t st, con
     return launch_combine_norm_nc<8, RES32, PAR32>(d, a, st, p);
 }
 
-// Rows from which the ring pays, for a block's output of its own.
-bool norm_many_rows(const Dims &d) { return d.T >= 8 * 152; }
+// Where the ring pays, with a block's output of its own: from about four rows to an SM on, up to 8192 channels. us, direct
+// and ring: 304 rows of 2048, 2.9 and 3.2; 608, 3.4 and 3.5; 4864, 17.2 and 16.5; 608 of 7168, 9.7 and 7.7; 2432, 44 and 30;
+// 608 of 16384 (a ring of two rows at most), 14.7 and 16.7; 4864, 130 and 138.
+bool norm_many_rows(const Dims &d) { return d.T >= 4 * 152 && d.H <= 8192; }
 
 template <bool RES32, bool PAR32, int NC>
 int launch_norm_rows(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
@@ -726,8 +744,7 @@ int launch_norm_rows(const Dims &d, const NormArgs &a, cudaStream_t st, const No
 template <bool RES32, bool PAR32>
 int launch_norm_rows_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormPtrs &p) {
     if (a.H8 <= 256) return launch_norm_rows<RES32, PAR32, 1>(d, a, st, p);
-    if (a.H8 <= 1024) return launch_norm_rows<RES32, PAR32, 2>(d, a, st, p);
-    return launch_norm_rows<RES32, PAR32, 4>(d, a, st, p);
+    return launch_norm_rows<RES32, PAR32, 2>(d, a, st, p);
 }
 // By the types that the call names: f(residual fp32, parameters fp32).
 template <typename F>
@@ -783,9 +800,11 @@ struct NormBwdPtrs {
 // A block takes the rows of one part (rows p, p + parts, ...) at a time and keeps that part's column
 // sums in registers: NC chunks of 8 columns to a thread. The rows of y, r, d_r and d_n come by
 // bulk copies into a ring, `depth` rows deep, so that loads run on while a row's two sums meet; they are
-// read there again for each of the three passes over a row, which leaves registers for twice the threads.
-template <bool RES32, bool PAR32, int NC>
-__global__ void __launch_bounds__(NC == 1 ? 256 : 512)
+// read there again for each of the three passes over a row, which leaves registers for the column sums.
+// Bound by the chain of a row's three passes and two sums, one row of 7168 to an SM at a time: 3.2 us a row,
+// of which its bytes need 1.9.
+template <bool RES32, bool PAR32, int NC, int MAXT>
+__global__ void __launch_bounds__(MAXT)
 norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
     extern __shared__ __align__(128) char bwd_ring[];
     __shared__ __align__(8) uint64_t full[kNormMaxDepth];
@@ -826,7 +845,7 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
         for (int i = 0; i < depth; ++i) fetch(i);
 
     // the vectors that every row uses, where registers hold them
-    constexpr bool kHold = !PAR32 && NC <= 2;
+    constexpr bool kHold = !PAR32 && MAXT <= 512 && NC <= 2;
     Raw8<PAR32> hold[kHold ? 3 : 1][kHold ? NC : 1];
     if constexpr (kHold) {
 #pragma unroll
@@ -866,7 +885,7 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
                 Raw8<PAR32> raw;
                 float wf[8];
                 if constexpr (kHold) raw = hold[which][i];
-                else load_param8(w, c, raw);
+                else load_param8_again(w, c, raw);
                 to_floats(raw, wf);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) f[q] = __fmul_rn(f[q], wf[q]);
@@ -1026,7 +1045,8 @@ norm_columns_kernel(NormArgs a, const float *part, int parts, const void *__rest
 }
 
 // Parts of the column sums: by the sizes alone, so that neither the grid nor the device changes a
-// sum's order. About as many as blocks that GB300's 152 SMs hold at once.
+// sum's order. About as many as blocks that GB300's 152 SMs hold at once; each part costs two rows of fp32 to
+// write and to read again.
 int norm_parts(long long T, int H) {
     const long long most = 152LL * std::max(1, std::min(8, 8192 / H));
     return (int)std::max(1LL, std::min(most, (T + 1) / 2));
@@ -1051,10 +1071,10 @@ int launch_columns(const Dims &d, const NormArgs &a, cudaStream_t st, const floa
                : MOE_ERR_CUDA;
 }
 
-template <bool RES32, bool PAR32, int NC>
+template <bool RES32, bool PAR32, int NC, int MAXT>
 int launch_backward_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormBwdPtrs &p, float *d_w_post,
                        float *d_w_pre, float *d_gate) {
-    const auto kernel = norm_backward_kernel<RES32, PAR32, NC>;
+    const auto kernel = norm_backward_kernel<RES32, PAR32, NC, MAXT>;
     const int threads = ((a.H8 + NC - 1) / NC + 31) / 32 * 32;
     const int row = d.H * ((p.y ? 2 : 0) + (p.w_pre ? (RES32 ? 6 : 4) : 0) + (p.d_r ? (RES32 ? 4 : 2) : 0));
     const int parts = norm_parts(d.T, d.H);
@@ -1070,9 +1090,13 @@ int launch_backward_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const 
 }
 template <bool RES32, bool PAR32, typename... A>
 int launch_norm_backward(const Dims &d, const NormArgs &a, A... args) {
-    if (a.H8 <= 256) return launch_backward_nc<RES32, PAR32, 1>(d, a, args...);
-    if (a.H8 <= 1024) return launch_backward_nc<RES32, PAR32, 2>(d, a, args...);
-    return launch_backward_nc<RES32, PAR32, 4>(d, a, args...);
+    if (a.H8 <= 256) return launch_backward_nc<RES32, PAR32, 1, 256>(d, a, args...);
+    // one block to an SM, of more warps with a chunk each, which leaves no registers for the vectors: 4096 x 7168 in 88 us,
+    // with two chunks 95; 608 x 7168 in 19.2 and 20.6. Where two blocks of two chunks fit an SM it loses: 4096 x 4096 in
+    // 65 us, with two chunks 54
+    if (a.H8 > 512 && a.H8 <= 896) return launch_backward_nc<RES32, PAR32, 1, 896>(d, a, args...);
+    if (a.H8 <= 1024) return launch_backward_nc<RES32, PAR32, 2, 512>(d, a, args...);
+    return launch_backward_nc<RES32, PAR32, 4, 512>(d, a, args...);
 }
 
 }  // namespace

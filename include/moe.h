@@ -490,7 +490,10 @@ typedef struct moe_norm {
  * p are used (its other sizes have to be valid). H <= 16384 (else
  * MOE_ERR_UNSUPPORTED). Rows whose sum of squares passes fp32 (entries from
  * about 2^60 on) are outside the norm's range. Row buffers, weights and a
- * channel gate 16-byte aligned, a token gate 4-byte. */
+ * channel gate 16-byte aligned, a token gate 4-byte. A row's results depend on
+ * its own values alone; max_blocks caps the grid and changes none. Waits on the
+ * kernel's own copies are bounded (moe_device_status). Launched as a programmatic
+ * dependent of the previous kernel. */
 int moe_block_norm(const moe_problem *p, const moe_norm *norm, const void *y, const void *residual,
                    const void *w_post, const void *w_pre, const void *gate, void *r, void *n, void *stream);
 
@@ -552,15 +555,16 @@ typedef struct moe_mlp {
  * invalid. Contents need no initialisation. */
 size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
 
-/* A whole mixture-of-experts layer for up to 32 tokens, in a few launches: the
- * choice as moe_route_gated makes it, then for every pair (t, j), e = topk_idx[t][j],
+/* A whole mixture-of-experts layer for up to 32 tokens, in three launches (bf16
+ * weights) or four: the choice as moe_route_gated makes it, then for every pair (t, j), e = topk_idx[t][j],
  *   u = x[t] Wup_e^T (2I values: the gate's I, then the up's)
  *   h[i] = round(silu(u[i]) u[I + i]),   silu(v) = v / (1 + exp(-v))
  *   out[t] = bf16(sum_j topk_w[t][j] h Wdown_e^T)
  * with the shared expert's term of weight 1 behind the pairs'. Products are exact,
- * sums fp32; h is rounded to the products' operand type, which is bf16, or with e4m3
- * weights fp16 behind a power of two for each row (x too: its values below 2^-29 of
- * their row's largest then lose bits, 2^-39 of that largest at most); out once. There
+ * sums fp32; h is rounded to the products' operand type, which is bf16, or with e4m3 and
+ * 4-bit weights fp16 behind a power of two for each row (x too: its values below 2^-25 of
+ * their row's largest then lose bits, 2^-36 of that largest at most, and an infinity or
+ * NaN makes its token's out NaN or infinite); out once. There
  * is no capacity: no pair is dropped, and choices that are no pair take no part (a
  * token without pairs and without a shared expert has out 0). Each chosen expert's weights
  * are read once, the others' not at all.
@@ -574,10 +578,10 @@ size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
  *   MOE_WEIGHTS_W4: codes u8 [S][M][K/2] packed as for moe_expert_w4 (w4_pack),
  *     scale bf16 [S][M][K/group].
  * T > 32, H or I no multiple of 64 (bf16) or 128 (fp8, 4-bit): MOE_ERR_UNSUPPORTED.
- * R and C of p are not used; max_blocks caps the grids. Deterministic, and
- * independent of max_blocks. Buffers 16-byte aligned (logits as for
- * moe_route_gated; bias, topk_idx, topk_w and fp8 scales 4-byte, 4-bit scales
- * 2-byte); outputs and workspace overlap no input. workspace: at least
+ * R and C of p are not used; max_blocks caps the grids of the products' kernels (the
+ * others have at most a block for each row). Deterministic, and independent of
+ * max_blocks. Buffers 16-byte aligned (logits as for moe_route_gated; bias, topk_idx,
+ * topk_w and fp8 scales 4-byte); outputs and workspace overlap no input. workspace: at least
  * moe_layer_few_workspace_bytes, not shared with a concurrent call. Waits on the
  * kernels' own copies are bounded (moe_device_status). Launched as programmatic
  * dependents. */
