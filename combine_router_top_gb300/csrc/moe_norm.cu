@@ -20,8 +20,8 @@
 //   norm, 1 x 7168                           5.2  (launch, load, two sums, store)
 //   norm, 16384 x 7168, bf16               159    (floor 140; a copy and two sums a row)
 //   combine and norm, 1024 x 7168, top-8    34.8  (floor 24)
-//   gradient, 4096 x 7168, channel gate     90    (floor 53)
-//   gradient, 16381 x 4096                 148    (floor 120)
+//   gradient, 4096 x 7168, channel gate     85    (floor 53)
+//   gradient, 16381 x 4096                 149    (floor 120)
 #include <math.h>
 
 #include <algorithm>
@@ -55,18 +55,19 @@ template <>
 struct Raw8<true> {
     uint4 a, b;
 };
-__device__ __forceinline__ void to_floats(const Raw8<false> &v, float (&f)[8]) {
+// fp32 in pairs: a product or a sum of two is one instruction.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ void to_floats(const Raw8<false> &v, float2 (&f)[4]) {
     const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
 }
-__device__ __forceinline__ void to_floats(const Raw8<true> &v, float (&f)[8]) {
+__device__ __forceinline__ void to_floats(const Raw8<true> &v, float2 (&f)[4]) {
     const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
 }
 // Chunk c of a row that is read once.
 __device__ __forceinline__ void load_row8(const void *row, int c, Raw8<false> &v) {
@@ -110,14 +111,14 @@ __device__ __forceinline__ void load_param8_again(const void *p, int c, Raw8<tru
     v.b = ld_again_v4(static_cast<const uint4 *>(p) + 2 * c + 1);
 }
 template <bool F32>
-__device__ __forceinline__ void store8(void *row, int c, const float (&f)[8]) {
+__device__ __forceinline__ void store8(void *row, int c, const float2 (&f)[4]) {
     if constexpr (F32) {
         uint4 *o = static_cast<uint4 *>(row) + 2 * c;
-        st_v4(o, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
-        st_v4(o + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+        st_v4(o, make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y)));
+        st_v4(o + 1, make_uint4(__float_as_uint(f[2].x), __float_as_uint(f[2].y), __float_as_uint(f[3].x), __float_as_uint(f[3].y)));
     } else {
-        st_v4(static_cast<uint4 *>(row) + c, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                        pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+        st_v4(static_cast<uint4 *>(row) + c, make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                                                        pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y)));
     }
 }
 
@@ -189,48 +190,51 @@ __device__ __forceinline__ float inv_rms(float sum_sq, const NormArgs &a) {
 // From the block's output v, of which a thread has NC chunks of 8 elements in registers, and the residual to r and n. g: the
 // scale and a token's gate. param(k, c): chunk c of w_post (k = 0), of the gate for each channel (1) or of w_pre (2).
 template <bool HAS_Y, bool RES32, int NC, typename Param>
-__device__ __forceinline__ void finish_row(const NormArgs &a, int t, float g, float (&v)[NC][8], const Raw8<RES32> (&res)[NC],
+__device__ __forceinline__ void finish_row(const NormArgs &a, int t, float g, float2 (&v)[NC][4], const Raw8<RES32> (&res)[NC],
                                            bool w_post, bool w_pre, Param param, void *r_out, void *n_out, BlockSum<1> &sums,
                                            unsigned &turn, int threads) {
     const size_t res_row = (size_t)a.H8 * (RES32 ? 32 : 16), bf_row = (size_t)a.H8 * 16;
-    const auto times = [&](int k, int c, float (&f)[8]) {
-        float p[8];
+    const auto times = [&](int k, int c, float2 (&f)[4]) {
+        float2 p[4];
         to_floats(param(k, c), p);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] = __fmul_rn(f[q], p[q]);
+        for (int q = 0; q < 4; ++q) f[q] = mul2(f[q], p[q]);
     };
-    float f[1] = {0.0f};
+    float f[1];
+    float2 sq = both(0.0f);
     if (HAS_Y && w_post) {
 #pragma unroll
         for (int i = 0; i < NC; ++i)
             if (i * threads + (int)threadIdx.x < a.H8)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) f[0] = __fmaf_rn(v[i][q], v[i][q], f[0]);
+                for (int q = 0; q < 4; ++q) sq = fma2(v[i][q], v[i][q], sq);
+        f[0] = __fadd_rn(sq.x, sq.y);
         block_sum(sums, f, turn, threads);
         g = __fmul_rn(g, inv_rms(f[0], a));
     }
-    f[0] = 0.0f;
+    sq = both(0.0f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = i * threads + (int)threadIdx.x;
         if (c < a.H8) {
-            float x[8];
+            float2 x[4];
             to_floats(res[i], x);
             if constexpr (HAS_Y) {
                 if (w_post) times(0, c, v[i]);
                 if (a.channel) times(1, c, v[i]);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) x[q] = __fmaf_rn(v[i][q], g, x[q]);
+                for (int q = 0; q < 4; ++q) x[q] = fma2(v[i][q], both(g), x[q]);
             }
             if (r_out) store8<RES32>(static_cast<char *>(r_out) + t * res_row, c, x);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                f[0] = __fmaf_rn(x[q], x[q], f[0]);
+            for (int q = 0; q < 4; ++q) {
+                sq = fma2(x[q], x[q], sq);
                 v[i][q] = x[q];
             }
         }
     }
     if (!w_pre) return;
+    f[0] = __fadd_rn(sq.x, sq.y);
     block_sum(sums, f, turn, threads);
     const float s = inv_rms(f[0], a);
 #pragma unroll
@@ -238,7 +242,7 @@ __device__ __forceinline__ void finish_row(const NormArgs &a, int t, float g, fl
         const int c = i * threads + (int)threadIdx.x;
         if (c < a.H8) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], s);
+            for (int q = 0; q < 4; ++q) v[i][q] = mul2(v[i][q], both(s));
             times(2, c, v[i]);
             store8<false>(static_cast<char *>(n_out) + t * bf_row, c, v[i]);
         }
@@ -263,7 +267,7 @@ norm_kernel(NormArgs a, const void *__restrict__ y, const void *residual, const 
         Raw8<RES32> res[NC];
         Raw8<false> yy[NC];
         Raw8<PAR32> p_post, p_pre, p_gate;
-        float v[NC][8];
+        float2 v[NC][4];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             c[i] = i * (int)blockDim.x + (int)threadIdx.x;
@@ -350,13 +354,13 @@ combine_norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__res
     for (int t = blockIdx.x; t < a.T; t += gridDim.x, at ^= 1u) {
         const Choices &now = choices[at];
         Raw8<RES32> res[NC];
-        float v[NC][8];
+        float2 v[NC][4];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = i * (int)blockDim.x + (int)threadIdx.x;
             if (c < a.H8) load_residual8(static_cast<const char *>(residual) + t * res_row, c, res[i]);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+            for (int q = 0; q < 4; ++q) v[i][q] = both(0.0f);
         }
         for (int j0 = 0; j0 < now.n; j0 += SRC) {                      // once, or more past SRC choices
             Raw8<false> in[SRC][NC];
@@ -374,10 +378,10 @@ combine_norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__res
                     const float w = now.w[j0 + j];
 #pragma unroll
                     for (int i = 0; i < NC; ++i) {
-                        float f[8];
+                        float2 f[4];
                         to_floats(in[j][i], f);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[i][q] = __fmaf_rn(w, f[q], v[i][q]);
+                        for (int q = 0; q < 4; ++q) v[i][q] = fma2(both(w), f[q], v[i][q]);
                     }
                 }
             }
@@ -473,13 +477,13 @@ combine_norm_rows_kernel(NormArgs a, const void *__restrict__ y, const int32_t *
     for (int t = blockIdx.x; t < a.T; t += gridDim.x, ++n_token) {
         const unsigned at = n_token % kAhead;
         Raw8<RES32> res[NC];
-        float v[NC][8];
+        float2 v[NC][4];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = i * threads + tid;
             if (c < a.H8) load_residual8(static_cast<const char *>(residual) + t * res_row, c, res[i]);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[i][q] = 0.0f;
+            for (int q = 0; q < 4; ++q) v[i][q] = both(0.0f);
         }
         wait(&known[at], n_token / kAhead);
         const int n = alive ? choices[at].n : 0;
@@ -491,10 +495,10 @@ combine_norm_rows_kernel(NormArgs a, const void *__restrict__ y, const int32_t *
             for (int i = 0; i < NC; ++i) {
                 const int c = i * threads + tid;
                 if (c < a.H8) {
-                    float f[8];
+                    float2 f[4];
                     to_floats(*reinterpret_cast<const Raw8<false> *>(in + (size_t)c * 16), f);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[i][q] = __fmaf_rn(w, f[q], v[i][q]);
+                    for (int q = 0; q < 4; ++q) v[i][q] = fma2(both(w), f[q], v[i][q]);
                 }
             }
             __syncwarp();
@@ -566,22 +570,24 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
         const char *in = norm_ring + (size_t)s * stage;
         Raw8<false> yy[NC];
         Raw8<RES32> res[NC];
-        float f[1] = {0.0f};
+        float f[1];
+        float2 sq = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = i * (int)blockDim.x + tid;
             if (c < a.H8) {
                 yy[i] = *reinterpret_cast<const Raw8<false> *>(in + (size_t)c * 16);
                 res[i] = *reinterpret_cast<const Raw8<RES32> *>(in + bf_row + (size_t)c * sizeof(Raw8<RES32>));
-                float v[8];
+                float2 v[4];
                 to_floats(yy[i], v);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) f[0] = __fmaf_rn(v[q], v[q], f[0]);
+                for (int q = 0; q < 4; ++q) sq = fma2(v[q], v[q], sq);
             }
         }
         float g = a.scale;
         if (a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
         if (w_post) {
+            f[0] = __fadd_rn(sq.x, sq.y);
             block_sum(sums, f, turn, (int)blockDim.x);
             g = __fmul_rn(g, inv_rms(f[0], a));
         } else {
@@ -593,40 +599,41 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
             s = 0;
             parity ^= 1u;
         }
-        float v[NC][8];
-        f[0] = 0.0f;
+        float2 v[NC][4];
+        sq = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = i * (int)blockDim.x + tid;
             if (c < a.H8) {
-                float x[8];
+                float2 x[4];
                 to_floats(yy[i], v[i]);
                 to_floats(res[i], x);
                 if (w_post) {
                     Raw8<PAR32> w;
-                    float p[8];
+                    float2 p[4];
                     load_param8(w_post, c, w);
                     to_floats(w, p);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], p[q]);
+                    for (int q = 0; q < 4; ++q) v[i][q] = mul2(v[i][q], p[q]);
                 }
                 if (a.channel) {
                     Raw8<PAR32> w;
-                    float p[8];
+                    float2 p[4];
                     load_param8(gate, c, w);
                     to_floats(w, p);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[i][q] = __fmul_rn(v[i][q], p[q]);
+                    for (int q = 0; q < 4; ++q) v[i][q] = mul2(v[i][q], p[q]);
                 }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    v[i][q] = __fmaf_rn(v[i][q], g, x[q]);
-                    f[0] = __fmaf_rn(v[i][q], v[i][q], f[0]);
+                for (int q = 0; q < 4; ++q) {
+                    v[i][q] = fma2(v[i][q], both(g), x[q]);
+                    sq = fma2(v[i][q], v[i][q], sq);
                 }
                 if (r_out) store8<RES32>(static_cast<char *>(r_out) + (size_t)t * res_row, c, v[i]);
             }
         }
         if (w_pre) {
+            f[0] = __fadd_rn(sq.x, sq.y);
             block_sum(sums, f, turn, (int)blockDim.x);
             const float by = inv_rms(f[0], a);
 #pragma unroll
@@ -634,11 +641,11 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
                 const int c = i * (int)blockDim.x + tid;
                 if (c < a.H8) {
                     Raw8<PAR32> w;
-                    float p[8];
+                    float2 p[4];
                     load_param8(w_pre, c, w);
                     to_floats(w, p);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) p[q] = __fmul_rn(__fmul_rn(v[i][q], by), p[q]);
+                    for (int q = 0; q < 4; ++q) p[q] = mul2(mul2(v[i][q], both(by)), p[q]);
                     store8<false>(static_cast<char *>(n_out) + (size_t)t * bf_row, c, p);
                 }
             }
@@ -801,7 +808,7 @@ struct NormBwdPtrs {
 // sums in registers: NC chunks of 8 columns to a thread. The rows of y, r, d_r and d_n come by
 // bulk copies into a ring, `depth` rows deep, so that loads run on while a row's two sums meet; they are
 // read there again for each of the three passes over a row, which leaves registers for the column sums.
-// Bound by the chain of a row's three passes and two sums, one row of 7168 to an SM at a time: 3.2 us a row,
+// Bound by the chain of a row's three passes and two sums, one row of 7168 to an SM at a time: 3.1 us a row,
 // of which its bytes need 1.9.
 template <bool RES32, bool PAR32, int NC, int MAXT>
 __global__ void __launch_bounds__(MAXT)
@@ -845,7 +852,7 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
         for (int i = 0; i < depth; ++i) fetch(i);
 
     // the vectors that every row uses, where registers hold them
-    constexpr bool kHold = !PAR32 && MAXT <= 512 && NC <= 2;
+    constexpr bool kHold = !PAR32 && MAXT == 256;
     Raw8<PAR32> hold[kHold ? 3 : 1][kHold ? NC : 1];
     if constexpr (kHold) {
 #pragma unroll
@@ -860,11 +867,11 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
     }
     unsigned turn3 = 0, turn1 = 0, n_row = 0, lost = 0, s = 0, parity = 0;
     for (int part = blockIdx.x; part < parts; part += gridDim.x) {
-        float sum_pre[NC][8], sum_post[NC][8];
+        float2 sum_pre[NC][4], sum_post[NC][4];
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) sum_pre[i][q] = sum_post[i][q] = 0.0f;
+            for (int q = 0; q < 4; ++q) sum_pre[i][q] = sum_post[i][q] = both(0.0f);
         for (int t = part; t < a.T; t += parts, ++n_row) {
             if (alive && !mbar_wait_bounded(&full[s], parity)) {
                 alive = false;                       // outputs stay wrong; the barriers below still meet
@@ -872,47 +879,49 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
                 atomicOr(p.status, kStatusWaitGaveUp);
             }
             const char *in = bwd_ring + (size_t)s * stage;
-            const auto y_of = [&](int c, float (&f)[8]) {
+            const auto y_of = [&](int c, float2 (&f)[4]) {
                 to_floats(*reinterpret_cast<const Raw8<false> *>(in + (size_t)c * 16), f);
             };
-            const auto r_of = [&](int c, float (&f)[8]) {
+            const auto r_of = [&](int c, float2 (&f)[4]) {
                 to_floats(*reinterpret_cast<const Raw8<RES32> *>(in + at_r + (size_t)c * sizeof(Raw8<RES32>)), f);
             };
-            const auto dn_of = [&](int c, float (&f)[8]) {
+            const auto dn_of = [&](int c, float2 (&f)[4]) {
                 to_floats(*reinterpret_cast<const Raw8<false> *>(in + at_dn + (size_t)c * 16), f);
             };
-            const auto times = [&](const void *w, int which, int i, int c, float (&f)[8]) {
+            const auto times = [&](const void *w, int which, int i, int c, float2 (&f)[4]) {
                 Raw8<PAR32> raw;
-                float wf[8];
+                float2 wf[4];
                 if constexpr (kHold) raw = hold[which][i];
                 else load_param8_again(w, c, raw);
                 to_floats(raw, wf);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) f[q] = __fmul_rn(f[q], wf[q]);
+                for (int q = 0; q < 4; ++q) f[q] = mul2(f[q], wf[q]);
             };
-            float v[NC][8], f[4] = {0.0f, 0.0f, 0.0f, 0.0f};                         // v: w_pre d_n, then w_post g D
+            float2 v[NC][4];                         // w_pre d_n, then w_post g D
+            float2 rr = both(0.0f), rn = both(0.0f), yy = both(0.0f);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = i * (int)blockDim.x + tid;
                 if (c < a.H8) {
-                    float x[8];
+                    float2 x[4];
                     if (p.w_post) {
                         y_of(c, x);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) f[2] = __fmaf_rn(x[q], x[q], f[2]);
+                        for (int q = 0; q < 4; ++q) yy = fma2(x[q], x[q], yy);
                     }
                     if (r_bytes) {
                         dn_of(c, v[i]);
                         times(p.w_pre, 0, i, c, v[i]);
                         r_of(c, x);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            f[0] = __fmaf_rn(x[q], x[q], f[0]);
-                            f[1] = __fmaf_rn(x[q], v[i][q], f[1]);
+                        for (int q = 0; q < 4; ++q) {
+                            rr = fma2(x[q], x[q], rr);
+                            rn = fma2(x[q], v[i][q], rn);
                         }
                     }
                 }
             }
+            float f[4] = {__fadd_rn(rr.x, rr.y), __fadd_rn(rn.x, rn.y), __fadd_rn(yy.x, yy.y), 0.0f};
             block_sum4(sums4, f, turn3);
             if (blockDim.x == 32) __syncwarp();
             // all are done with the row before this one
@@ -921,44 +930,45 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
             const float rs = inv_rms(f[0], a), ys = p.w_post ? inv_rms(f[2], a) : 1.0f;
             const float mean = __fmul_rn(__fmul_rn(f[1], rs), a.inv_h);         // of r^ w_pre d_n
             const float g = a.token ? __ldg(static_cast<const float *>(p.gate) + t) : 1.0f, gy = __fmul_rn(g, ys);
-            float e[1] = {0.0f};
+            float2 dot = both(0.0f);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = i * (int)blockDim.x + tid;
                 if (c < a.H8) {
-                    float D[8], x[8];
+                    float2 D[4], x[4];
                     if (dr_bytes)
                         to_floats(*reinterpret_cast<const Raw8<RES32> *>(in + at_dr + (size_t)c * sizeof(Raw8<RES32>)), D);
                     else
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) D[q] = 0.0f;
+                        for (int q = 0; q < 4; ++q) D[q] = both(0.0f);
                     if (r_bytes) {
-                        float n[8];
+                        float2 n[4];
                         r_of(c, x);
                         dn_of(c, n);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float rh = __fmul_rn(x[q], rs);
-                            sum_pre[i][q] = __fmaf_rn(n[q], rh, sum_pre[i][q]);
-                            D[q] = __fmaf_rn(rs, __fmaf_rn(-rh, mean, v[i][q]), D[q]);
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 rh = mul2(x[q], both(rs));
+                            sum_pre[i][q] = fma2(n[q], rh, sum_pre[i][q]);
+                            D[q] = fma2(both(rs), fma2(rh, both(-mean), v[i][q]), D[q]);
                         }
                     }
                     store8<RES32>(static_cast<char *>(p.d_residual) + (size_t)t * res_row, c, D);
                     if (y_bytes) {
                         y_of(c, x);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) sum_post[i][q] = __fmaf_rn(D[q], __fmul_rn(x[q], gy), sum_post[i][q]);
+                        for (int q = 0; q < 4; ++q) sum_post[i][q] = fma2(D[q], mul2(x[q], both(gy)), sum_post[i][q]);
                         if (a.channel) times(p.gate, 2, i, c, D);
                         if (p.w_post) times(p.w_post, 1, i, c, D);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
+                        for (int q = 0; q < 4; ++q) {
                             v[i][q] = D[q];
-                            e[0] = __fmaf_rn(D[q], x[q], e[0]);
+                            dot = fma2(D[q], x[q], dot);
                         }
                     }
                 }
             }
             if (y_bytes) {
+                float e[1] = {__fadd_rn(dot.x, dot.y)};
                 if (p.w_post || p.d_gate_token) block_sum(sums1, e, turn1, (int)blockDim.x);
                 const float by = __fmul_rn(a.scale, g);
                 if (p.d_gate_token && tid == 0) p.d_gate_token[t] = __fmul_rn(__fmul_rn(a.scale, ys), e[0]);
@@ -968,10 +978,10 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
                 for (int i = 0; i < NC; ++i) {
                     const int c = i * (int)blockDim.x + tid;
                     if (c < a.H8) {
-                        float x[8];
+                        float2 x[4];
                         y_of(c, x);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) x[q] = __fmul_rn(__fmaf_rn(-x[q], less, v[i][q]), by_y);
+                        for (int q = 0; q < 4; ++q) x[q] = mul2(fma2(x[q], both(-less), v[i][q]), both(by_y));
                         store8<false>(static_cast<char *>(p.d_y) + (size_t)t * bf_row, c, x);
                     }
                 }
@@ -1091,11 +1101,11 @@ int launch_backward_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const 
 template <bool RES32, bool PAR32, typename... A>
 int launch_norm_backward(const Dims &d, const NormArgs &a, A... args) {
     if (a.H8 <= 256) return launch_backward_nc<RES32, PAR32, 1, 256>(d, a, args...);
-    // one block to an SM, of more warps with a chunk each, which leaves no registers for the vectors: 4096 x 7168 in 88 us,
-    // with two chunks 95; 608 x 7168 in 19.2 and 20.6. Where two blocks of two chunks fit an SM it loses: 4096 x 4096 in
-    // 65 us, with two chunks 54
+    // A chunk to a thread, as many warps as there can be, though that leaves no registers for the vectors: they are read again
+    // for each row. us with one chunk a thread and with two and the vectors held: 4096 x 7168, 85 and 95; 16381 x 4096, 149 and
+    // 152; 237 x 2056, 15.0 and 17.1. Up to 896 threads there are more registers for each: 4096 x 7168 within 64 takes 89.
     if (a.H8 > 512 && a.H8 <= 896) return launch_backward_nc<RES32, PAR32, 1, 896>(d, a, args...);
-    if (a.H8 <= 1024) return launch_backward_nc<RES32, PAR32, 2, 512>(d, a, args...);
+    if (a.H8 <= 1024) return launch_backward_nc<RES32, PAR32, 1, 1024>(d, a, args...);
     return launch_backward_nc<RES32, PAR32, 4, 512>(d, a, args...);
 }
 
