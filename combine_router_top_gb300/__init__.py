@@ -415,8 +415,8 @@ def moe_layer_few_workspace_bytes(p: moe_problem, mlp: moe_mlp) -> int:
 
 def moe_layer_few(p, gate, mlp, x, logits, bias, w_up, up_scale, w_down, down_scale, topk_idx, topk_w, out, workspace,
                   stream=None):
-    """The whole layer for up to 32 tokens in two launches: choice, gate and up products, SiLU, down product and
-    weighted sum. Scales None for bf16 weights; topk_idx and topk_w may be None."""
+    """The whole layer for up to 32 tokens in three or four launches: choice, gate and up products, SiLU, down product
+    and weighted sum. Scales None for bf16 weights; topk_idx and topk_w may be None."""
     rc = lib().moe_layer_few(C.byref(p), C.byref(gate), C.byref(mlp), _ptr(x), _ptr(logits), _ptr(bias), _ptr(w_up),
                              _ptr(up_scale), _ptr(w_down), _ptr(down_scale), _ptr(topk_idx), _ptr(topk_w), _ptr(out),
                              _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
@@ -602,7 +602,8 @@ def run_few_block(p: moe_problem, gate: moe_gate, mlp: moe_mlp, norm: moe_norm, 
                   down_scale, residual, w_post, w_pre, branch_gate, bufs: dict, out, r, n, stream=None):
     """A block of a decode step, for up to 32 tokens: moe_layer_few of x, this block's normed input, into out, then
     moe_block_norm of it with the residual stream into r and n, the next block's input. bufs: a dict of the caller's (empty
-    at first) that keeps the layer's workspace, which grows with the problem that needs more."""
+    at first) that keeps the layer's workspace, which grows with the problem that needs more; calls that may run at
+    once have a dict each, and one whose calls were captured in a graph is not given a larger problem while the graph lives."""
     stream = _stream(stream)
     need = moe_layer_few_workspace_bytes(p, mlp)
     if need == 0:
