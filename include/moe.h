@@ -528,7 +528,9 @@ size_t moe_block_norm_backward_workspace_bytes(const moe_problem *p, const moe_n
  * of the sums depends on the sizes alone. An empty batch writes zeros for the
  * sums over tokens. Bounds and alignment are those of moe_block_norm; d_w_post,
  * d_w_pre and d_gate 4-byte, workspace 16-byte aligned and not shared with a
- * concurrent call. Waits on the kernel's own copies are bounded (moe_device_status). */
+ * concurrent call. max_blocks caps the grid of the rows' kernel; the columns' sums
+ * take two blocks for each 128 channels. Waits on the kernel's own copies are
+ * bounded (moe_device_status). Launched as programmatic dependents. */
 int moe_block_norm_backward(const moe_problem *p, const moe_norm *norm, const void *y, const void *r,
                             const void *d_r, const void *d_n, const void *w_post, const void *w_pre,
                             const void *gate, void *d_y, void *d_residual, float *d_w_post, float *d_w_pre,
