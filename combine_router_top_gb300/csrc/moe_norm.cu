@@ -13,15 +13,17 @@
 //   d_y = (w_post c - y^ mean(y^ w_post c)) / s_y,  c = a g D
 //   d_w_pre = sum_t d_n r^    d_w_post = sum_t c y^    d_gate = a sum D b  (over t, or over h)
 // Both norms' statistics come from the row itself again, which is in shared memory: the forward
-// pass keeps nothing but y and r.
+// pass keeps nothing but y and r. The second mean, over D, is taken from sums of its parts,
+//   sum y w_post g D = sum y w_post g d_r + 1/s_r (sum y w_post g w_pre d_n - 1/s_r mean sum y w_post g r),
+// so that one sum over the block makes all of a row's means.
 //
 // All of it is bound by HBM where there are many rows, and by a launch and two sums over a block
 // where there are few. One call a row's block, us on GB300 (floor: bytes at the measured copy rate):
 //   norm, 1 x 7168                           5.2  (launch, load, two sums, store)
 //   norm, 16384 x 7168, bf16               159    (floor 140; a copy and two sums a row)
 //   combine and norm, 1024 x 7168, top-8    34.8  (floor 24)
-//   gradient, 4096 x 7168, channel gate     85    (floor 53)
-//   gradient, 16381 x 4096                 149    (floor 120)
+//   gradient, 4096 x 7168, channel gate     73    (floor 53)
+//   gradient, 16381 x 4096                 140    (floor 120)
 #include <math.h>
 
 #include <algorithm>
@@ -153,34 +155,41 @@ __device__ __forceinline__ void block_sum(BlockSum<N> &s, float (&v)[N], unsigne
     }
 }
 
-// Sums of four values over the block: over the warp by halves, two values to a lane after one exchange, one after two,
-// which takes 6 shuffles instead of 20; then over the warps, a lane to a value of a warp.
-struct BlockSum4 {
-    float part[2][32][4];
+// Sums of eight values over the block: over the warp by halves, four values to a lane after one exchange, two after the
+// next, one after three, which takes 9 shuffles instead of 40; then over the warps, a lane to a value of a warp.
+struct BlockSum8 {
+    float part[2][32][8];
 };
-__device__ __forceinline__ void block_sum4(BlockSum4 &s, float (&v)[4], unsigned &turn) {
+__device__ __forceinline__ void block_sum8(BlockSum8 &s, float (&v)[8], unsigned &turn) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const bool odd = lane & 1, upper = lane & 2;
-    // lanes with bit 1 go on with values 2 and 3, the others with 0 and 1; then bit 0 chooses between two
-    float a0 = upper ? v[2] : v[0], a1 = upper ? v[3] : v[1];
-    a0 += __shfl_xor_sync(kFull, upper ? v[0] : v[2], 2);
-    a1 += __shfl_xor_sync(kFull, upper ? v[1] : v[3], 2);
-    float x = odd ? a1 : a0;
-    x += __shfl_xor_sync(kFull, odd ? a0 : a1, 1);
+    float a[4], b[2], x;
+    // lanes with bit 2 go on with values 4 to 7, the others with 0 to 3; then bits 1 and 0 choose among those
 #pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
-    if (warps > 1) {
-        const unsigned b = turn & 1u;
-        ++turn;
-        if (lane < 4) s.part[b][warp][lane] = x;
-        __syncthreads();
-        x = 0.0f;
-        for (int i = lane >> 2; i < warps; i += 8) x += s.part[b][i][lane & 3];
-#pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+    for (int i = 0; i < 4; ++i) {
+        a[i] = lane & 4 ? v[4 + i] : v[i];
+        a[i] += __shfl_xor_sync(kFull, lane & 4 ? v[i] : v[4 + i], 4);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(kFull, x, i);
+    for (int i = 0; i < 2; ++i) {
+        b[i] = lane & 2 ? a[2 + i] : a[i];
+        b[i] += __shfl_xor_sync(kFull, lane & 2 ? a[i] : a[2 + i], 2);
+    }
+    x = lane & 1 ? b[1] : b[0];
+    x += __shfl_xor_sync(kFull, lane & 1 ? b[0] : b[1], 1);
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+    if (warps > 1) {
+        const unsigned at = turn & 1u;
+        ++turn;
+        if (lane < 8) s.part[at][warp][lane] = x;
+        __syncthreads();
+        x = 0.0f;
+        for (int i = lane >> 3; i < warps; i += 4) x += s.part[at][i][lane & 7];
+#pragma unroll
+        for (int o = 8; o <= 16; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(kFull, x, i);
 }
 
 __device__ __forceinline__ float inv_rms(float sum_sq, const NormArgs &a) {
@@ -807,16 +816,18 @@ struct NormBwdPtrs {
 // A block takes the rows of one part (rows p, p + parts, ...) at a time and keeps that part's column
 // sums in registers: NC chunks of 8 columns to a thread. The rows of y, r, d_r and d_n come by
 // bulk copies into a ring, `depth` rows deep, so that loads run on while a row's two sums meet; they are
-// read there again for each of the three passes over a row, which leaves registers for the column sums.
-// Bound by the chain of a row's three passes and two sums, one row of 7168 to an SM at a time: 3.1 us a row,
-// of which its bytes need 1.9.
-template <bool RES32, bool PAR32, int NC, int MAXT>
+// read there again for the second of the two passes over a row, which leaves registers for the column sums. One sum over the
+// block a row, of six values: with a second one for the mean over D, and a third pass behind it, 4096 x 7168 takes 85 us, so 73.
+// DOTS: that mean, or a token's gate's gradient, is wanted. (Known when compiled: its six sums would cost the other kernel
+// spills, 16381 x 4096 in 179 us instead of 140.) Bound by the chain of a row's passes, one row of 7168 to an SM at a time:
+// 2.7 us a row, of which its bytes need 1.9.
+template <bool RES32, bool PAR32, int NC, int MAXT, bool DOTS>
 __global__ void __launch_bounds__(MAXT)
 norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
     extern __shared__ __align__(128) char bwd_ring[];
     __shared__ __align__(8) uint64_t full[kNormMaxDepth];
-    __shared__ BlockSum4 sums4;
-    __shared__ BlockSum<1> sums1;
+    __shared__ BlockSum8 sums8;
+    __shared__ BlockSum<2> sums2;
     const int tid = threadIdx.x;
     const unsigned bf_row = (unsigned)a.H8 * 16u, res_row = RES32 ? 2u * bf_row : bf_row;
     const unsigned y_bytes = p.y ? bf_row : 0u, r_bytes = p.w_pre ? res_row : 0u;
@@ -851,21 +862,27 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
     if (tid == 0)
         for (int i = 0; i < depth; ++i) fetch(i);
 
-    // the vectors that every row uses, where registers hold them
-    constexpr bool kHold = !PAR32 && MAXT == 256;
-    Raw8<PAR32> hold[kHold ? 3 : 1][kHold ? NC : 1];
-    if constexpr (kHold) {
+    // w_post and a channel's gate in one: where a thread has one chunk, once for all rows
+    constexpr bool kHold = NC == 1 && MAXT <= 896;
+    const auto post_of = [&](int c, float2 (&f)[4]) {
+        Raw8<PAR32> raw;
+        float2 g[4];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = i * (int)blockDim.x + tid;
-            if (c < a.H8) {
-                if (p.w_pre) load_param8(p.w_pre, c, hold[0][i]);
-                if (p.w_post) load_param8(p.w_post, c, hold[1][i]);
-                if (a.channel) load_param8(p.gate, c, hold[2][i]);
-            }
+        for (int q = 0; q < 4; ++q) f[q] = both(1.0f);
+        if (p.w_post) {
+            load_param8_again(p.w_post, c, raw);
+            to_floats(raw, f);
         }
-    }
-    unsigned turn3 = 0, turn1 = 0, n_row = 0, lost = 0, s = 0, parity = 0;
+        if (a.channel) {
+            load_param8_again(p.gate, c, raw);
+            to_floats(raw, g);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) f[q] = mul2(f[q], g[q]);
+        }
+    };
+    float2 held[4];
+    if (kHold && tid < a.H8) post_of(tid, held);
+    unsigned turn = 0, n_row = 0, lost = 0, s = 0, parity = 0;
     for (int part = blockIdx.x; part < parts; part += gridDim.x) {
         float2 sum_pre[NC][4], sum_post[NC][4];
 #pragma unroll
@@ -885,59 +902,87 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
             const auto r_of = [&](int c, float2 (&f)[4]) {
                 to_floats(*reinterpret_cast<const Raw8<RES32> *>(in + at_r + (size_t)c * sizeof(Raw8<RES32>)), f);
             };
+            const auto dr_of = [&](int c, float2 (&f)[4]) {
+                to_floats(*reinterpret_cast<const Raw8<RES32> *>(in + at_dr + (size_t)c * sizeof(Raw8<RES32>)), f);
+            };
             const auto dn_of = [&](int c, float2 (&f)[4]) {
                 to_floats(*reinterpret_cast<const Raw8<false> *>(in + at_dn + (size_t)c * 16), f);
             };
-            const auto times = [&](const void *w, int which, int i, int c, float2 (&f)[4]) {
-                Raw8<PAR32> raw;
-                float2 wf[4];
-                if constexpr (kHold) raw = hold[which][i];
-                else load_param8_again(w, c, raw);
-                to_floats(raw, wf);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) f[q] = mul2(f[q], wf[q]);
-            };
-            float2 v[NC][4];                         // w_pre d_n, then w_post g D
-            float2 rr = both(0.0f), rn = both(0.0f), yy = both(0.0f);
+            float2 v[NC][4];                         // w_pre d_n
+            float2 rr = both(0.0f), rn = both(0.0f), yy = both(0.0f), yd = both(0.0f), yn = both(0.0f), yr = both(0.0f);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = i * (int)blockDim.x + tid;
                 if (c < a.H8) {
-                    float2 x[4];
-                    if (p.w_post) {
-                        y_of(c, x);
+                    float2 x[4], y[4], w[4];
+                    if constexpr (DOTS) {
+                        y_of(c, y);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) yy = fma2(x[q], x[q], yy);
+                        for (int q = 0; q < 4; ++q) yy = fma2(y[q], y[q], yy);
+                        if constexpr (!kHold) post_of(c, w);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) y[q] = mul2(y[q], kHold ? held[q] : w[q]);
+                        if (dr_bytes) {
+                            dr_of(c, x);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) yd = fma2(y[q], x[q], yd);
+                        }
                     }
                     if (r_bytes) {
+                        Raw8<PAR32> raw;
+                        load_param8_again(p.w_pre, c, raw);
+                        to_floats(raw, w);
                         dn_of(c, v[i]);
-                        times(p.w_pre, 0, i, c, v[i]);
                         r_of(c, x);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
+                            v[i][q] = mul2(v[i][q], w[q]);
                             rr = fma2(x[q], x[q], rr);
                             rn = fma2(x[q], v[i][q], rn);
+                        }
+                        if constexpr (DOTS) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                yn = fma2(y[q], v[i][q], yn);
+                                yr = fma2(y[q], x[q], yr);
+                            }
                         }
                     }
                 }
             }
-            float f[4] = {__fadd_rn(rr.x, rr.y), __fadd_rn(rn.x, rn.y), __fadd_rn(yy.x, yy.y), 0.0f};
-            block_sum4(sums4, f, turn3);
+            float f[DOTS ? 8 : 2];
+            f[0] = __fadd_rn(rr.x, rr.y);
+            f[1] = __fadd_rn(rn.x, rn.y);
+            if constexpr (DOTS) {
+                f[2] = __fadd_rn(yy.x, yy.y);
+                f[3] = __fadd_rn(yd.x, yd.y);
+                f[4] = __fadd_rn(yn.x, yn.y);
+                f[5] = __fadd_rn(yr.x, yr.y);
+                f[6] = f[7] = 0.0f;
+                block_sum8(sums8, f, turn);
+            } else {
+                block_sum(sums2, f, turn, (int)blockDim.x);
+            }
             if (blockDim.x == 32) __syncwarp();
             // all are done with the row before this one
             if (tid == 0 && n_row > 0 && depth > 1) fetch(s == 0 ? depth - 1 : s - 1);
 
-            const float rs = inv_rms(f[0], a), ys = p.w_post ? inv_rms(f[2], a) : 1.0f;
+            const float rs = inv_rms(f[0], a), ys = DOTS && p.w_post ? inv_rms(f[DOTS ? 2 : 0], a) : 1.0f;
             const float mean = __fmul_rn(__fmul_rn(f[1], rs), a.inv_h);         // of r^ w_pre d_n
             const float g = a.token ? __ldg(static_cast<const float *>(p.gate) + t) : 1.0f, gy = __fmul_rn(g, ys);
-            float2 dot = both(0.0f);
+            // the sum of y w_post D from its parts' sums: D = d_r + rs (w_pre d_n - r rs mean)
+            float e = 0.0f;
+            if constexpr (DOTS) e = __fmaf_rn(rs, __fmaf_rn(-__fmul_rn(rs, mean), f[5], f[4]), f[3]);
+            if (DOTS && p.d_gate_token && tid == 0) p.d_gate_token[t] = __fmul_rn(__fmul_rn(a.scale, ys), e);
+            const float m = __fmul_rn(__fmul_rn(e, ys), a.inv_h);               // of y^ w_post D
+            const float by_y = __fmul_rn(__fmul_rn(a.scale, g), ys), less = DOTS && p.w_post ? __fmul_rn(ys, m) : 0.0f;
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = i * (int)blockDim.x + tid;
                 if (c < a.H8) {
-                    float2 D[4], x[4];
+                    float2 D[4], x[4], w[4];
                     if (dr_bytes)
-                        to_floats(*reinterpret_cast<const Raw8<RES32> *>(in + at_dr + (size_t)c * sizeof(Raw8<RES32>)), D);
+                        dr_of(c, D);
                     else
 #pragma unroll
                         for (int q = 0; q < 4; ++q) D[q] = both(0.0f);
@@ -955,33 +1000,13 @@ norm_backward_kernel(NormArgs a, NormBwdPtrs p, int parts, int depth) {
                     store8<RES32>(static_cast<char *>(p.d_residual) + (size_t)t * res_row, c, D);
                     if (y_bytes) {
                         y_of(c, x);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) sum_post[i][q] = fma2(D[q], mul2(x[q], both(gy)), sum_post[i][q]);
-                        if (a.channel) times(p.gate, 2, i, c, D);
-                        if (p.w_post) times(p.w_post, 1, i, c, D);
+                        if constexpr (!kHold) post_of(c, w);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            v[i][q] = D[q];
-                            dot = fma2(D[q], x[q], dot);
+                            sum_post[i][q] = fma2(D[q], mul2(x[q], both(gy)), sum_post[i][q]);
+                            D[q] = mul2(D[q], kHold ? held[q] : w[q]);
+                            x[q] = mul2(DOTS ? fma2(x[q], both(-less), D[q]) : D[q], both(by_y));
                         }
-                    }
-                }
-            }
-            if (y_bytes) {
-                float e[1] = {__fadd_rn(dot.x, dot.y)};
-                if (p.w_post || p.d_gate_token) block_sum(sums1, e, turn1, (int)blockDim.x);
-                const float by = __fmul_rn(a.scale, g);
-                if (p.d_gate_token && tid == 0) p.d_gate_token[t] = __fmul_rn(__fmul_rn(a.scale, ys), e[0]);
-                const float m = __fmul_rn(__fmul_rn(e[0], ys), a.inv_h);        // of y^ w_post D
-                const float by_y = __fmul_rn(by, ys), less = p.w_post ? __fmul_rn(ys, m) : 0.0f;
-#pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    const int c = i * (int)blockDim.x + tid;
-                    if (c < a.H8) {
-                        float2 x[4];
-                        y_of(c, x);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) x[q] = mul2(fma2(x[q], both(-less), v[i][q]), both(by_y));
                         store8<false>(static_cast<char *>(p.d_y) + (size_t)t * bf_row, c, x);
                     }
                 }
@@ -1081,10 +1106,10 @@ int launch_columns(const Dims &d, const NormArgs &a, cudaStream_t st, const floa
                : MOE_ERR_CUDA;
 }
 
-template <bool RES32, bool PAR32, int NC, int MAXT>
+template <bool RES32, bool PAR32, int NC, int MAXT, bool DOTS>
 int launch_backward_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const NormBwdPtrs &p, float *d_w_post,
                        float *d_w_pre, float *d_gate) {
-    const auto kernel = norm_backward_kernel<RES32, PAR32, NC, MAXT>;
+    const auto kernel = norm_backward_kernel<RES32, PAR32, NC, MAXT, DOTS>;
     const int threads = ((a.H8 + NC - 1) / NC + 31) / 32 * 32;
     const int row = d.H * ((p.y ? 2 : 0) + (p.w_pre ? (RES32 ? 6 : 4) : 0) + (p.d_r ? (RES32 ? 4 : 2) : 0));
     const int parts = norm_parts(d.T, d.H);
@@ -1098,15 +1123,16 @@ int launch_backward_nc(const Dims &d, const NormArgs &a, cudaStream_t st, const 
     if (launch_pdl_smem(kernel, grid, threads, smem, st, a, p, parts, depth) != cudaSuccess) return MOE_ERR_CUDA;
     return launch_columns<PAR32>(d, a, st, p.part, parts, p.w_post, p.gate, d_w_post, d_w_pre, d_gate);
 }
-template <bool RES32, bool PAR32, typename... A>
+template <bool RES32, bool PAR32, bool DOTS, typename... A>
 int launch_norm_backward(const Dims &d, const NormArgs &a, A... args) {
-    if (a.H8 <= 256) return launch_backward_nc<RES32, PAR32, 1, 256>(d, a, args...);
+    if (a.H8 <= 256) return launch_backward_nc<RES32, PAR32, 1, 256, DOTS>(d, a, args...);
     // A chunk to a thread, as many warps as there can be, though that leaves no registers for the vectors: they are read again
-    // for each row. us with one chunk a thread and with two and the vectors held: 4096 x 7168, 85 and 95; 16381 x 4096, 149 and
-    // 152; 237 x 2056, 15.0 and 17.1. Up to 896 threads there are more registers for each: 4096 x 7168 within 64 takes 89.
-    if (a.H8 > 512 && a.H8 <= 896) return launch_backward_nc<RES32, PAR32, 1, 896>(d, a, args...);
-    if (a.H8 <= 1024) return launch_backward_nc<RES32, PAR32, 1, 1024>(d, a, args...);
-    return launch_backward_nc<RES32, PAR32, 4, 512>(d, a, args...);
+    // for each row. us with one chunk a thread and with two and the vectors held, both with two sums a row: 4096 x 7168, 85 and
+    // 95; 16381 x 4096, 149 and 152; 237 x 2056, 15.0 and 17.1. Up to 896 threads there are more registers for each: 4096 x 7168
+    // within 64 took 89.
+    if (a.H8 > 512 && a.H8 <= 896) return launch_backward_nc<RES32, PAR32, 1, 896, DOTS>(d, a, args...);
+    if (a.H8 <= 1024) return launch_backward_nc<RES32, PAR32, 1, 1024, DOTS>(d, a, args...);
+    return launch_backward_nc<RES32, PAR32, 4, 512, DOTS>(d, a, args...);
 }
 
 }  // namespace
@@ -1195,6 +1221,8 @@ extern "C" int moe_block_norm_backward(const moe_problem *p, const moe_norm *nor
     cudaStream_t st = as_stream(stream);
     if (a.token) d_gate = nullptr;                                     // a token's comes from its row
     return by_types(norm, [&](auto res, auto par) {
-        return launch_norm_backward<decltype(res)::value, decltype(par)::value>(d, a, st, b, d_w_post, d_w_pre, d_gate);
+        constexpr bool kRes = decltype(res)::value, kPar = decltype(par)::value;
+        if (y && (w_post || b.d_gate_token)) return launch_norm_backward<kRes, kPar, true>(d, a, st, b, d_w_post, d_w_pre, d_gate);
+        return launch_norm_backward<kRes, kPar, false>(d, a, st, b, d_w_post, d_w_pre, d_gate);
     });
 }
