@@ -815,7 +815,7 @@ struct NormBwdPtrs {
 
 // A block takes the rows of one part (rows p, p + parts, ...) at a time and keeps that part's column
 // sums in registers: NC chunks of 8 columns to a thread. The rows of y, r, d_r and d_n come by
-// bulk copies into a ring, `depth` rows deep, so that loads run on while a row's two sums meet; they are
+// bulk copies into a ring, `depth` rows deep, so that loads run on while a row's sums meet; they are
 // read there again for the second of the two passes over a row, which leaves registers for the column sums. One sum over the
 // block a row, of six values: with a second one for the mean over D, and a third pass behind it, 4096 x 7168 takes 85 us, so 73.
 // DOTS: that mean, or a token's gate's gradient, is wanted. (Known when compiled: its six sums would cost the other kernel

@@ -85,3 +85,16 @@ def test_two_calls_at_once(M):
     for o in made:
         assert torch.equal(o["r"], r) and torch.equal(o["n"], n)
         assert all(torch.equal(o[name], want[name]) for name in ("d_y", "d_residual", "d_w_post", "d_w_pre", "d_gate"))
+
+
+@pytest.mark.parametrize("T,H", [(5, 264), (9, 4104), (6, 7168), (3, 12296)])
+@pytest.mark.parametrize("kind", ["none", "channel", "token"])
+def test_a_gradient_along_the_row(M, T, H, kind):
+    """w_pre d_n along r, up to its rounding: the norm's gradient cancels, and with it the mean over D, which the kernel takes
+    from sums of D's parts."""
+    s = make(M, T, H, kind, "f32", "bf16")
+    r, _ = forward(M, s)
+    s["d_n"] = (r / s["w_pre"].float()).to(torch.bfloat16)
+    check_backward(s, r, backward(M, s, r, with_dr=False), with_dr=False)
+    s["d_r"] *= 2.0 ** -12
+    check_backward(s, r, backward(M, s, r))
