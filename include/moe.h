@@ -526,7 +526,9 @@ size_t moe_block_norm_backward_workspace_bytes(const moe_problem *p, const moe_n
  * d_y are then NULL. d_w_post, d_w_pre and d_gate may be NULL where they are not
  * wanted. d_residual may be d_r itself; no other outputs overlap inputs. The order
  * of the sums depends on the sizes alone. An empty batch writes zeros for the
- * sums over tokens. Bounds and alignment are those of moe_block_norm; d_w_post,
+ * sums over tokens. Bounds and alignment are those of moe_block_norm; a row's dot
+ * products of y w_post g with d_r, r and w_pre d_n have to stay within fp32 as its
+ * sums of squares do (they make the mean in d_y); d_w_post,
  * d_w_pre and d_gate 4-byte, workspace 16-byte aligned and not shared with a
  * concurrent call. max_blocks caps the grid of the rows' kernel; the columns' sums
  * take two blocks for each 128 channels. Waits on the kernel's own copies are
