@@ -560,7 +560,8 @@ typedef struct moe_mlp {
 size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
 
 /* A whole mixture-of-experts layer for up to 32 tokens, in three launches (bf16
- * weights) or four: the choice as moe_route_gated makes it, then for every pair (t, j), e = topk_idx[t][j],
+ * weights) or four: the choice as moe_route_gated makes it, then for every pair (t, j),
+ * e = topk_idx[t][j],
  *   u = x[t] Wup_e^T (2I values: the gate's I, then the up's)
  *   h[i] = round(silu(u[i]) u[I + i]),   silu(v) = v / (1 + exp(-v))
  *   out[t] = bf16(sum_j topk_w[t][j] h Wdown_e^T)
@@ -568,8 +569,10 @@ size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
  * sums fp32; h is rounded to the products' operand type, which is bf16, or with e4m3 and
  * 4-bit weights fp16 behind a power of two for each row (x too: its values below 2^-25 of
  * their row's largest then lose bits, 2^-36 of that largest at most, and an infinity or
- * NaN makes its token's out NaN or infinite); out once. There
- * is no capacity: no pair is dropped, and choices that are no pair take no part (a
+ * NaN makes its token's out NaN or infinite); out once. A 4-bit code q enters its
+ * group's fp32 sum as 1024 + q, taken off again: that sum's rounding is relative to
+ * 1040 |x| for each input, 2^-24 of that at a time (2^-14 of |x| times the scale),
+ * whatever the codes are. There is no capacity: no pair is dropped, and choices that are no pair take no part (a
  * token without pairs and without a shared expert has out 0). Each chosen expert's weights
  * are read once, the others' not at all.
  * x bf16 [T][H] (p's dispatch_dtype must be MOE_DTYPE_BF16); logits [T][E] of the
