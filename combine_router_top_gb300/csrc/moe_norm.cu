@@ -155,6 +155,37 @@ __device__ __forceinline__ void block_sum(BlockSum<N> &s, float (&v)[N], unsigne
     }
 }
 
+// The sum over the block where a thread holds two chunks of a row, `threads` apart (a: from the first, b: from the second),
+// in the order that block_sum has with one chunk to a thread: 32 neighbouring chunks by a butterfly, a half of the lanes for
+// each of a warp's two, then those sums. A row's sum is then the same in the kernel that has one chunk to a thread, so that
+// the number of rows, by which the kernel is chosen, leaves a row's results as they are. 2 to 16 warps.
+__device__ __forceinline__ float block_sum_pairs(BlockSum<1> &s, float a, float b, unsigned &turn, int threads) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = threads >> 5;
+    float x = lane & 16 ? b : a;
+    x += __shfl_xor_sync(kFull, lane & 16 ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+    const unsigned at = turn & 1u;
+    ++turn;
+    if ((lane & 15) == 0) s.part[at][0][(lane >> 4) * warps + warp] = x;
+    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+    x = lane < 2 * warps ? s.part[at][0][lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+    return x;
+}
+// A row's sum of squares from a thread's: PAIRS, of each of its two chunks.
+template <bool PAIRS>
+__device__ __forceinline__ float row_sum(BlockSum<1> &s, const float2 (&sq)[PAIRS ? 2 : 1], unsigned &turn, int threads) {
+    if constexpr (PAIRS) {
+        return block_sum_pairs(s, __fadd_rn(sq[0].x, sq[0].y), __fadd_rn(sq[1].x, sq[1].y), turn, threads);
+    } else {
+        float f[1] = {__fadd_rn(sq[0].x, sq[0].y)};
+        block_sum(s, f, turn, threads);
+        return f[0];
+    }
+}
+
 // Sums of eight values over the block: over the warp by halves, four values to a lane after one exchange, two after the
 // next, one after three, which takes 9 shuffles instead of 40; then over the warps, a lane to a value of a warp.
 struct BlockSum8 {
@@ -197,8 +228,9 @@ __device__ __forceinline__ float inv_rms(float sum_sq, const NormArgs &a) {
 }
 
 // From the block's output v, of which a thread has NC chunks of 8 elements in registers, and the residual to r and n. g: the
-// scale and a token's gate. param(k, c): chunk c of w_post (k = 0), of the gate for each channel (1) or of w_pre (2).
-template <bool HAS_Y, bool RES32, int NC, typename Param>
+// scale and a token's gate. param(k, c): chunk c of w_post (k = 0), of the gate for each channel (1) or of w_pre (2). PAIRS:
+// the sums in the order of one chunk to a thread.
+template <bool HAS_Y, bool RES32, int NC, bool PAIRS, typename Param>
 __device__ __forceinline__ void finish_row(const NormArgs &a, int t, float g, float2 (&v)[NC][4], const Raw8<RES32> (&res)[NC],
                                            bool w_post, bool w_pre, Param param, void *r_out, void *n_out, BlockSum<1> &sums,
                                            unsigned &turn, int threads) {
@@ -209,19 +241,22 @@ __device__ __forceinline__ void finish_row(const NormArgs &a, int t, float g, fl
 #pragma unroll
         for (int q = 0; q < 4; ++q) f[q] = mul2(f[q], p[q]);
     };
-    float f[1];
-    float2 sq = both(0.0f);
+    constexpr int kSums = PAIRS ? 2 : 1;
+    float2 sq[kSums];
+    const auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) sq[i] = both(0.0f);
+    };
+    clear();
     if (HAS_Y && w_post) {
 #pragma unroll
         for (int i = 0; i < NC; ++i)
             if (i * threads + (int)threadIdx.x < a.H8)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) sq = fma2(v[i][q], v[i][q], sq);
-        f[0] = __fadd_rn(sq.x, sq.y);
-        block_sum(sums, f, turn, threads);
-        g = __fmul_rn(g, inv_rms(f[0], a));
+                for (int q = 0; q < 4; ++q) sq[i % kSums] = fma2(v[i][q], v[i][q], sq[i % kSums]);
+        g = __fmul_rn(g, inv_rms(row_sum<PAIRS>(sums, sq, turn, threads), a));
     }
-    sq = both(0.0f);
+    clear();
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = i * threads + (int)threadIdx.x;
@@ -237,15 +272,13 @@ __device__ __forceinline__ void finish_row(const NormArgs &a, int t, float g, fl
             if (r_out) store8<RES32>(static_cast<char *>(r_out) + t * res_row, c, x);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                sq = fma2(x[q], x[q], sq);
+                sq[i % kSums] = fma2(x[q], x[q], sq[i % kSums]);
                 v[i][q] = x[q];
             }
         }
     }
     if (!w_pre) return;
-    f[0] = __fadd_rn(sq.x, sq.y);
-    block_sum(sums, f, turn, threads);
-    const float s = inv_rms(f[0], a);
+    const float s = inv_rms(row_sum<PAIRS>(sums, sq, turn, threads), a);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = i * threads + (int)threadIdx.x;
@@ -307,7 +340,7 @@ norm_kernel(NormArgs a, const void *__restrict__ y, const void *residual, const 
                 return raw;
             }
         };
-        finish_row<HAS_Y, RES32, NC>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, (int)blockDim.x);
+        finish_row<HAS_Y, RES32, NC, false>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, (int)blockDim.x);
     }
 }
 
@@ -411,7 +444,7 @@ combine_norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__res
             load_param8_again(k == 0 ? w_post : k == 1 ? gate : w_pre, ch, raw);
             return raw;
         };
-        finish_row<true, RES32, NC>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, (int)blockDim.x);
+        finish_row<true, RES32, NC, false>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, (int)blockDim.x);
         if ((!w_post && !w_pre) || blockDim.x == 32) __syncthreads();  // the choices' buffers turn behind a barrier
     }
 }
@@ -533,7 +566,7 @@ combine_norm_rows_kernel(NormArgs a, const void *__restrict__ y, const int32_t *
             load_param8_again(k == 0 ? w_post : k == 1 ? gate : w_pre, ch, raw);
             return raw;
         };
-        finish_row<true, RES32, NC>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, threads);
+        finish_row<true, RES32, NC, NC == 2>(a, t, g, v, res, w_post != nullptr, w_pre != nullptr, param, r_out, n_out, sums, turn, threads);
     }
 }
 
@@ -548,6 +581,7 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
     extern __shared__ __align__(128) char norm_ring[];
     __shared__ __align__(8) uint64_t full[kNormMaxDepth];
     __shared__ BlockSum<1> sums;
+    constexpr int kSums = NC == 2 ? 2 : 1;
     const int tid = threadIdx.x;
     const unsigned bf_row = (unsigned)a.H8 * 16u, res_row = RES32 ? 2u * bf_row : bf_row, stage = bf_row + res_row;
     if (tid < depth) {
@@ -579,8 +613,9 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
         const char *in = norm_ring + (size_t)s * stage;
         Raw8<false> yy[NC];
         Raw8<RES32> res[NC];
-        float f[1];
-        float2 sq = both(0.0f);
+        float2 sq[kSums];
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) sq[i] = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = i * (int)blockDim.x + tid;
@@ -590,15 +625,13 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
                 float2 v[4];
                 to_floats(yy[i], v);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) sq = fma2(v[q], v[q], sq);
+                for (int q = 0; q < 4; ++q) sq[i % kSums] = fma2(v[q], v[q], sq[i % kSums]);
             }
         }
         float g = a.scale;
         if (a.token) g = __fmul_rn(g, __ldg(static_cast<const float *>(gate) + t));
         if (w_post) {
-            f[0] = __fadd_rn(sq.x, sq.y);
-            block_sum(sums, f, turn, (int)blockDim.x);
-            g = __fmul_rn(g, inv_rms(f[0], a));
+            g = __fmul_rn(g, inv_rms(row_sum<NC == 2>(sums, sq, turn, (int)blockDim.x), a));
         } else {
             __syncthreads();
         }
@@ -609,7 +642,8 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
             parity ^= 1u;
         }
         float2 v[NC][4];
-        sq = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) sq[i] = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = i * (int)blockDim.x + tid;
@@ -636,15 +670,13 @@ norm_rows_kernel(NormArgs a, const void *y, const void *residual, const void *__
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     v[i][q] = fma2(v[i][q], both(g), x[q]);
-                    sq = fma2(v[i][q], v[i][q], sq);
+                    sq[i % kSums] = fma2(v[i][q], v[i][q], sq[i % kSums]);
                 }
                 if (r_out) store8<RES32>(static_cast<char *>(r_out) + (size_t)t * res_row, c, v[i]);
             }
         }
         if (w_pre) {
-            f[0] = __fadd_rn(sq.x, sq.y);
-            block_sum(sums, f, turn, (int)blockDim.x);
-            const float by = inv_rms(f[0], a);
+            const float by = inv_rms(row_sum<NC == 2>(sums, sq, turn, (int)blockDim.x), a);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int c = i * (int)blockDim.x + tid;

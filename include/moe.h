@@ -491,7 +491,8 @@ typedef struct moe_norm {
  * MOE_ERR_UNSUPPORTED). Rows whose sum of squares passes fp32 (entries from
  * about 2^60 on) are outside the norm's range. Row buffers, weights and a
  * channel gate 16-byte aligned, a token gate 4-byte. A row's results depend on
- * its own values alone; max_blocks caps the grid and changes none. Waits on the
+ * its own values alone: neither the other rows, nor how many there are, nor
+ * max_blocks (which caps the grid) changes them. Waits on the
  * kernel's own copies are bounded (moe_device_status). Launched as a programmatic
  * dependent of the previous kernel. */
 int moe_block_norm(const moe_problem *p, const moe_norm *norm, const void *y, const void *residual,
