@@ -18,9 +18,10 @@
 //   - weights of 8 and 4 bits are made fp16 operands, which costs least: an e4m3 pair one conversion (a bf16
 //     pair takes five instructions), a 4-bit pair one logic operation, which leaves 1024 + q, or 1024 + 16 q where
 //     the code stands 4 bits higher. The inputs of such weights are fp16 too, each row behind a power of two that
-//     brings its largest value to 2^14 .. 2^15: a bf16 x keeps all its bits there but for values below 2^-25 of
-//     the row's largest, which keep an error of 2^-36 of it; h, kept in fp32 meanwhile, is rounded to its 11 bits.
-//     4-bit weights: inputs whose code stands higher are divided by 16, and what 1024 (or 64) and the codes' middle,
+//     brings its largest value to 2^14 .. 2^15 and is 2^112 at most: half of fp16's lowest step, 2^-25, is then 2^-39 of the
+//     largest value, or 2^-137 where that is below 2^-98. h, kept in fp32 meanwhile, is rounded to fp16's 11 bits.
+//     4-bit weights: inputs whose code stands higher are divided by 16 (their error is 2^-35 of the largest, or 2^-133), and
+//     what 1024 (or 64) and the codes' middle,
 //     8, add to a group's sum is taken off it in fp32: sum x (1024 + q) - 1032 sum x.
 //
 // us on GB300, with the floor of the chosen experts' bytes at the measured copy rate:
@@ -171,7 +172,8 @@ __device__ __forceinline__ void row_to_half(const T *row, int n, int group, cons
     if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
     __syncthreads();
     for (int i = 0; i < (int)blockDim.x >> 5; ++i) m = fmaxf(m, most[i]);
-    // the power of two from the exponent's bits; a row with infinities stays as it is
+    // the power of two from the exponent's bits; a row with infinities stays as it is. 2^112 at most: a tiny row's sums with large
+    // weights stay within fp32, and its scale times a routing weight down to 2^-14 within fp32's normal numbers
     const int e = (int)(__float_as_uint(m) >> 23) - 127;
     const int s = m == 0.0f || e == 128 ? 0 : max(e - 14, -112);
     const float by = __uint_as_float((uint32_t)(127 - s) << 23);

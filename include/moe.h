@@ -568,9 +568,13 @@ size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
  *   out[t] = bf16(sum_j topk_w[t][j] h Wdown_e^T)
  * with the shared expert's term of weight 1 behind the pairs'. Products are exact,
  * sums fp32; h is rounded to the products' operand type, which is bf16, or with e4m3 and
- * 4-bit weights fp16 behind a power of two for each row (x too: its values below 2^-25 of
- * their row's largest then lose bits, 2^-36 of that largest at most, and an infinity or
- * NaN makes its token's out NaN or infinite); out once. A 4-bit code q enters its
+ * 4-bit weights fp16 behind a power of two for each row, x too; out once. Such a power
+ * brings the row's largest value to 2^14 .. 2^15, and is 2^112 at most: with e4m3 weights
+ * values of x below 2^-31 of their row's largest lose bits, 2^-39 of that largest at
+ * most (2^-137 where the largest is below 2^-98), and with 4-bit weights, half of whose
+ * inputs are divided by 16, values below 2^-27 of it, 2^-35 of it at most (2^-133); h has
+ * that error besides its rounding to 11 bits. An infinity or NaN in x makes its token's
+ * out NaN or infinite. A 4-bit code q enters its
  * group's fp32 sum as 1024 + q, taken off again: that sum's rounding is relative to
  * 1040 |x| for each input, 2^-24 of that at a time (2^-14 of |x| times the scale),
  * whatever the codes are. There is no capacity: no pair is dropped, and choices that are no pair take no part (a
