@@ -202,21 +202,18 @@ __device__ __forceinline__ void row_to_half(const T *row, int n, int group, cons
     if (threadIdx.x == 0) to.scale[at] = __uint_as_float((uint32_t)(127 + s) << 23);
 }
 
-// h as fp16, a block to a pair. Lets the down kernel start at once.
+// h as fp16, a block to a pair. Lets the down kernel start at once. A choice that is no pair has a row too, whatever the
+// workspace held, which nothing reads: so this kernel needs no list, and reads nothing before its wait.
 __global__ void __launch_bounds__(256)
-few_half_kernel(const FewLists *l, const float *h, int I, int group, FewInputs to) {
+few_half_kernel(const float *h, int I, int group, FewInputs to) {
     pdl_launch_dependents();
-    // the lists are there: the up kernel, which let this one start, waited for them
-    const bool live = (int)blockIdx.x < l->off[l->n];
-    const int pair = l->pair[blockIdx.x];
     pdl_wait();
-    if (!live) return;
-    row_to_half(h + (size_t)pair * I, I, group, to, pair);
+    row_to_half(h + (size_t)blockIdx.x * I, I, group, to, blockIdx.x);
 }
 
 // The choice of all tokens, a warp to a token, and the lists: block 0. With weights of 8 or 4 bits the other blocks, one
-// to a token, make its x fp16. The other kernels' blocks read the lists; the
-// down kernel's may do so before the up kernel has ended, which lets them start only once this one has.
+// to a token, make its x fp16. The up and down kernels' blocks read the lists; the
+// down kernel's may do so before the up kernel has ended, which lets others start only once this one has.
 template <typename T, int V>
 __global__ void __launch_bounds__(V <= 16 ? 1024 : 256)
 few_choice_kernel(const __grid_constant__ FewArgs a, const T *__restrict__ logits, const float *__restrict__ bias,
@@ -463,7 +460,8 @@ few_kernel(const __grid_constant__ CUtensorMap map, FewArgs a, int team, int spl
         pdl_launch_dependents();
         if (kFewHalf<WT> && tid < a.T) token_scale[tid] = in.scale[tid];
     }
-    // the up kernel lets the down kernel start once the choice is made
+    // down: before its wait. The choice's kernel has ended and flushed them by then: the up kernel lets the next one start only
+    // behind its own wait for that, and all loads of them are from L2, so that no earlier call's are found in an L1.
     for (int i = tid; i < (int)(sizeof(FewLists) / 16); i += kFewThreads)
         reinterpret_cast<uint4 *>(&lists)[i] = ld_l2_v4(reinterpret_cast<const uint4 *>(made) + i);
     __syncthreads();
@@ -939,8 +937,8 @@ int launch_few(const Dims &d, const FewArgs &a, cudaStream_t st, const void *x, 
     if (launch_pdl_smem(few_kernel<WT, false, NTM>, few_grid(units, d.max_blocks), kFewThreads, kFewRing, st, up, a, few_team(units), 0,
                         s.lists, up_x, up_scale, s.h, o, s.parts, status) != cudaSuccess)
         return MOE_ERR_CUDA;
-    if (half && launch_pdl(few_half_kernel, d.T * (d.k + a.shared), 256, st, s.lists, static_cast<const float *>(s.h), a.I, group,
-                           s.h_half) != cudaSuccess)
+    if (half && launch_pdl(few_half_kernel, d.T * (d.k + a.shared), 256, st, static_cast<const float *>(s.h), a.I, group, s.h_half) !=
+                    cudaSuccess)
         return MOE_ERR_CUDA;
     const int split = s.split;
     units = (long long)(d.H / 16) << split;

@@ -185,7 +185,14 @@ inline int lane_tasks(int n_tasks) {
 // Launches `kernel` on `st` allowing programmatic dependent launch: the grid
 // may be scheduled while the previous kernel on the stream finishes. Every
 // kernel of this library starts with pdl_wait(), so none touches global memory
-// before its predecessor has completed and flushed.
+// before its predecessor has completed and flushed; only that wait orders
+// memory, not the launch itself. moe_few.cu has the two exceptions. Its kernel
+// for h as fp16 lets the next one start before it waits, and touches no memory
+// until then. Its down kernel, before it waits, reads the lists of the choice's
+// kernel and starts copies of weights, which no kernel of a call writes. What that
+// needs: the lists' writer has completed before the kernel between them, the up
+// kernel, lets anything start, as it does so behind its own wait; and the lists
+// are loaded from L2. A kernel put into that row of launches keeps both.
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(Params...), int grid, int block, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
