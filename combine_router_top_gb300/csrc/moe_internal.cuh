@@ -288,6 +288,13 @@ __device__ __forceinline__ void pdl_enter() {
     pdl_wait();
     pdl_launch_dependents();
 }
+// pdl_enter() where a kernel reads what the one before it wrote by loads that the compiler may move (__ldg, __ldcg, asm that
+// is not volatile): the pointers come out of this call anew, so that no load through them is made ahead of the wait.
+template <typename... P>
+__device__ __forceinline__ void pdl_enter_before(P &...pointers) {
+    pdl_enter();
+    (([&] { asm volatile("" : "+l"(pointers) : : "memory"); }()), ...);
+}
 
 // Exclusive scan of min(counts[e], C) over e into off[0..E] (off[E] = kept rows).
 __device__ __forceinline__ void kept_row_offsets(const int32_t *__restrict__ counts, int E, int C, int32_t *off, int32_t *warp_tot) {
@@ -352,10 +359,11 @@ struct UnitWalk {
 };
 
 // 16-byte load through the read-only path, not kept in L1 (each row is read
-// once). Only for data no kernel writes while this one runs.
+// once). Only for data no kernel writes while this one runs. Volatile: it stays
+// behind pdl_wait() and where the program order has it.
 __device__ __forceinline__ uint4 ld_stream_v4(const void *p) {
     uint4 r;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                  : "l"(p));
     return r;
