@@ -549,7 +549,8 @@ def run_path(p: moe_problem, x, logits, s, bufs: dict, out, stream=None, fused=F
 def _w4_workspace(bufs: dict, n: int, device, stream: int, name="w4_workspace"):
     """bufs[name] of at least n bytes for work on the stream with this handle: made once, kept with the
     problem's buffers. Its memory belongs to the stream that it was made for, so that a dropped one is only handed on
-    behind that stream's work; use on another stream is recorded with the allocator."""
+    behind that stream's work; use on another stream is recorded with the allocator. One that a graph was captured with
+    is kept beside it, in bufs[name + "_captured"], when a later call needs more: the graph writes to it at every replay."""
     import torch
 
     def torch_stream():                                  # ExternalStream takes no default stream
@@ -561,6 +562,22 @@ def _w4_workspace(bufs: dict, n: int, device, stream: int, name="w4_workspace"):
         bufs[name + "_stream"] = stream
     elif bufs.get(name + "_stream") != stream:
         ws.record_stream(torch_stream())
+    if _capturing(stream, torch_stream):
+        held = bufs.setdefault(name + "_captured", [])
+        if not any(t is bufs[name] for t in held):
+            held.append(bufs[name])
+
+
+def _capturing(stream: int, torch_stream) -> bool:
+    """Whether work on the stream with this handle, torch_stream() for torch, goes into a graph. 1 us for the current
+    stream, 11 for another, which has to become the current one for the question."""
+    import torch
+    if not torch.cuda.is_initialized():
+        return False
+    if stream == _stream(None):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(torch_stream()):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def _w4_experts(p, gate, x, logits, bias, gate_up, down, b: dict, h, stream):
@@ -581,7 +598,8 @@ def run_w4_path(p: moe_problem, gate: moe_gate, x, logits, bias, gate_up, down, 
     """moe_route_gated -> moe_dispatch -> experts with 4-bit weights (gate and up through SiLU, then down) ->
     moe_combine for one batch, on one stream. gate_up and down: (w4 shape, w_q, w_scale) of H -> I with
     MOE_ACT_SILU_GATE and of I -> H; bufs as alloc_buffers(p) makes them, to which the path adds the experts' workspace
-    (which grows with the problem that needs more); h bf16 [E][C][I], the MLP's inner rows."""
+    (which grows with the problem that needs more; one that a graph was captured with lives as long as bufs); h bf16
+    [E][C][I], the MLP's inner rows."""
     b, stream = bufs, _stream(stream)
     _w4_experts(p, gate, x, logits, bias, gate_up, down, b, h, stream)
     moe_combine(p, b["y"], b["topk_idx"], b["topk_w"], b["slot"], out, stream)
@@ -603,7 +621,7 @@ def run_few_block(p: moe_problem, gate: moe_gate, mlp: moe_mlp, norm: moe_norm, 
     """A block of a decode step, for up to 32 tokens: moe_layer_few of x, this block's normed input, into out, then
     moe_block_norm of it with the residual stream into r and n, the next block's input. bufs: a dict of the caller's (empty
     at first) that keeps the layer's workspace, which grows with the problem that needs more; calls that may run at
-    once have a dict each, and one whose calls were captured in a graph is not given a larger problem while the graph lives."""
+    once, replayed graphs among them, have a dict each. A graph's workspace lives as long as the dict."""
     stream = _stream(stream)
     need = moe_layer_few_workspace_bytes(p, mlp)
     if need == 0:
@@ -625,7 +643,8 @@ def run_gate_backward(p: moe_problem, gate: moe_gate, logits, d_out, bufs: dict,
 def run_block_backward(p: moe_problem, gate: moe_gate, norm: moe_norm, logits, out, r, d_r, d_n, w_post, w_pre, branch_gate,
                        bufs: dict, d_out, d_residual, d_w_post, d_w_pre, d_branch_gate, d_y, d_topk_w, d_logits, stream=None):
     """The way back through run_w4_block's join, combine and router: moe_block_norm_backward from the forward pass's out and
-    r, then run_gate_backward of d_out, on the buffers that the forward pass left. Weights' gradients may be None."""
+    r, then run_gate_backward of d_out, on the buffers that the forward pass left, to which it adds the norms' workspace as
+    run_w4_path does the experts'. Weights' gradients may be None."""
     stream = _stream(stream)
     _w4_workspace(bufs, moe_block_norm_backward_workspace_bytes(p, norm), d_out.device, stream, "norm_workspace")
     moe_block_norm_backward(p, norm, out, r, d_r, d_n, w_post, w_pre, branch_gate, d_out, d_residual, d_w_post, d_w_pre,
