@@ -624,8 +624,8 @@ def run_few_block(p: moe_problem, gate: moe_gate, mlp: moe_mlp, norm: moe_norm, 
     once, replayed graphs among them, have a dict each. A graph's workspace lives as long as the dict."""
     stream = _stream(stream)
     need = moe_layer_few_workspace_bytes(p, mlp)
-    if need == 0:
-        raise MoeError("moe_layer_few_workspace_bytes", MOE_ERR_INVALID_ARG)
+    if need == 0:                                        # sizes that the layer refuses: with its own reason, nothing launched
+        _check("moe_layer_few", lib().moe_layer_few(C.byref(p), C.byref(gate), C.byref(mlp), *[None] * 11, 0, None))
     _w4_workspace(bufs, need, x.device, stream, "few_workspace")
     moe_layer_few(p, gate, mlp, x, logits, bias, w_up, up_scale, w_down, down_scale, bufs.get("topk_idx"), bufs.get("topk_w"),
                   out, bufs["few_workspace"], stream)
