@@ -21,17 +21,19 @@
 //     brings its largest value to 2^14 .. 2^15 and is 2^112 at most: half of fp16's lowest step, 2^-25, is then 2^-39 of the
 //     largest value, or 2^-137 where that is below 2^-98. h, kept in fp32 meanwhile, is rounded to fp16's 11 bits.
 //     4-bit weights: inputs whose code stands higher are divided by 16 (their error is 2^-35 of the largest, or 2^-133), and
-//     what 1024 (or 64) and the codes' middle,
-//     8, add to a group's sum is taken off it in fp32: sum x (1024 + q) - 1032 sum x.
+//     what 1024 (or 64) and the codes' middle, 8, add to a group's sum is taken off it in fp32: sum x (1024 + q) - 1032 sum x.
 //
 // us on GB300, with the floor of the chosen experts' bytes at the measured copy rate:
-//   1 token, 2 of 8 experts of 14336 x 4096, bf16             108    (floor 105)
-//   1 token, 8 of 256 of 2048 x 7168 and a shared one, 4-bit   60    (30.5)
-//   13 tokens, top-6 of 64 of 1408 x 2048 and shared, e4m3     94    (60.7; 46 experts live and the shared one)
-//   32 tokens, top-8 of 256 of 2048 x 7168, e4m3              797    (664; 101 live)
-// A call of next to no work takes 12.5 us: four launches one behind the other. What the slower ones spend: 4-bit
-// weights are bound by the instructions that make operands and scale their sums; lists of more than 8 rows by those
-// that load the inputs of each 16 of them.
+//   1 token, 2 of 8 experts of 14336 x 4096, bf16             112    (floor 105)
+//   1 token, 8 of 256 of 2048 x 7168 and a shared one, 4-bit   61    (30.5)
+//   13 tokens, top-6 of 64 of 1408 x 2048 and shared, e4m3     97    (62.9; 48 experts live and the shared one)
+//   32 tokens, top-8 of 256 of 2048 x 7168, e4m3              804    (664; 101 live)
+// A call of next to no work (256 experts of 128 x 128) takes 12.5 us with one token, four launches one behind the other;
+// 18.6 with 8 tokens and 25.3 with 32. Each by itself, with 1, 8 and 32: the choice 6.5, 6.6 and 10.9, up 5.5, 5.6 and 6.4,
+// h's fp16 3.4, down 6.2, 12.6 and 14.1, where eight units each go through all lists. What the slower ones
+// spend: 4-bit weights are bound by the instructions that make operands and scale their sums; lists of more than 8 rows by
+// those that load the inputs of each 16 of them; the down kernel of 8- and 4-bit weights by a list's sums at nearly every
+// piece, and by spills (128 registers; in the up kernel of e4m3 weights, for up to 32 tokens, too).
 #include <algorithm>
 #include <type_traits>
 

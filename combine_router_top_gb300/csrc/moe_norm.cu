@@ -18,12 +18,14 @@
 // so that one sum over the block makes all of a row's means.
 //
 // All of it is bound by HBM where there are many rows, and by a launch and two sums over a block
-// where there are few. One call a row's block, us on GB300 (floor: bytes at the measured copy rate):
-//   norm, 1 x 7168                           5.2  (launch, load, two sums, store)
-//   norm, 16384 x 7168, bf16               159    (floor 140; a copy and two sums a row)
+// where there are few. us on GB300, call behind call on inputs in turn (floor: bytes at the measured copy rate):
+//   norm, 1 x 7168                           5.2  (2.9 in a graph; launch, load, two sums, store)
+//   norm, 16384 x 7168, bf16               156    (floor 140; a copy and two sums a row)
 //   combine and norm, 1024 x 7168, top-8    34.8  (floor 24)
-//   gradient, 4096 x 7168, channel gate     73    (floor 53)
-//   gradient, 16381 x 4096                 140    (floor 120)
+//   gradient, 4096 x 7168, channel gate     74    (floor 53)
+//   gradient, 16381 x 4096, no norm after  129    (floor 120)
+// The norm of the stream alone (no y) takes a row straight into registers whatever the number of rows: 16384 x 7168 in 170,
+// with a floor of 70.
 #include <math.h>
 
 #include <algorithm>
@@ -383,7 +385,7 @@ __device__ __forceinline__ void put_choices(const NormArgs &a, const Choice &c, 
 
 // moe_combine_norm: the same behind the weighted sum of SRC experts' rows at a time, a token after the other, whose
 // choices are loaded a token ahead. Few tokens or short rows: all of a token's rows are asked for at once. 237 x 2056,
-// top-6: 6.7 us.
+// top-6: 7.2 us, 4.6 in a graph.
 template <int SRC, bool RES32, bool PAR32, int NC, int MAXT>
 __global__ void __launch_bounds__(MAXT)
 combine_norm_kernel(NormArgs a, const void *__restrict__ y, const int32_t *__restrict__ topk_idx,
@@ -853,9 +855,9 @@ struct NormBwdPtrs {
 // sums in registers: NC chunks of 8 columns to a thread. The rows of y, r, d_r and d_n come by
 // bulk copies into a ring, `depth` rows deep, so that loads run on while a row's sums meet; they are
 // read there again for the second of the two passes over a row, which leaves registers for the column sums. One sum over the
-// block a row, of six values: with a second one for the mean over D, and a third pass behind it, 4096 x 7168 takes 85 us, so 73.
+// block a row, of six values: with a second one for the mean over D, and a third pass behind it, 4096 x 7168 takes 85 us, so 74.
 // DOTS: that mean, or a token's gate's gradient, is wanted. (Known when compiled: its six sums would cost the other kernel
-// spills, 16381 x 4096 in 179 us instead of 140.) Bound by the chain of a row's passes, one row of 7168 to an SM at a time:
+// spills, 16381 x 4096 without a norm after the block in 160 us instead of 129.) Bound by the chain of a row's passes, one row of 7168 to an SM at a time:
 // 2.7 us a row, of which its bytes need 1.9.
 template <bool RES32, bool PAR32, int NC, int MAXT, bool DOTS>
 __global__ void __launch_bounds__(MAXT)

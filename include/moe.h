@@ -579,7 +579,11 @@ size_t moe_layer_few_workspace_bytes(const moe_problem *p, const moe_mlp *mlp);
  * 1040 |x| for each input, 2^-24 of that at a time (2^-14 of |x| times the scale),
  * whatever the codes are. There is no capacity: no pair is dropped, and choices that are no pair take no part (a
  * token without pairs and without a shared expert has out 0). Each chosen expert's weights
- * are read once, the others' not at all.
+ * are read once, the others' not at all. With 4-bit weights and no shared expert the path
+ * of moe_route_gated, moe_dispatch, moe_expert_w4 and moe_combine does the same, with h
+ * and the experts' rows in bf16: on GB300 as fast for one token and faster for more (8 of
+ * 256 experts of 2048 x 7168: 58 us here and 57 there for one token, 331 and 275 for 8,
+ * 950 and 725 for 32).
  * x bf16 [T][H] (p's dispatch_dtype must be MOE_DTYPE_BF16); logits [T][E] of the
  *   gate's type; bias f32 [E] or NULL; topk_idx i32 [T][k] and topk_w f32 [T][k],
  *   as moe_route_gated writes them, or NULL where they are not wanted; out bf16 [T][H].
