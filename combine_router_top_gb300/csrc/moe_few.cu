@@ -20,6 +20,9 @@
 //     the code stands 4 bits higher. The inputs of such weights are fp16 too, each row behind a power of two that
 //     brings its largest value to 2^14 .. 2^15 and is 2^112 at most: half of fp16's lowest step, 2^-25, is then 2^-39 of the
 //     largest value, or 2^-137 where that is below 2^-98. h, kept in fp32 meanwhile, is rounded to fp16's 11 bits.
+//     With bf16 weights h is rounded to bf16, since a product's operands are of one type: the output is then 0.0023 of its
+//     norm off the value in 64 bits, of which its own rounding makes 0.0017. h in two bf16 parts would mend that for a second
+//     product of each; the layer is defined with the one.
 //     4-bit weights: inputs whose code stands higher are divided by 16 (their error is 2^-35 of the largest, or 2^-133), and
 //     what 1024 (or 64) and the codes' middle, 8, add to a group's sum is taken off it in fp32: sum x (1024 + q) - 1032 sum x.
 //
